@@ -19,6 +19,12 @@ from typing import Dict, Optional, Sequence
 
 import numpy as np
 
+from . import lowbit
+from .lowbit import (BCQ_KV_MAX_TOKENS, KVCache, bcq_int_gemm, bcq_int_linear, bcq_int_quantize,
+                     bcq_int_workspace_bytes, bcq_kv_append, bcq_kv_attend, bcq_kv_evict,
+                     bcq_kv_evict_workspace_bytes, bcq_kv_read, bcq_kv_workspace_bytes,
+                     new_int_workspace, new_kv_evict_workspace, new_kv_workspace)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbcq.so")
 
@@ -56,7 +62,7 @@ EXPORTS = (
     "bcq_dequantize",
     "bcq_quantize",
     "bcq_status_string",
-)
+) + lowbit.EXPORTS
 
 
 class BCQError(RuntimeError):
@@ -121,6 +127,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                         vp, ctypes.c_int, vp]),
         "bcq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     }
+    sig.update(lowbit.SIGNATURES)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res

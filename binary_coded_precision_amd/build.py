@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbcq.so")
 SOURCES = ["bcq_api.hip", "pack.hip", "gemv_lut.hip", "gemm_mfma.hip", "lowrank.hip", "dequant.hip",
-           "quantize.hip"]
+           "quantize.hip", "serve_api.hip", "int_gemm.hip", "kv_cache.hip", "kv_attend.hip"]
 # Per-file flags: the quantizer takes its sign decisions on exactly rounded
 # fp64 values, so no multiply-add there is fused into one rounding.
 FILE_FLAGS = {"quantize.hip": ["-ffp-contract=off"]}

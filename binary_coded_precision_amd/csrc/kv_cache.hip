@@ -1,0 +1,451 @@
+// kv_cache.hip -- what fills, reads back and shrinks the 4-bit key/value cache
+// (bcq_kv_append, bcq_kv_read, bcq_kv_evict).
+//
+// A vector of D channels (one token's K or V of one cached head) is
+// zero + scale * code: zero = fp16(min), scale = fp16((max - min) * (1/15)),
+// code = rint((x - zero) / scale) held to 0..15, each step rounded to fp32 (the
+// constant too), so the codes are a function of the inputs alone.
+#include "serve_internal.h"
+
+namespace bcq {
+namespace {
+
+struct __attribute__((aligned(8))) Half4 {
+  _Float16 x[4];
+};
+
+// D/4 lanes hold a vector, 4 consecutive channels each.  Lane i's two bytes of
+// codes are bytes 2i, 2i+1 of a K row; in a block of 4 tokens of V they are one
+// 16-bit unit: row i % 16, channel block i / 16.
+template <int D>
+__device__ __forceinline__ int64_t k_byte(int64_t token, int i) {
+  return token * (D / 2) + i * 2;
+}
+template <int D>
+__device__ __forceinline__ int64_t v_byte(int64_t token, int i) {
+  return (token & ~(int64_t)3) * (D / 2) + (i & 15) * (D / 8) + (i >> 4) * 8 + (token & 3) * 2;
+}
+
+// NaN wins, as a vector holding one cannot be represented.
+__device__ __forceinline__ float nan_min(float a, float b) { return (a < b || a != a) ? a : b; }
+__device__ __forceinline__ float nan_max(float a, float b) { return (a > b || a != a) ? a : b; }
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load4(float (&x)[4], const T *p) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    const Half4 h = *reinterpret_cast<const Half4 *>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (float)h.x[e];
+  } else if constexpr (VEC) {
+    const float4 f = *reinterpret_cast<const float4 *>(p);
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (float)p[e];
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store4(T *p, const float (&x)[4]) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    Half4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h.x[e] = (_Float16)x[e];
+    *reinterpret_cast<Half4 *>(p) = h;
+  } else if constexpr (VEC) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = (T)x[e];
+  }
+}
+
+// Vector `vec` of a call over n tokens: K and V of (sequence, token, head), V last.
+struct Place {
+  int b, i, h, slot;
+  bool v;
+};
+__device__ __forceinline__ Place place(const KvView &c, int n, int64_t vec) {
+  Place p;
+  p.v = vec & 1;
+  vec >>= 1;
+  p.h = (int)(vec % c.H);
+  vec /= c.H;
+  p.i = (int)(vec % n);
+  p.b = (int)(vec / n);
+  p.slot = kv_len(c, p.b) - n + p.i;
+  return p;
+}
+
+// Bound by the bytes of the vectors read; every lane converts what it loads,
+// the extremes meet in D/4 lanes and no shared memory is needed.
+template <int D, typename T, bool VEC>
+__global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k, KvStrides ks,
+                                                     const T *v, KvStrides vs,
+                                                     const int32_t *positions, float *weights,
+                                                     int32_t *pos, int64_t vecs) {
+  constexpr int L = D / 4;
+  const int64_t vec = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int i = threadIdx.x % L;
+  if (vec >= vecs) return;  // whole groups of L lanes leave together
+  const Place p = place(c, n, vec);
+  const KvStrides st = p.v ? vs : ks;
+  const T *src = (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4;
+  float x[4];
+  load4<T, VEC>(x, src);
+  float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
+  float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
+#pragma unroll
+  for (int d = 1; d < L; d <<= 1) {
+    lo = nan_min(lo, __shfl_xor(lo, d));
+    hi = nan_max(hi, __shfl_xor(hi, d));
+  }
+  const _Float16 zh = (_Float16)lo, sh = (_Float16)((hi - lo) * (1.f / 15.f));
+  const float zero = (float)zh, scale = (float)sh;
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float q = scale > 0.f ? rintf((x[e] - zero) / scale) : 0.f;
+    q = fminf(fmaxf(q, 0.f), 15.f);
+    word |= (uint32_t)q << (4 * e);
+  }
+  if (p.slot < 0) return;
+  const int64_t token = kv_token(c, p.b, p.h, p.slot);
+  if (token < 0) return;
+  *reinterpret_cast<uint16_t *>(p.v ? c.v + v_byte<D>(token, i) : c.k + k_byte<D>(token, i)) =
+      (uint16_t)word;
+  if (i == 0) {
+    union {
+      _Float16 h[2];
+      uint32_t u;
+    } m;
+    m.h[0] = sh;
+    m.h[1] = zh;
+    *reinterpret_cast<uint32_t *>(c.scales + token * 4 + (p.v ? 2 : 0)) = m.u;
+    if (!p.v) {
+      const int64_t at = ((int64_t)p.b * c.H + p.h) * c.room() + p.slot;
+      if (weights != nullptr) weights[at] = 0.f;
+      if (pos != nullptr)
+        pos[at] = positions != nullptr ? positions[(int64_t)p.b * n + p.i] : p.slot;
+    }
+  }
+}
+
+template <int D, typename T, bool VEC>
+__global__ __launch_bounds__(256) void read_kernel(KvView c, int n, T *k, KvStrides ks, T *v,
+                                                   KvStrides vs, int64_t vecs) {
+  constexpr int L = D / 4;
+  const int64_t vec = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int i = threadIdx.x % L;
+  if (vec >= vecs) return;
+  const Place p = place(c, n, vec);
+  const KvStrides st = p.v ? vs : ks;
+  T *dst = (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4;
+  const int64_t token = p.slot < 0 ? -1 : kv_token(c, p.b, p.h, p.slot);
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (token >= 0) {
+    const uint32_t word = *reinterpret_cast<const uint16_t *>(
+        p.v ? c.v + v_byte<D>(token, i) : c.k + k_byte<D>(token, i));
+    union {
+      uint32_t u;
+      _Float16 h[2];
+    } m;
+    m.u = *reinterpret_cast<const uint32_t *>(c.scales + token * 4 + (p.v ? 2 : 0));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[e] = (float)m.h[1] + (float)m.h[0] * (float)((word >> (4 * e)) & 15u);
+  }
+  store4<T, VEC>(dst, x);
+}
+
+bool vec_ok(const void *p, KvStrides s, size_t size) {
+  return (uintptr_t)p % (4 * size) == 0 && s.batch % 4 == 0 && s.token % 4 == 0 &&
+         s.head % 4 == 0;
+}
+
+template <int D, typename T>
+hipError_t append_dim(const KvView &c, int n, const void *k, KvStrides ks, const void *v,
+                      KvStrides vs, const int32_t *positions, float *weights, int32_t *pos,
+                      hipStream_t s) {
+  const int64_t vecs = (int64_t)c.B * n * c.H * 2, per = 256 / (D / 4);
+  const unsigned grid = (unsigned)((vecs + per - 1) / per);
+  if (vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T)))
+    append_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, (const T *)k, ks, (const T *)v, vs,
+                                                   positions, weights, pos, vecs);
+  else
+    append_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, (const T *)k, ks, (const T *)v, vs,
+                                                    positions, weights, pos, vecs);
+  return hipGetLastError();
+}
+
+template <int D, typename T>
+hipError_t read_dim(const KvView &c, int n, void *k, KvStrides ks, void *v, KvStrides vs,
+                    hipStream_t s) {
+  const int64_t vecs = (int64_t)c.B * n * c.H * 2, per = 256 / (D / 4);
+  const unsigned grid = (unsigned)((vecs + per - 1) / per);
+  if (vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T)))
+    read_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, (T *)k, ks, (T *)v, vs, vecs);
+  else
+    read_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, (T *)k, ks, (T *)v, vs, vecs);
+  return hipGetLastError();
+}
+
+// ---- eviction
+//
+// Each (sequence, cached head) keeps its own tokens: the `recent` newest by
+// position, then those of the largest accumulated weight, the lower slot first
+// among equals.  Kept tokens already in front stay where they are and the i-th
+// evicted slot in front takes the i-th kept token from behind, so that what
+// moves is the least possible and no move reads what another writes.
+
+// Order of a slot: recent tokens above every weight, NaN below every weight.
+__device__ __forceinline__ uint32_t order_of(float w, bool late) {
+  if (late) return 0xffffffffu;
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);  // -0 counts as 0
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+constexpr int kEvictThreads = 1024, kEvictWaves = kEvictThreads / 64;
+constexpr int kCopies = 16;       // of the histogram, so that lanes rarely meet in a counter
+constexpr int kEvictKeys = 32768;  // slots whose orders shared memory holds
+
+struct EvictArgs {
+  KvView c;
+  int keep, recent;
+  const float *weights;
+  const int32_t *pos;
+  int32_t *lens_out;
+  float *weights_out;
+  int32_t *pos_out;
+  int32_t *count;  // [BH] moves
+  int2 *moves;     // [BH][most]: (from, to)
+  int most;
+};
+
+// One workgroup a row.  A radix select over the orders, eight bits a pass,
+// finds the last one kept; then the waves, each with its own stretch of slots,
+// count and lay out what moves, in slot order.
+template <bool HELD>
+__global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
+  extern __shared__ uint32_t keys[];
+  __shared__ uint32_t hist[256 * kCopies];
+  __shared__ uint32_t total[256];
+  __shared__ int tmp[kEvictWaves], base[3][kEvictWaves + 1];
+  __shared__ uint32_t picked, above;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = blockIdx.x, b = row / a.c.H;
+  const int64_t at = (int64_t)row * a.c.room();
+  const int L = kv_len(a.c, b), m = min(L, a.keep);
+  const float *w = a.weights + at;
+  const int32_t *pos = a.pos + at;
+  if (L <= a.keep) {
+    for (int s = tid; s < L; s += kEvictThreads) {
+      a.weights_out[at + s] = w[s];
+      a.pos_out[at + s] = pos[s];
+    }
+    if (tid == 0) a.count[row] = 0;
+    return;
+  }
+  int newest = INT32_MIN;
+  for (int s = tid; s < L; s += kEvictThreads) newest = max(newest, pos[s]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
+  if (lane == 0) tmp[wave] = newest;
+  __syncthreads();
+  for (int i = 0; i < kEvictWaves; ++i) newest = max(newest, tmp[i]);
+  const int64_t late_from = (int64_t)newest - a.recent;
+  auto key = [&](int s) { return HELD ? keys[s] : order_of(w[s], pos[s] > late_from); };
+  if (HELD)
+    for (int s = tid; s < L; s += kEvictThreads) keys[s] = order_of(w[s], pos[s] > late_from);
+
+  uint32_t prefix = 0;
+  int left = m;  // still to be taken among the slots whose order starts with prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256 * kCopies; i += kEvictThreads) hist[i] = 0;
+    __syncthreads();
+    for (int s = tid; s < L; s += kEvictThreads) {
+      const uint32_t k = key(s);
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
+        atomicAdd(&hist[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+    }
+    __syncthreads();
+    if (tid < 256) {
+      uint32_t t = 0;
+      for (int i = 0; i < kCopies; ++i) t += hist[tid * kCopies + i];
+      total[tid] = t;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      // lane l sums bins 4l..4l+3; the bin where the count from the top passes `left`
+      uint32_t t[4], sum = 0;
+      for (int i = 0; i < 4; ++i) sum += t[i] = total[lane * 4 + i];
+      uint32_t up = sum;  // of this lane's bins and all above
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_down(up, d);
+        if (lane + d < 64) up += o;
+      }
+      uint32_t over = up - sum;
+      for (int i = 3; i >= 0; --i) {
+        if (over < (uint32_t)left && over + t[i] >= (uint32_t)left) {
+          picked = lane * 4 + i;
+          above = over;
+        }
+        over += t[i];
+      }
+    }
+    __syncthreads();
+    prefix |= picked << shift;
+    left -= (int)above;
+    __syncthreads();
+  }
+  // kept: every order above prefix, and the first `left` slots at it
+  const int span = (L + kEvictThreads - 1) / kEvictThreads * 64;  // slots of a wave
+  const int s0 = wave * span, s1 = min(L, s0 + span);
+  int ties = 0;
+  for (int s = s0; s < s1; s += 64)
+    ties += __popcll(__ballot(s + lane < s1 && key(s + lane) == prefix));
+  if (lane == 0) base[0][wave] = ties;
+  __syncthreads();
+  int tie0 = 0;
+  for (int i = 0; i < wave; ++i) tie0 += base[0][i];
+  const uint64_t before = (1ull << lane) - 1;
+  auto walk = [&](auto &&visit) {
+    int tie = tie0;
+    for (int s = s0; s < s1; s += 64) {
+      const bool in = s + lane < s1;
+      const uint32_t k = in ? key(s + lane) : 0;
+      const uint64_t eq = __ballot(in && k == prefix);
+      const bool kept = in && (k > prefix || (k == prefix && tie + __popcll(eq & before) < left));
+      tie += __popcll(eq);
+      const int slot = s + lane;
+      visit(slot, kept, __ballot(in && slot < m && !kept), __ballot(slot >= m && kept));
+    }
+  };
+  int holes = 0, fills = 0;
+  walk([&](int, bool, uint64_t hole, uint64_t fill) {
+    holes += __popcll(hole);
+    fills += __popcll(fill);
+  });
+  if (lane == 0) {
+    base[1][wave] = holes;
+    base[2][wave] = fills;
+  }
+  __syncthreads();
+  int hole_at = 0, fill_at = 0, moves = 0;
+  for (int i = 0; i < kEvictWaves; ++i) {
+    if (i < wave) {
+      hole_at += base[1][i];
+      fill_at += base[2][i];
+    }
+    moves += base[1][i];
+  }
+  int2 *mv = a.moves + (int64_t)row * a.most;
+  walk([&](int slot, bool kept, uint64_t hole, uint64_t fill) {
+    const uint64_t bit = 1ull << lane;
+    if (hole & bit) mv[hole_at + __popcll(hole & before)].y = slot;
+    if (fill & bit) mv[fill_at + __popcll(fill & before)].x = slot;
+    if (kept && slot < m) {
+      a.weights_out[at + slot] = w[slot];
+      a.pos_out[at + slot] = pos[slot];
+    }
+    hole_at += __popcll(hole);
+    fill_at += __popcll(fill);
+  });
+  if (tid == 0) a.count[row] = moves;
+}
+
+// D/4 lanes a move.  A stride of the grid over the row's moves, so that the
+// host need not know their number.
+template <int D>
+__global__ __launch_bounds__(256) void move_kernel(EvictArgs a) {
+  constexpr int L = D / 4;
+  const int row = blockIdx.x, b = row / a.c.H, h = row % a.c.H;
+  const int i = threadIdx.x % L;
+  if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    // the only place that reads lens after the selection, so it may be lens_out
+    const int len = kv_len(a.c, b);
+    a.lens_out[b] = min(len, a.keep);
+  }
+  const int64_t at = (int64_t)row * a.c.room();
+  const int count = a.count[row];
+  for (int k = blockIdx.y * (256 / L) + threadIdx.x / L; k < count; k += gridDim.y * (256 / L)) {
+    const int2 mv = a.moves[(int64_t)row * a.most + k];
+    const int64_t from = kv_token(a.c, b, h, mv.x), to = kv_token(a.c, b, h, mv.y);
+    if (from >= 0 && to >= 0) {
+      *reinterpret_cast<uint16_t *>(a.c.k + k_byte<D>(to, i)) =
+          *reinterpret_cast<const uint16_t *>(a.c.k + k_byte<D>(from, i));
+      *reinterpret_cast<uint16_t *>(a.c.v + v_byte<D>(to, i)) =
+          *reinterpret_cast<const uint16_t *>(a.c.v + v_byte<D>(from, i));
+      if (i == 0)
+        *reinterpret_cast<uint2 *>(a.c.scales + to * 4) =
+            *reinterpret_cast<const uint2 *>(a.c.scales + from * 4);
+    }
+    if (i == 0) {
+      a.weights_out[at + mv.y] = a.weights[at + mv.x];
+      a.pos_out[at + mv.y] = a.pos[at + mv.x];
+    }
+  }
+}
+
+int most_moves(int room, int keep) { return keep < room - keep ? keep : room - keep; }
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvView &c, int D, int n, const void *k, KvStrides ks,
+                            const void *v, KvStrides vs, bcq_dtype dt, const int32_t *positions,
+                            float *weights, int32_t *pos, hipStream_t s) {
+#define BCQ_DIM(D_)                                                                            \
+  return dt == BCQ_F16                                                                         \
+             ? append_dim<D_, _Float16>(c, n, k, ks, v, vs, positions, weights, pos, s)        \
+             : append_dim<D_, float>(c, n, k, ks, v, vs, positions, weights, pos, s)
+  if (D == 64) BCQ_DIM(64);
+  if (D == 128) BCQ_DIM(128);
+  BCQ_DIM(256);
+#undef BCQ_DIM
+}
+
+hipError_t launch_kv_read(const KvView &c, int D, int n, void *k, KvStrides ks, void *v,
+                          KvStrides vs, bcq_dtype dt, hipStream_t s) {
+#define BCQ_DIM(D_)                                                  \
+  return dt == BCQ_F16 ? read_dim<D_, _Float16>(c, n, k, ks, v, vs, s) \
+                       : read_dim<D_, float>(c, n, k, ks, v, vs, s)
+  if (D == 64) BCQ_DIM(64);
+  if (D == 128) BCQ_DIM(128);
+  BCQ_DIM(256);
+#undef BCQ_DIM
+}
+
+size_t evict_workspace_bytes(int B, int H, int room, int keep) {
+  if (keep >= room) return (size_t)B * H * 8;
+  return (size_t)B * H * (8 + (size_t)most_moves(room, keep) * sizeof(int2));
+}
+
+hipError_t launch_kv_evict(const KvView &c, int D, int keep, int recent, const float *weights,
+                           const int32_t *pos, int32_t *lens_out, float *weights_out,
+                           int32_t *pos_out, void *ws, hipStream_t s) {
+  const int BH = c.B * c.H, room = c.room();
+  EvictArgs a{c, keep, recent, weights, pos, lens_out, weights_out, pos_out, nullptr, nullptr, 0};
+  a.most = keep < room ? most_moves(room, keep) : 0;
+  a.moves = static_cast<int2 *>(ws);
+  a.count = reinterpret_cast<int32_t *>(a.moves + (size_t)BH * a.most);
+  if (room <= kEvictKeys)
+    select_kernel<true><<<BH, kEvictThreads, (size_t)room * 4, s>>>(a);
+  else
+    select_kernel<false><<<BH, kEvictThreads, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int per = 256 / (D / 4);
+  int chunks = (a.most + per - 1) / per;
+  chunks = chunks < 1 ? 1 : (chunks > 64 ? 64 : chunks);
+  const dim3 grid(BH, chunks);
+  if (D == 64)
+    move_kernel<64><<<grid, 256, 0, s>>>(a);
+  else if (D == 128)
+    move_kernel<128><<<grid, 256, 0, s>>>(a);
+  else
+    move_kernel<256><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace bcq

@@ -62,6 +62,8 @@ extern "C" {
 /* bcq_gemv_lowrank adds the correction inside the product's own launch (one
  * rounding of y) for K <= 4096 and R up to this rank. */
 #define BCQ_LOWRANK_FUSED_MAX_RANK 1024
+/* Largest number of tokens a sequence's page table may have room for. */
+#define BCQ_KV_MAX_TOKENS (1 << 24)
 /* Device scratch held by the library for bcq_gemm_skinny_noalloc, per GPU. */
 #define BCQ_NOALLOC_SCRATCH_BYTES (16u << 20)
 
@@ -403,6 +405,188 @@ bcq_status bcq_gemv_lowrank(const bcq_store *store, int32_t p, const void *x, bc
 bcq_status bcq_quantize(const void *W, bcq_dtype w_dtype, int32_t M, int32_t K, int32_t ldw,
                         int32_t P, int32_t p_low, int32_t iters, uint32_t *signs, void *alpha,
                         void *zero, bcq_dtype out_dtype, hipStream_t stream);
+
+/*
+ * 8-bit integer linear layer, for the prompts and batches whose products are
+ * bound by the matrix cores: weights in 8 bits with a scale for each output
+ * channel, activations rounded to 8 bits with a scale for each token.
+ *
+ * bcq_int_quantize rounds each row of X [rows][ldx] (ldx >= K, 16-byte aligned
+ * with ldx*size a multiple of 16 bytes) to 8 bits:
+ *     scales[r] = max_k |X[r][k]| * (1/127),  codes[r][k] = rint(X[r][k] / scales[r])
+ * in fp32 (the constant too), halves to even, codes in -127..127; a row of zeros has scale 0, a
+ * row that holds an infinity or NaN has scale NaN, and both have codes 0.
+ * codes: [rows][ldc] int8, ldc a multiple of 16 and at least K rounded up to
+ * one, 16-byte aligned; zeros are written from K up to that multiple, nothing
+ * past it.  It serves for tokens and, once, for weights.  rows = 0 does nothing.
+ */
+bcq_status bcq_int_quantize(const void *X, bcq_dtype dtype, int32_t rows, int32_t K, int32_t ldx,
+                            int8_t *codes, int32_t ldc, float *scales, hipStream_t stream);
+
+/*
+ * Y[t][m] = (sum_k A[t][k] * W[m][k]) * (a_scales[t] * w_scales[m]) + bias[m]
+ * with the sum exact in 32-bit integers, scaled and biased in fp32 and rounded
+ * once to dtype.
+ * A: [T][lda] codes as bcq_int_quantize writes them (zeros from K up to the next
+ *   multiple of 16), a_scales: [T] fp32.
+ * W: [M][ldw] codes of any value, readable up to the next multiple of 16 past
+ *   K, w_scales: [M] fp32.  lda, ldw: multiples of 16, at least K rounded up
+ *   to one; A and W 16-byte aligned.  1 <= K <= 131071, any M >= 1.
+ * bias: [M] of dtype, or NULL.  Y: [T][ldy], ldy >= M, element aligned, dtype
+ *   BCQ_F16 or BCQ_F32; columns past M are not written.
+ * workspace: bcq_int_workspace_bytes(T, M, K) bytes, 16-byte aligned, contents
+ *   of no account before and after; calls that may run at the same time need
+ *   separate ones.
+ * T = 0 does nothing.  Validation and stream behaviour as in bcq_gemv.
+ */
+bcq_status bcq_int_gemm(const int8_t *A, const float *a_scales, int32_t T, int32_t lda,
+                        const int8_t *W, const float *w_scales, int32_t M, int32_t K, int32_t ldw,
+                        const void *bias, void *Y, int32_t ldy, bcq_dtype dtype, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * bcq_int_quantize of the tokens X [T][ldx] and bcq_int_gemm with their codes,
+ * in one launch where the tokens are few and in two or three otherwise; the
+ * same results either way.  X and Y share dtype.
+ */
+bcq_status bcq_int_linear(const void *X, int32_t T, int32_t ldx, const int8_t *W,
+                          const float *w_scales, int32_t M, int32_t K, int32_t ldw,
+                          const void *bias, void *Y, int32_t ldy, bcq_dtype dtype,
+                          void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Device workspace of bcq_int_gemm and bcq_int_linear, 0 for an invalid shape. */
+size_t bcq_int_workspace_bytes(int32_t T, int32_t M, int32_t K);
+
+/*
+ * A key/value cache held in 4 bits, in pages.
+ *
+ * Each vector (one token's key or value of one cached head, head_dim channels)
+ * is zero + scale * code with codes 0..15 and an fp16 scale and zero of its
+ * own, as an asymmetric group of head_dim channels:
+ *     zero = fp16(min), scale = fp16((max - min) * (1/15)),
+ *     code = rint((x - zero) / scale), held to 0..15   (0 where scale is 0)
+ * evaluated in fp32 (the constant too).  A vector holding NaN, or values past fp16's range, gets
+ * a scale or zero that is not finite, and what reads it NaN.
+ *
+ * k_codes: [num_pages][heads][page_tokens][head_dim/2] bytes, channel 2i in the
+ *   low half of byte i, channel 2i + 1 in the high half.
+ * v_codes: [num_pages][heads][page_tokens/4][16][head_dim/64][4][2] bytes: a
+ *   block of 4 tokens holds channels 64h + 4r + 2c (low half) and
+ *   64h + 4r + 2c + 1 of its token t in byte [r][h][t][c].
+ * scales: [num_pages][heads][page_tokens][4] fp16: scale and zero of K, scale
+ *   and zero of V.
+ * page_table: [batch][max_pages]: page of each page_tokens slots of a sequence.
+ *   Entries past a sequence's length are not read.  Entries outside
+ *   [0, num_pages) are never followed: nothing is written there, and what is
+ *   read there is of no meaning but in bounds.
+ * lens: [batch] cached tokens of each sequence, read on the device (clamped to
+ *   0 .. max_pages * page_tokens).
+ * k_codes, v_codes and scales 16-byte aligned, the others 4.  head_dim 64, 128
+ * or 256, page_tokens a power of two from 16 to 256 (otherwise
+ * BCQ_ERR_UNSUPPORTED).  The memory is the caller's; the tables may change
+ * between calls, so calls may be captured in a graph.
+ *
+ * The tokens of a call are the last n of each sequence: token i of n lies in
+ * slot lens[b] - n + i, lens already counting them; tokens whose slot would be
+ * negative are not there (a sequence shorter than n).
+ */
+typedef struct {
+  int32_t batch;
+  int32_t heads; /* cached heads */
+  int32_t head_dim;
+  int32_t page_tokens;
+  int32_t num_pages;
+  int32_t max_pages; /* entries of a sequence in page_table */
+  uint8_t *k_codes;
+  uint8_t *v_codes;
+  void *scales;
+  const int32_t *page_table;
+  const int32_t *lens;
+} bcq_kv_cache;
+
+/*
+ * Quantizes the last n tokens of every sequence into the cache.
+ * K, V: element (b, i, h, d) at b*_batch + i*_token + h*_head + d, in elements of
+ *   dtype (BCQ_F16 or BCQ_F32), element aligned: any layout with contiguous
+ *   channels, as a slice of a projection's output.
+ * weights, pos: [batch][heads][max_pages * page_tokens], or NULL: for each slot
+ *   written, weights becomes 0 and pos the token's position, positions[b][i]
+ *   (or the slot where positions is NULL), as bcq_kv_evict reads them.
+ * n = 0 does nothing.  Validation and stream behaviour as in bcq_gemv.
+ */
+bcq_status bcq_kv_append(const bcq_kv_cache *cache, int32_t n, const void *K, int64_t k_batch,
+                         int64_t k_token, int64_t k_head, const void *V, int64_t v_batch,
+                         int64_t v_token, int64_t v_head, bcq_dtype dtype,
+                         const int32_t *positions, float *weights, int32_t *pos,
+                         hipStream_t stream);
+
+/*
+ * The values the last n tokens' codes stand for (zero + scale * code, rounded
+ * once to dtype), laid out as in bcq_kv_append; zeros for tokens that are not
+ * there.  For inspection, and for what needs the cache dense.
+ */
+bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_batch,
+                       int64_t k_token, int64_t k_head, void *V, int64_t v_batch,
+                       int64_t v_token, int64_t v_head, bcq_dtype dtype, hipStream_t stream);
+
+/*
+ * Attention of the last n tokens' queries over the cache, causal: query i of
+ * sequence b sees slots 0 .. lens[b] - n + i.
+ *     O[b][i][g] = sum_t softmax_t(scale * Q[b][i][g] . k_t) v_t
+ * with query head g reading cached head g / (q_heads / heads).  n = 1 is a
+ * decode step, larger n drafted tokens or a prompt (appended before).  A query
+ * that sees nothing gets zeros.  What a query does not see has no influence,
+ * whatever its scales hold.
+ * Q, O: strides as in bcq_kv_append, q_heads heads (a multiple of heads), dtype
+ *   BCQ_F16 or BCQ_F32.  scale: finite; 1/sqrt(head_dim) is usual.
+ * weights: NULL, or [batch][heads][max_pages * page_tokens] fp32, to whose slots
+ *   the probabilities are added, summed over the queries and over the query
+ *   heads of a cached head, in a fixed order.
+ * Products run on the matrix cores with the codes as they are; softmax and
+ * sums are in fp32.  In fp16 calls each token's probability times its V scale
+ * is rounded once to fp16 (relative to the largest of its row); fp32 calls
+ * hold it, and the queries, in 22 bits.
+ * workspace: bcq_kv_workspace_bytes(cache, n, q_heads, weights != NULL) bytes,
+ *   16-byte aligned, of no account before and after; calls that may run at the
+ *   same time need separate ones.  NULL when that is 0.
+ * n = 0 does nothing.  Validation and stream behaviour as in bcq_gemv.
+ */
+bcq_status bcq_kv_attend(const bcq_kv_cache *cache, const void *Q, int32_t n, int32_t q_heads,
+                         int64_t q_batch, int64_t q_token, int64_t q_head, void *O,
+                         int64_t o_batch, int64_t o_token, int64_t o_head, bcq_dtype dtype,
+                         float scale, float *weights, void *workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* Device workspace of bcq_kv_attend, 0 when none or for an invalid call. */
+size_t bcq_kv_workspace_bytes(const bcq_kv_cache *cache, int32_t n, int32_t q_heads,
+                              int32_t with_weights);
+
+/*
+ * Shrinks every sequence longer than `keep` tokens to `keep`, each cached head
+ * choosing for itself: the `recent` newest tokens (those with pos above the
+ * head's largest minus recent) first, then the largest weights, the lower slot
+ * first among equals; a NaN weight counts as the smallest.
+ * Kept tokens in slots below keep stay; the i-th evicted slot there receives the
+ * i-th kept token from behind, codes, scales, weight and position, so only
+ * what has to move is moved.  Slots from keep on are free afterwards, and
+ * attention, which sees every cached token of the past, does not depend on
+ * their order.
+ * weights, pos: as bcq_kv_append and bcq_kv_attend keep them.
+ * lens_out [batch], weights_out, pos_out: the state afterwards, each the array
+ *   read (cache->lens, weights, pos) for an update in place, or one that does
+ *   not overlap it; entries past a sequence's new length are not written.
+ * 1 <= keep, 0 <= recent <= keep.
+ * workspace: bcq_kv_evict_workspace_bytes(cache, keep) bytes, 16-byte aligned,
+ *   of no account before and after; calls that may run at the same time need
+ *   separate ones.  Validation and stream behaviour as in bcq_gemv.
+ */
+bcq_status bcq_kv_evict(const bcq_kv_cache *cache, int32_t keep, int32_t recent,
+                        const float *weights, const int32_t *pos, int32_t *lens_out,
+                        float *weights_out, int32_t *pos_out, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/* Device workspace of bcq_kv_evict, 0 for an invalid call. */
+size_t bcq_kv_evict_workspace_bytes(const bcq_kv_cache *cache, int32_t keep);
 
 /* Static text for a status code (never null). */
 const char *bcq_status_string(bcq_status status);
