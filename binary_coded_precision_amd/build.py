@@ -18,9 +18,13 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbcq.so")
 SOURCES = ["bcq_api.hip", "pack.hip", "gemv_lut.hip", "gemm_mfma.hip", "lowrank.hip", "dequant.hip",
            "quantize.hip", "serve_api.hip", "int_gemm.hip", "kv_cache.hip", "kv_attend.hip"]
-# Per-file flags: the quantizer takes its sign decisions on exactly rounded
-# fp64 values, so no multiply-add there is fused into one rounding.
-FILE_FLAGS = {"quantize.hip": ["-ffp-contract=off"]}
+# Per-file flags: the quantizers' codes are functions of exactly rounded values
+# (fp64 in the planes', fp32 in the key/value cache's), so no multiply-add there
+# is fused into one rounding.
+# The attention's accumulators stay in ordinary registers: it rescales them, and
+# in the matrix cores' own ones every rescaling loop would copy them both ways.
+FILE_FLAGS = {"quantize.hip": ["-ffp-contract=off"], "kv_cache.hip": ["-ffp-contract=off"],
+              "kv_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 # Measurement kernels of the benchmark's floor row (empty launch, plain
 # streaming read): a library of their own, outside the BCQ ABI.
 PROBE_LIB = os.path.join(HERE, "libbcq_probe.so")

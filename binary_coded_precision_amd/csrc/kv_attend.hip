@@ -6,7 +6,7 @@
 //
 //   s_t = scale * (ks_t * (q . ck_t) + kz_t * sum(q))        (in log2 units here)
 //   out = sum_t p_t v_t / sum_t p_t,  p_t = 2^(s_t - m)
-//       = (sum_t (p_t vs_t) (cv_t - 8) + sum_t p_t (vz_t + 8 vs_t)) / sum_t p_t
+//       = (sum_t (p_t vs_t) (cv_t - 7.5) + sum_t p_t (vz_t + 7.5 vs_t)) / sum_t p_t
 //
 // so both products run on the codes themselves, which fp16 holds exactly, and
 // each token's four factors enter in fp32 afterwards.  A code c of K sits in an
@@ -22,13 +22,15 @@
 // Roundings below 32 bits, for fp16 calls: p_t * vs_t, once, to fp16, relative
 // to the row's largest (below).  It is as large as the output's own rounding.
 // For fp32 calls the queries (after a power of two for each row) and p_t * vs_t
-// are each held as the sum of two fp16, 22 bits.
+// are each held as the sum of two fp16, 22 bits; and as the matrix cores cut off
+// what they add to a running sum, 1e-7 of it each time and always downwards
+// (measured), fp32 calls start every product at zero and sum in ordinary fp32.
 //
 // The reference m of a row's exponentials is a maximum over s_t + log2(vs_t)
 // (log2 to a tenth, from the fp16's bits) rather than over s_t: then p_t * vs_t
 // stays within fp16's normal range around its largest whatever the scales of V
 // are, and sum p_t in fp32 has room for the difference.  m is raised, and what
-// is summed so far rescaled, only when a tile exceeds it by more than 2^8, so
+// is summed so far rescaled, only when a tile exceeds it by more than 2^6, so
 // the lanes of a row rarely have to agree.
 //
 // Layout: S^T = K Q^T with 16 tokens as a tile's rows and 16 query rows as its
@@ -51,8 +53,11 @@ typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr float kNegInf = -INFINITY;
 // A tile may exceed a row's reference by this many powers of two before what is
-// summed is rescaled: p_t * vs_t then stays below 2^10 in fp16.
-constexpr float kSlack = 8.f;
+// summed is rescaled, and terms are held larger by kLift powers of two than that
+// reference says: p_t * vs_t is about 2^9 at a row's largest and stays below 2^15.1
+// in fp16, and what fp32 calls keep of its rounding is above fp16's smallest.
+constexpr float kSlack = 6.f, kLift = 9.f;
+constexpr float kRaise = 15.f + kLift;  // 15: the exponent's bias in the V scale's bits
 constexpr float kCodeScale = 16777216.f;  // 2^24: a code's subnormal back to the code
 
 struct Ws {
@@ -66,12 +71,12 @@ union Frag {
   half8 h;
 };
 
-// One 16-token tile as a lane holds it.
+// Two 16-token tiles as a lane holds them.
 template <int D>
-struct Tile {
-  uint32_t k[D / 32];  // its quarter of one token's K codes
-  uint32_t v[D / 32];  // 4 tokens' codes of its D/16 channels
-  uint4 m[2];          // the 4 tokens' factors
+struct Tiles {
+  uint32_t k[2][D / 32];  // its quarter of one token's K codes
+  uint32_t v[2][D / 32];  // 4 tokens' codes of its D/16 channels
+  uint32_t m[2][8];       // the 4 tokens' factors: (K scale, zero), (V scale, zero) each
 };
 
 template <int N>
@@ -88,86 +93,89 @@ __device__ __forceinline__ void load_words(uint32_t (&dst)[N], const uint8_t *sr
   }
 }
 
-template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &t, const KvView &c, int b, int h, int tok,
-                                          int lane) {
-  const int r = lane & 15, g = lane >> 4;
-  const int page = __builtin_amdgcn_readfirstlane(
-      c.table[(int64_t)b * c.max_pages + (tok >> c.page_log)]);
-  // an entry that names no page is never followed
-  const int safe = (unsigned)page < (unsigned)c.num_pages ? page : 0;
-  const int64_t at = (((int64_t)safe * c.H + h) << c.page_log) + (tok & ((1 << c.page_log) - 1));
-  load_words(t.k, c.k + at * (D / 2) + r * (D / 2) + g * (D / 8));
-  load_words(t.v, c.v + at * (D / 2) + g * (2 * D) + r * (D / 8));
-  const uint4 *m = reinterpret_cast<const uint4 *>(c.scales + at * 4) + g * 2;
-  t.m[0] = m[0];
-  t.m[1] = m[1];
-}
-
-__device__ __forceinline__ float half_bits(uint32_t w) {
-  union {
-    uint16_t u;
-    _Float16 h;
-  } x;
-  x.u = (uint16_t)w;
-  return (float)x.h;
-}
-
-// A token's factors: K scale and zero in log2 units, V scale and the value of
-// its code 8, and the
-// rough log2 of the V scale (its fp16 bits over 1024, exact at powers of two).
-struct Factors {
-  float ks, kz, vs, vz, lv;
+// Where the two tiles of tokens t..t+31 lie.  The second is the first again where
+// the sequence ends before it; an entry that names no page is never followed.
+struct Where {
+  int64_t at[2];
 };
-__device__ __forceinline__ Factors factors(uint32_t kw, uint32_t vw, float scale_log2) {
-  Factors f;
-  f.ks = half_bits(kw) * (scale_log2 * kCodeScale);
-  f.kz = half_bits(kw >> 16) * scale_log2;
-  f.vs = half_bits(vw);
-  f.vz = half_bits(vw >> 16) + 8.f * f.vs;
-  f.lv = (float)(vw & 0x7fffu) * (1.f / 1024.f) - 15.f;
-  return f;
+__device__ __forceinline__ Where where(const KvView &c, int b, int h, int t, int len) {
+  Where w;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int tok = t + 16 * s < len ? t + 16 * s : t;
+    const int page = __builtin_amdgcn_readfirstlane(
+        c.table[(int64_t)b * c.max_pages + (tok >> c.page_log)]);
+    const int safe = (unsigned)page < (unsigned)c.num_pages ? page : 0;
+    w.at[s] = (((int64_t)safe * c.H + h) << c.page_log) + (tok & ((1 << c.page_log) - 1));
+  }
+  return w;
 }
 template <int D>
-__device__ __forceinline__ Factors factors(const Tile<D> &t, int i, float scale_log2) {
-  const uint4 m = t.m[i >> 1];
-  return (i & 1) ? factors(m.z, m.w, scale_log2) : factors(m.x, m.y, scale_log2);
+__device__ __forceinline__ void load_k(Tiles<D> &t, const KvView &c, const Where &w, int lane) {
+  const int off = (lane & 15) * (D / 2) + (lane >> 4) * (D / 8);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) load_words(t.k[s], c.k + w.at[s] * (D / 2) + off);
 }
-
-// Left operand of S^T for word w of the tile: channels 8w..8w+7 of the lane's
-// quarter in the order 0 4 1 5 2 6 3 7, the odd ones sixteenfold.
 template <int D>
-__device__ __forceinline__ half8 k_frag(const Tile<D> &t, int w) {
-  const uint32_t lo = t.k[w], hi = lo >> 8;
-  Frag f;
-  f.w[0] = lo & 0x000f000fu;
-  f.w[1] = lo & 0x00f000f0u;
-  f.w[2] = hi & 0x000f000fu;
-  f.w[3] = hi & 0x00f000f0u;
-  return f.h;
+__device__ __forceinline__ void load_v(Tiles<D> &t, const KvView &c, const Where &w, int lane) {
+  const int off = (lane >> 4) * (2 * D) + (lane & 15) * (D / 8);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) load_words(t.v[s], c.v + w.at[s] * (D / 2) + off);
+}
+template <int D>
+__device__ __forceinline__ void load_m(Tiles<D> &t, const KvView &c, const Where &w, int lane) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    load_words(t.m[s],
+               reinterpret_cast<const uint8_t *>(c.scales) + w.at[s] * 8 + (lane >> 4) * 32);
 }
 
-// Codes less 8 of two tokens: the nibbles N (of a 16-bit unit's lower two) of
-// both halves of a word.  A nibble in a mantissa under the exponent of 2^10, or
-// of 2^6 for one four bits up, is 1024 + c or 64 + c; the subtraction is exact.
-template <int N>
-__device__ __forceinline__ half2v centred(uint32_t w) {
+__device__ __forceinline__ half2v pair_of(uint32_t w) {
   union {
     uint32_t u;
     half2v h;
   } x;
-  x.u = N ? (w & 0x00f000f0u) | 0x54005400u : (w & 0x000f000fu) | 0x64006400u;
-  const _Float16 base = N ? (_Float16)72.f : (_Float16)1032.f;
-  return x.h - half2v{base, base};
+  x.u = w;
+  return x.h;
 }
 
-// Right operand of S^T: a query row's channels in k_frag's order.
-__device__ __forceinline__ half8 q_order(const float (&x)[8]) {
+// Left operand of S^T for word w of a tile: channels 8w..8w+7 of the lane's
+// quarter in the order 0 4 1 5 2 6 3 7.  fp16 calls take the odd ones 16-fold,
+// as their bits lie.  fp32 calls shift all of them there: the matrix cores keep
+// fewer bits of a product with a smaller subnormal (measured: 1e-6 of a sum of
+// 32 products with c * 2^-24, 2e-8 with 16c * 2^-24).
+template <int D, bool F32>
+__device__ __forceinline__ half8 k_frag(const Tiles<D> &t, int s, int w) {
+  const uint32_t x = t.k[s][w], x8 = x >> 8;
+  Frag f;
+  f.w[0] = F32 ? (x << 4) & 0x00f000f0u : x & 0x000f000fu;
+  f.w[1] = x & 0x00f000f0u;
+  f.w[2] = F32 ? (x >> 4) & 0x00f000f0u : x8 & 0x000f000fu;
+  f.w[3] = x8 & 0x00f000f0u;
+  return f.h;
+}
+
+// (code - 7.5) / 512 of two tokens, the low (N = 0) or high nibbles of the bytes
+// at the bottom of a word's halves: as subnormals c * 2^-24 or 16c * 2^-24, which
+// one exact multiply-add takes to the centred value.
+template <int N>
+__device__ __forceinline__ half2v centred(uint32_t w) {
+  const half2v x = pair_of(w & (N ? 0x00f000f0u : 0x000f000fu));
+  const _Float16 up = (_Float16)(N ? 2048.f : 32768.f), mid = (_Float16)(-7.5f / 512.f);
+  return __builtin_elementwise_fma(x, half2v{up, up}, half2v{mid, mid});
+}
+constexpr float kCentreScale = 512.f;
+
+// Right operand of S^T: a query row's channels in k_frag's order, the odd ones
+// times `odd`.
+__device__ __forceinline__ half8 q_order(const float (&x)[8], float odd) {
   half8 f;
-  f[0] = (_Float16)x[0], f[1] = (_Float16)x[4];
-  f[2] = (_Float16)(x[1] * 0.0625f), f[3] = (_Float16)(x[5] * 0.0625f);
-  f[4] = (_Float16)x[2], f[5] = (_Float16)x[6];
-  f[6] = (_Float16)(x[3] * 0.0625f), f[7] = (_Float16)(x[7] * 0.0625f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float by = (e & 1) ? odd : 1.f;
+    f[2 * e] = (_Float16)(x[e] * by);
+    f[2 * e + 1] = (_Float16)(x[e + 4] * by);
+  }
   return f;
 }
 
@@ -186,7 +194,7 @@ template <int D, int CT, bool F32>
 struct Queries {
   half8 hi[CT][D / 32];
   half8 lo[F32 ? CT : 1][F32 ? D / 32 : 1];
-  float sum[CT];
+  float sum[CT];  // of the row, in the codes' unit 2^-24
   float row_scale[F32 ? CT : 1];
 };
 
@@ -202,11 +210,24 @@ __device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q, const Atten
       const int i = row / a.G, hq = h * a.G + row % a.G;
       const int64_t at = b * a.qs.batch + i * a.qs.token + hq * a.qs.head + g * (D / 4);
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w)
+      for (int w = 0; w < D / 32; ++w) {
+        if (a.q_wide && F32) {
+          const float4v *p =
+              reinterpret_cast<const float4v *>(static_cast<const float *>(a.q) + at + w * 8);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[w][e] = F32 ? static_cast<const float *>(a.q)[at + w * 8 + e]
-                        : (float)static_cast<const _Float16 *>(a.q)[at + w * 8 + e];
+          for (int e = 0; e < 8; ++e) x[w][e] = p[e >> 2][e & 3];
+        } else if (a.q_wide) {
+          const half8 v =
+              *reinterpret_cast<const half8 *>(static_cast<const _Float16 *>(a.q) + at + w * 8);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[w][e] = (float)v[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[w][e] = F32 ? static_cast<const float *>(a.q)[at + w * 8 + e]
+                          : (float)static_cast<const _Float16 *>(a.q)[at + w * 8 + e];
+        }
+      }
     } else {
 #pragma unroll
       for (int w = 0; w < D / 32; ++w)
@@ -218,56 +239,61 @@ __device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q, const Atten
     for (int w = 0; w < D / 32; ++w)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        x[w][e] = a.negate ? -x[w][e] : x[w][e];
         sum += x[w][e];
         top = fmaxf(top, fabsf(x[w][e]));
       }
-    Q.sum[ct] = group_sum(sum);
+    Q.sum[ct] = group_sum(sum) * (1.f / kCodeScale);
     if constexpr (F32) {
       top = group_max(top);
-      const int e2 = (top > 0.f && top < INFINITY) ? ilogbf(top) : 0;
-      Q.row_scale[ct] = ldexpf(1.f, e2);
+      // the largest to 2^10..2^11: what the first fp16 leaves stays a normal one
+      const int e2 = (top > 0.f && top < INFINITY) ? ilogbf(top) - 10 : 0;
+      Q.row_scale[ct] = ldexpf(1.f, e2 - 4);  // and k_frag's 16
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         float y[8], rest[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[w][e], -e2);
-        Q.hi[ct][w] = q_order(y);
-        // what the first fp16 leaves, taken at the scale it was rounded at
-#pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float f = (e & 1) ? 0.0625f : 1.f, inv = (e & 1) ? 16.f : 1.f;
-          rest[e] = y[e] - (float)(_Float16)(y[e] * f) * inv;
+          y[e] = ldexpf(x[w][e], -e2);
+          rest[e] = y[e] - (float)(_Float16)y[e];
         }
-        Q.lo[ct][w] = q_order(rest);
+        Q.hi[ct][w] = q_order(y, 1.f);
+        Q.lo[ct][w] = q_order(rest, 1.f);
       }
     } else {
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) Q.hi[ct][w] = q_order(x[w]);
+      for (int w = 0; w < D / 32; ++w) Q.hi[ct][w] = q_order(x[w], 0.0625f);
     }
   }
 }
 
 // q . c (times 2^-24) of one 16-token tile for the lane's column and 4 tokens.
 template <int D, int CT, bool F32>
-__device__ __forceinline__ void tile_scores(float4v (&S)[CT], const Tile<D> &t,
+__device__ __forceinline__ void tile_scores(float4v (&S)[CT], const Tiles<D> &t, int s,
                                             const Queries<D, CT, F32> &Q) {
+  const float4v zero = {0.f, 0.f, 0.f, 0.f};
+  float4v low[F32 ? CT : 1];
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) S[ct] = float4v{0.f, 0.f, 0.f, 0.f};
+  for (int ct = 0; ct < CT; ++ct) {
+    S[ct] = zero;
+    if constexpr (F32) low[ct] = zero;
+  }
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {
-    const half8 kf = k_frag<D>(t, w);
+    const half8 kf = k_frag<D, F32>(t, s, w);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      S[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, Q.hi[ct][w], S[ct], 0, 0, 0);
-      if constexpr (F32)
-        S[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, Q.lo[ct][w], S[ct], 0, 0, 0);
+      if constexpr (F32) {
+        low[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, Q.lo[ct][w], low[ct], 0, 0, 0);
+        S[ct] += __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, Q.hi[ct][w], zero, 0, 0, 0);
+      } else {
+        S[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, Q.hi[ct][w], S[ct], 0, 0, 0);
+      }
     }
   }
   if constexpr (F32) {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) S[ct][i] *= Q.row_scale[ct];
+    for (int ct = 0; ct < CT; ++ct) S[ct] = (S[ct] + low[ct]) * Q.row_scale[ct];
   }
 }
 
@@ -278,49 +304,80 @@ struct Sums {
   float m[CT], l[CT], z[CT];
 };
 
-template <int D, int CT, bool F32, bool MASK, bool STORE>
-__device__ __forceinline__ void step(Sums<D, CT> &A, const Tile<D> (&T)[2],
-                                     const Queries<D, CT, F32> &Q, const AttendArgs &a, int t,
-                                     const int (&last)[CT], int len, float *const (&sc)[CT],
-                                     int lane) {
-  const int g = lane >> 4;
-  float4v S[2][CT];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) tile_scores<D, CT, F32>(S[s], T[s], Q);
+// A score before the softmax's scale, in the unit 2^-24: ks * (q . c) + kz * sum(q).
+__device__ __forceinline__ float raw_score(float qc, float sum, uint32_t m) {
+  const half2v f = pair_of(m);
+  return fmaf(qc, (float)f[0], sum * (float)f[1]);
+}
 
+template <int D, int CT, bool F32>
+__device__ __forceinline__ void raw_scores(float4v (&S)[2][CT], const Tiles<D> &T,
+                                           const Queries<D, CT, F32> &Q) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    tile_scores<D, CT, F32>(S[s], T, s, Q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        S[s][ct][i] = raw_score(S[s][ct][i], Q.sum[ct], T.m[s][2 * i]);
+  }
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
+// Scores of the tokens past each row's last to -inf.  Factors of V that are not
+// finite would reach hidden rows as 0 * NaN: they become 0, and the score of a
+// row that does see them NaN, which makes its output NaN all the same.
+template <int D, int CT>
+__device__ __forceinline__ void mask_scores(float4v (&S)[2][CT], Tiles<D> &T, int t,
+                                            const int (&last)[CT]) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // opaque here, so that the compiler leaves the test in this branch
+      asm volatile("" : "+v"(T.m[s][2 * i + 1]));
+      const bool bad = not_finite(T.m[s][2 * i + 1]);
+      T.m[s][2 * i + 1] = bad ? 0u : T.m[s][2 * i + 1];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const float x = bad ? NAN : S[s][ct][i];
+        S[s][ct][i] = t + 16 * s + i > last[ct] ? kNegInf : x;
+      }
+    }
+}
+
+// The softmax's step over 32 tokens: raises the rows' references, rescales, adds
+// to their sums and leaves probability times V scale in P.
+template <int D, int CT, bool TWO>
+__device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, half8 (&P)[CT],
+                                              half8 (&Plo)[TWO ? CT : 1],
+                                              const float4v (&S)[2][CT], const Tiles<D> &T,
+                                              float unit) {
   float top[CT];
-  bool raise = false;
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) top[ct] = kNegInf;
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const Factors f = factors<D>(T[s], i, a.scale_log2);
+      // the V scale's bits over 1024: its log2 to a tenth, plus 15
+      const float lv = (float)(T.m[s][2 * i + 1] & 0xffffu) * (1.f / 1024.f);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        float x = S[s][ct][i] * f.ks + Q.sum[ct] * f.kz;
-        if (MASK && t + 16 * s + 4 * g + i > last[ct]) x = kNegInf;
-        S[s][ct][i] = x;
-        top[ct] = fmaxf(top[ct], x + f.lv);
-      }
+      for (int ct = 0; ct < CT; ++ct) top[ct] = fmaxf(top[ct], fmaf(S[s][ct][i], unit, lv));
     }
-  if constexpr (STORE) {
+  bool raise = false;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        if (sc[ct] != nullptr && t + 16 * s < len)
-          *reinterpret_cast<float4v *>(sc[ct] + t + 16 * s + 4 * g) = S[s][ct];
-  }
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) raise |= top[ct] > A.m[ct] + kSlack;
+  for (int ct = 0; ct < CT; ++ct) raise |= top[ct] > A.m[ct] + (kRaise + kSlack);
   if (__any(raise)) {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       // each row by its own scores, so that no row depends on its neighbours
-      const float t = group_max(top[ct]);
-      const float m = t > A.m[ct] + kSlack ? t : A.m[ct];
+      const float z = group_max(top[ct]);
+      const float m = z > A.m[ct] + (kRaise + kSlack) ? z - kRaise : A.m[ct];
       const float f = m == A.m[ct] ? 1.f : exp2f(A.m[ct] - m);
       A.m[ct] = m;
       A.l[ct] *= f;
@@ -331,30 +388,45 @@ __device__ __forceinline__ void step(Sums<D, CT> &A, const Tile<D> (&T)[2],
         for (int i = 0; i < 4; ++i) A.o[ct][d][i] *= f;
     }
   }
-  half8 P[CT], Plo[F32 ? CT : 1];
+  // a row that has seen nothing yet has no reference; its terms are 2^-inf
+  float m[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) m[ct] = fmaxf(A.m[ct], -3.0e38f);
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const Factors f = factors<D>(T[s], i, a.scale_log2);
+      const half2v f = pair_of(T.m[s][2 * i + 1]);
+      const float mid = fmaf(7.5f, (float)f[0], (float)f[1]);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        const bool hidden = MASK && t + 16 * s + 4 * g + i > last[ct];
-        // a masked token's factors may hold anything, NaN included
-        const float p = hidden ? 0.f : __builtin_amdgcn_exp2f(S[s][ct][i] - A.m[ct]);
+        const float p = __builtin_amdgcn_exp2f(fmaf(S[s][ct][i], unit, -m[ct]));
         A.l[ct] += p;
-        A.z[ct] += hidden ? 0.f : p * f.vz;
-        const float pv = hidden ? 0.f : p * f.vs;
-        P[ct][4 * s + i] = (_Float16)pv;
-        if constexpr (F32) Plo[ct][4 * s + i] = (_Float16)(pv - (float)(_Float16)pv);
+        A.z[ct] = fmaf(p, mid, A.z[ct]);
+        float pv = p * (float)f[0];
+        if constexpr (TWO) {
+          // one value for both parts: the product and its rounding could be fused
+          asm volatile("" : "+v"(pv));
+          const _Float16 high = (_Float16)pv;
+          P[ct][4 * s + i] = high;
+          Plo[ct][4 * s + i] = (_Float16)(pv - (float)high);
+        } else {
+          P[ct][4 * s + i] = (_Float16)pv;
+        }
       }
     }
+}
+
+template <int D, int CT, bool F32, bool TWO>
+__device__ __forceinline__ void add_values(Sums<D, CT> &A, const half8 (&P)[CT],
+                                           const half8 (&Plo)[TWO ? CT : 1],
+                                           const Tiles<D> &T) {
 #pragma unroll
   for (int hh = 0; hh < D / 64; ++hh) {
     half8 vf[4];  // by the channel's place in its four
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t w = T[e >> 1].v[2 * hh + (e & 1)], w8 = w >> 8;
+      const uint32_t w = T.v[e >> 1][2 * hh + (e & 1)], w8 = w >> 8;
       const half2v x[4] = {centred<0>(w), centred<1>(w), centred<0>(w8), centred<1>(w8)};
 #pragma unroll
       for (int j = 0; j < 4; ++j) vf[j][2 * e] = x[j][0], vf[j][2 * e + 1] = x[j][1];
@@ -364,8 +436,15 @@ __device__ __forceinline__ void step(Sums<D, CT> &A, const Tile<D> (&T)[2],
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float4v &o = A.o[ct][4 * hh + j];
-        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct], o, 0, 0, 0);
-        if constexpr (F32) o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct], o, 0, 0, 0);
+        if constexpr (F32) {
+          float4v x = {0.f, 0.f, 0.f, 0.f};
+          x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct], x, 0, 0, 0);
+          o += __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct], x, 0, 0, 0);
+        } else {
+          if constexpr (TWO)
+            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct], o, 0, 0, 0);
+          o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct], o, 0, 0, 0);
+        }
       }
   }
 }
@@ -381,32 +460,50 @@ __device__ __forceinline__ int64_t out_at(const AttendArgs &a, int b, int h, int
   return b * a.os.batch + (row / a.G) * a.os.token + (int64_t)(h * a.G + row % a.G) * a.os.head;
 }
 
+// Waves a SIMD that the registers are held to: with few rows the loads' latency
+// is what counts, and 4 waves (128 registers) hide more of it than 3.
+constexpr int least_waves(int D, int CT, int WT, bool f32) {
+  return WT == 4 && CT == 1 && D <= 128 && !f32 ? 4 : 1;
+}
+
 // Grid: BH x splits x row_blocks workgroups, the cached head fastest (those of
 // one head are 8 apart whenever BH is a multiple of 8, so they share an XCD's
-// L2), the last rows first (they see the most tokens).
-template <int D, int CT, int WT, bool F32, bool STORE>
-__global__ __launch_bounds__(256) void attend_kernel(AttendArgs a, int splits, int row_blocks,
-                                                     Ws ws) {
-  constexpr int WR = 4 / WT;
+// L2), the last rows first (they see the most tokens).  WT waves take turns over
+// the tokens of a workgroup's rows, or WR waves have rows of their own.
+template <int D, int CT, int WT, int WR, bool F32, bool STORE>
+__global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void attend_kernel(AttendArgs a, int splits,
+                                                             int row_blocks, Ws ws) {
+  constexpr bool TWO = F32 || WT > 1;  // probability times V scale in two fp16
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WT, wt = wave % WT;
   const int BH = a.c.B * a.c.H, R = a.n * a.G;
-  const int bh = blockIdx.x % BH, rest = blockIdx.x / BH;
+  const int rest = blockIdx.x / BH;
   const int split = rest % splits, rb = row_blocks - 1 - rest / splits;
-  const int b = bh / a.c.H, h = bh % a.c.H;
+  // each split starts at another sequence, so that the compute unit that gets
+  // the same place of every split does not get one long sequence's share each time
+  const int h = blockIdx.x % BH % a.c.H;
+  const int b = (blockIdx.x % BH / a.c.H + split * ((a.c.B + splits - 1) / splits)) % a.c.B;
+  const int bh = b * a.c.H + h;
   const int L = kv_len(a.c, b);
   const int row0 = (rb * WR + wr) * CT * 16;
 
   // tokens of these rows and of this split
-  int tile_end = 0, tile_begin = 0, free_end = 0;
+  int tile_end = 0, tile = 0, free_end = 0;
   if (row0 < R) {
     const int end_row = min(row0 + CT * 16, R) - 1;
     const int tiles = (max(0, L - a.n + end_row / a.G + 1) + 31) / 32;
     const int chunk = (tiles + splits - 1) / splits;
-    tile_begin = split * chunk;
-    tile_end = min(tiles, tile_begin + chunk);
+    tile = split * chunk + wt;
+    tile_end = min(tiles, split * chunk + chunk);
     free_end = max(0, L - a.n + row0 / a.G + 1) / 32;  // tiles before it need no mask
+  }
+  Tiles<D> T;
+  if (tile < tile_end) {
+    const Where w = where(a.c, b, h, tile * 32, L);
+    load_k(T, a.c, w, lane);
+    load_m(T, a.c, w, lane);
+    load_v(T, a.c, w, lane);
   }
 
   Queries<D, CT, F32> Q;
@@ -425,23 +522,28 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a, int splits, i
     for (int d = 0; d < D / 16; ++d) A.o[ct][d] = float4v{0.f, 0.f, 0.f, 0.f};
   }
 
-  int tile = tile_begin + wt;
-  Tile<D> cur[2], nxt[2];
-  auto load = [&](Tile<D>(&T)[2], int ti) {
-    const int t = ti * 32;
-    load_tile<D>(T[0], a.c, b, h, t, lane);
-    load_tile<D>(T[1], a.c, b, h, t + 16 < L ? t + 16 : t, lane);
-  };
-  if (tile < tile_end) load(cur, tile);
+  // the next tiles are asked for as soon as the registers of these are free
   while (tile < tile_end) {
     const int next = tile + WT;
-    load(nxt, next < tile_end ? next : tile);
-    if (tile < free_end)
-      step<D, CT, F32, false, STORE>(A, cur, Q, a, tile * 32, last, L, sc, lane);
-    else
-      step<D, CT, F32, true, STORE>(A, cur, Q, a, tile * 32, last, L, sc, lane);
-    cur[0] = nxt[0];
-    cur[1] = nxt[1];
+    const Where w = where(a.c, b, h, (next < tile_end ? next : tile) * 32, L);
+    float4v S[2][CT];
+    raw_scores<D, CT, F32>(S, T, Q);
+    load_k(T, a.c, w, lane);
+    if (tile >= free_end) mask_scores<D, CT>(S, T, tile * 32 + 4 * g, last);
+    if constexpr (STORE) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          if (sc[ct] != nullptr && tile * 32 + 16 * s < L)
+            *reinterpret_cast<float4v *>(sc[ct] + tile * 32 + 16 * s + 4 * g) =
+                S[s][ct] * a.unit;
+    }
+    half8 P[CT], Plo[TWO ? CT : 1];
+    softmax_tiles<D, CT, TWO>(A, P, Plo, S, T, a.unit);
+    load_m(T, a.c, w, lane);
+    add_values<D, CT, F32, TWO>(A, P, Plo, T);
+    load_v(T, a.c, w, lane);
     tile = next;
   }
 
@@ -454,11 +556,12 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a, int splits, i
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        A.o[ct][d][i] += A.z[ct];
+        A.o[ct][d][i] = fmaf(A.o[ct][d][i], kCentreScale, A.z[ct]);
   }
 
   if constexpr (WT > 1) {
-    // the waves' rows are the same: join them in shared memory
+    // the waves' rows are the same: they meet in shared memory, then a wave joins
+    // a row
     constexpr int N = CT * 16;
     __shared__ float so[WT][N][D + 4];
     __shared__ float sm[WT][N], sl[WT][N];
@@ -469,35 +572,43 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a, int splits, i
         sm[wt][col] = A.m[ct];
         sl[wt][col] = A.l[ct];
       }
+      if (row0 + col < R)
 #pragma unroll
-      for (int hh = 0; hh < D / 64; ++hh)
+        for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float4v x;
+          for (int i = 0; i < 4; ++i) {
+            float4v x;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = A.o[ct][4 * hh + j][i];
-          *reinterpret_cast<float4v *>(&so[wt][col][64 * hh + 16 * g + 4 * i]) = x;
-        }
+            for (int j = 0; j < 4; ++j) x[j] = A.o[ct][4 * hh + j][i];
+            *reinterpret_cast<float4v *>(&so[wt][col][64 * hh + 16 * g + 4 * i]) = x;
+          }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < N * D; e += 256) {
-      const int col = e / D, d = e % D, row = row0 + col;
-      if (row >= R) break;
-      float m = sm[0][col], l = 0.f, o = 0.f;
+    for (int col = wave; col < N && row0 + col < R; col += WT) {
+      const int row = row0 + col;
+      const float mw = lane < WT ? sm[lane][col] : kNegInf;
+      float m = mw;
 #pragma unroll
-      for (int w = 1; w < WT; ++w) m = fmaxf(m, sm[w][col]);
+      for (int d = 1; d < WT; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+      const float f = mw == kNegInf ? 0.f : exp2f(mw - m);
+      float l = lane < WT ? f * sl[lane][col] : 0.f;
 #pragma unroll
-      for (int w = 0; w < WT; ++w) {
-        const float f = m == kNegInf ? 0.f : exp2f(sm[w][col] - m);
-        l += f * sl[w][col];
-        o += f * so[w][col][d];
+      for (int d = 1; d < WT; d <<= 1) l += __shfl_xor(l, d);
+      m = __shfl(m, 0);
+      l = __shfl(l, 0);
+      const int64_t part = ((int64_t)split * BH + bh) * R + row;
+      const int64_t at = out_at(a, b, h, row);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < WT; ++w) o += __shfl(f, w) * so[w][col][c * 64 + lane];
+        if (splits == 1)
+          store_out(a, at + c * 64 + lane, l == 0.f ? 0.f : o / l, F32);
+        else
+          ws.o[part * D + c * 64 + lane] = o;
       }
-      if (splits == 1)
-        store_out(a, out_at(a, b, h, row) + d, l == 0.f ? 0.f : o / l, F32);
-      else
-        ws.o[(((int64_t)split * BH + bh) * R + row) * D + d] = o;
-      if (d == 0 && ws.ml != nullptr)
-        ws.ml[((int64_t)split * BH + bh) * R + row] = make_float2(m, l);
+      if (lane == 0 && ws.ml != nullptr) ws.ml[part] = make_float2(m, l);
     }
   } else {
 #pragma unroll
@@ -525,8 +636,100 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a, int splits, i
   }
 }
 
-// log2 of a row's sum of exponentials over all splits; +inf for a row that
-// sees nothing, so that its probabilities come out as zero.
+constexpr int kMaxSplits = 64;  // one a lane where they are joined
+
+// Splits of one row over the lanes of a wave: each split's factor against the
+// row's largest reference (0 for lanes past them), the sum of exponentials, and
+// that reference.
+struct RowJoin {
+  float f, l, m;
+};
+__device__ __forceinline__ RowJoin join_row(const Ws &ws, int splits, int64_t stride, int64_t row,
+                                            int lane) {
+  const float2 x =
+      lane < splits ? ws.ml[lane * stride + row] : make_float2(kNegInf, 0.f);
+  RowJoin j;
+  j.m = x.x;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) j.m = fmaxf(j.m, __shfl_xor(j.m, d));
+  j.f = x.x == kNegInf ? 0.f : exp2f(x.x - j.m);
+  j.l = x.y * j.f;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) j.l += __shfl_xor(j.l, d);
+  return j;
+}
+// log2 of a row's sum of exponentials; +inf for a row that sees nothing, so
+// that its probabilities come out as zero.
+__device__ __forceinline__ float lse_of(const RowJoin &j) {
+  return j.m == kNegInf ? INFINITY : j.m + log2f(j.l);
+}
+
+// Joins the splits (blocks [0, join)), a wave a row, and adds the rows'
+// probabilities to the weights from the stored scores (the other blocks, 1024
+// tokens each).
+constexpr int kSumTokens = 1024;
+template <int D>
+__global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int join, bool f32,
+                                                   Ws ws) {
+  const int BH = a.c.B * a.c.H, R = a.n * a.G;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t rows = (int64_t)BH * R;
+  if ((int)blockIdx.x < join) {
+    const int64_t row = (int64_t)blockIdx.x * 4 + wave;
+    if (row >= rows) return;
+    const RowJoin j = join_row(ws, splits, rows, row, lane);
+    const int bh = (int)(row / R), r = (int)(row % R);
+    const int64_t at = out_at(a, bh / a.c.H, bh % a.c.H, r);
+    float o[D / 64] = {};
+    for (int s0 = 0; s0 < splits; s0 += 4) {  // four splits' reads in flight
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int s = min(s0 + k, splits - 1);
+        const float f = s0 + k < splits ? __shfl(j.f, s) : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          o[c] += f * ws.o[(s * rows + row) * D + c * 64 + lane];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      store_out(a, at + c * 64 + lane, j.l == 0.f ? 0.f : o[c] / j.l, f32);
+    return;
+  }
+  __shared__ float lse[32];
+  const int blk = blockIdx.x - join, bh = blk % BH;
+  const int t = blk / BH * kSumTokens + threadIdx.x * 4;
+  const int L = kv_len(a.c, bh / a.c.H);
+  if (blk / BH * kSumTokens >= L) return;
+  for (int r = wave; r < R; r += 4) {
+    const float e = lse_of(join_row(ws, splits, rows, (int64_t)bh * R + r, lane));
+    if (lane == 0) lse[r] = e;
+  }
+  __syncthreads();
+  if (t >= L) return;
+  float4v sum = {0.f, 0.f, 0.f, 0.f};
+  for (int r0 = 0; r0 < R; r0 += 4) {
+    float4v s[4];  // four rows' reads in flight
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      s[k] = *reinterpret_cast<const float4v *>(
+          ws.scores + ((int64_t)bh * R + min(r0 + k, R - 1)) * a.c.room() + t);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = min(r0 + k, R - 1);
+      // nothing is stored in tiles past the last token that a row sees
+      const int seen = r0 + k < R ? L - a.n + r / a.G : -1;
+      const float e = lse[r];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sum[i] += t + i > seen ? 0.f : __builtin_amdgcn_exp2f(s[k][i] - e);
+    }
+  }
+  float *w = a.weights + (int64_t)bh * a.c.room() + t;
+  for (int i = 0; i < 4 && t + i < L; ++i) w[i] += sum[i];
+}
+
+// The same of one row in every lane, for the few splits that calls with many rows have.
 __device__ __forceinline__ float row_lse(const Ws &ws, int splits, int64_t stride, int64_t row) {
   float m = kNegInf;
   for (int s = 0; s < splits; ++s) m = fmaxf(m, ws.ml[s * stride + row].x);
@@ -537,57 +740,6 @@ __device__ __forceinline__ float row_lse(const Ws &ws, int splits, int64_t strid
     l += x.y * exp2f(x.x - m);
   }
   return m + log2f(l);
-}
-
-// Joins the splits (blocks [0, join)), one thread a channel, and adds the
-// rows' probabilities to the weights from the stored scores (the other blocks,
-// 1024 tokens each).
-constexpr int kSumTokens = 1024;
-template <int D>
-__global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int join, bool f32,
-                                                   Ws ws) {
-  const int BH = a.c.B * a.c.H, R = a.n * a.G;
-  const int64_t rows = (int64_t)BH * R;
-  if ((int)blockIdx.x < join) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = e / D;
-    const int d = e % D;
-    if (row >= rows) return;
-    float m = kNegInf;
-    for (int s = 0; s < splits; ++s) m = fmaxf(m, ws.ml[s * rows + row].x);
-    float l = 0.f, o = 0.f;
-    if (m != kNegInf)
-      for (int s = 0; s < splits; ++s) {
-        const float2 x = ws.ml[s * rows + row];
-        const float f = exp2f(x.x - m);
-        l += f * x.y;
-        o += f * ws.o[(s * rows + row) * D + d];
-      }
-    const int bh = (int)(row / R), r = (int)(row % R);
-    store_out(a, out_at(a, bh / a.c.H, bh % a.c.H, r) + d, l == 0.f ? 0.f : o / l, f32);
-    return;
-  }
-  __shared__ float lse[32];
-  const int blk = blockIdx.x - join, bh = blk % BH;
-  const int t = blk / BH * kSumTokens + threadIdx.x * 4;
-  const int L = kv_len(a.c, bh / a.c.H);
-  if (blk / BH * kSumTokens >= L) return;
-  if ((int)threadIdx.x < R) lse[threadIdx.x] = row_lse(ws, splits, rows, (int64_t)bh * R + threadIdx.x);
-  __syncthreads();
-  if (t >= L) return;
-  float4v sum = {0.f, 0.f, 0.f, 0.f};
-  for (int r = 0; r < R; ++r) {
-    const int seen = L - a.n + r / a.G;
-    // tiles past the last token a row sees were not visited: nothing is stored
-    if (t / 32 * 32 > seen) continue;
-    const float4v s =
-        *reinterpret_cast<const float4v *>(ws.scores + ((int64_t)bh * R + r) * a.c.room() + t);
-    const float e = lse[r];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] += t + i > seen ? 0.f : exp2f(s[i] - e);
-  }
-  float *w = a.weights + (int64_t)bh * a.c.room() + t;
-  for (int i = 0; i < 4 && t + i < L; ++i) w[i] += sum[i];
 }
 
 // The weights of many rows: 32 tokens a workgroup, whose waves take turns over
@@ -604,9 +756,10 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
   const int b = bh / a.c.H, h = bh % a.c.H;
   const int L = kv_len(a.c, b);
   if (t >= L) return;
-  Tile<D> T[2];
-  load_tile<D>(T[0], a.c, b, h, t, lane);
-  load_tile<D>(T[1], a.c, b, h, t + 16 < L ? t + 16 : t, lane);
+  Tiles<D> T;
+  const Where at = where(a.c, b, h, t, L);
+  load_k(T, a.c, at, lane);
+  load_m(T, a.c, at, lane);
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.f;
@@ -621,13 +774,13 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float4v S[1];
-      tile_scores<D, 1, F32>(S, T[s], Q);
+      tile_scores<D, 1, F32>(S, T, s, Q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const Factors f = factors<D>(T[s], i, a.scale_log2);
-        const float x = S[0][i] * f.ks + Q.sum[0] * f.kz;
-        sum[4 * s + i] +=
-            t + 16 * s + 4 * g + i > last ? 0.f : __builtin_amdgcn_exp2f(x - lse);
+        const float x = raw_score(S[0][i], Q.sum[0], T.m[s][2 * i]);
+        sum[4 * s + i] += t + 16 * s + 4 * g + i > last
+                              ? 0.f
+                              : __builtin_amdgcn_exp2f(fmaf(x, a.unit, -lse));
       }
     }
   }
@@ -645,39 +798,49 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
   }
 }
 
-template <int D, int CT, int WT, bool F32>
+// Tiles of rows that a wave holds when the waves have rows of their own.
+constexpr int many_rows_ct(int D) { return D <= 128 ? 2 : 1; }
+// Waves of a wide workgroup: what its joining area in shared memory and its
+// registers allow.
+constexpr int wide_waves(int D, bool f32) { return D == 256 || f32 ? 8 : 16; }
+
+template <int D, int CT, int WT, int WR, bool F32>
 void launch_attend(const AttendArgs &a, const AttendPlan &p, const Ws &ws, hipStream_t s) {
   const unsigned grid = (unsigned)a.c.B * a.c.H * p.splits * p.row_blocks;
+  const int threads = 64 * WT * WR;
   if constexpr (WT > 1) {
     if (p.scores) {
-      attend_kernel<D, CT, WT, F32, true><<<grid, 256, 0, s>>>(a, p.splits, p.row_blocks, ws);
+      attend_kernel<D, CT, WT, WR, F32, true>
+          <<<grid, threads, 0, s>>>(a, p.splits, p.row_blocks, ws);
       return;
     }
   }
-  attend_kernel<D, CT, WT, F32, false><<<grid, 256, 0, s>>>(a, p.splits, p.row_blocks, ws);
+  attend_kernel<D, CT, WT, WR, F32, false>
+      <<<grid, threads, 0, s>>>(a, p.splits, p.row_blocks, ws);
 }
 
 template <int D, bool F32>
 hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
   const int BH = a.c.B * a.c.H, R = a.n * a.G, room = a.c.room();
-  const AttendPlan p = attend_plan(a.c.B, a.c.H, D, room, a.n, a.G * a.c.H, a.weights != nullptr);
+  const AttendPlan p =
+      attend_plan(a.c.B, a.c.H, D, room, a.n, a.G * a.c.H, F32, a.weights != nullptr);
   char *w = static_cast<char *>(a.ws);
   Ws ws{};
   if (p.splits > 1 || a.weights != nullptr) ws.ml = reinterpret_cast<float2 *>(w);
   if (p.splits > 1) ws.o = reinterpret_cast<float *>(w + p.off_o);
   if (p.scores) ws.scores = reinterpret_cast<float *>(w + p.off_scores);
-  if (p.wt == 4) {
-    if (p.ct == 1)
-      launch_attend<D, 1, 4, F32>(a, p, ws, s);
-    else if constexpr (D <= 128)
-      launch_attend<D, 2, 4, F32>(a, p, ws, s);
-  } else {
-    launch_attend<D, D <= 128 ? 2 : 1, 1, F32>(a, p, ws, s);
-  }
+  if (p.wt == 1)
+    launch_attend<D, many_rows_ct(D), 1, 4, F32>(a, p, ws, s);
+  else if (p.ct == 2) {
+    if constexpr (D <= 128) launch_attend<D, 2, 4, 1, F32>(a, p, ws, s);
+  } else if (p.wt == 4)
+    launch_attend<D, 1, 4, 1, F32>(a, p, ws, s);
+  else
+    launch_attend<D, 1, wide_waves(D, F32), 1, F32>(a, p, ws, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.splits > 1 || p.scores) {
-    const int join = p.splits > 1 ? (int)(((int64_t)BH * R * D + 255) / 256) : 0;
+    const int join = p.splits > 1 ? (int)(((int64_t)BH * R + 3) / 4) : 0;
     const int sums = p.scores ? BH * ((room + kSumTokens - 1) / kSumTokens) : 0;
     join_kernel<D><<<join + sums, 256, 0, s>>>(a, p.splits, join, F32, ws);
     e = hipGetLastError();
@@ -692,14 +855,16 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
 
 }  // namespace
 
-AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool weights) {
+AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool f32,
+                       bool weights) {
   AttendPlan p{};
   const int64_t R = (int64_t)n * (q_heads / H), BH = (int64_t)B * H;
   // Up to 16 rows (32 up to 128 channels) a workgroup holds them all and its
   // waves share the tokens; more rows are spread over the waves.
   p.ct = D <= 128 && R > 16 ? 2 : 1;
   p.wt = R <= 16 * p.ct ? 4 : 1;
-  const int block = p.ct * 16 * (4 / p.wt);
+  if (p.wt == 1) p.ct = many_rows_ct(D);
+  const int block = p.ct * 16 * (p.wt == 1 ? 4 : 1);
   p.row_blocks = (int)((R + block - 1) / block);
   const int64_t units = BH * p.row_blocks;
   // Enough workgroups for 256 compute units, none with less than one step of
@@ -708,8 +873,16 @@ AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool w
   int64_t splits = (want + units - 1) / units;
   const int64_t most = (room + least - 1) / least;
   splits = splits > most ? most : splits;
+  splits = splits > kMaxSplits ? kMaxSplits : splits;
   p.splits = (int)(splits < 1 ? 1 : splits);
-  p.scores = weights && p.wt == 4;
+  // Short caches: one wide workgroup a head, of up to 4 steps a wave, rather
+  // than splits and a second launch that joins them.
+  const int wide = wide_waves(D, f32);
+  if (p.wt == 4 && p.ct == 1 && p.splits > 1 && room <= wide * 32 * 4) {
+    p.wt = wide;
+    p.splits = 1;
+  }
+  p.scores = weights && p.wt != 1;
   const size_t rows = (size_t)(BH * R);
   size_t at = 0;
   if (p.splits > 1 || weights) at += rows * p.splits * sizeof(float2);
@@ -723,7 +896,13 @@ AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool w
   return p;
 }
 
-hipError_t launch_kv_attend(const AttendArgs &a, int D, bcq_dtype dt, hipStream_t s) {
+hipError_t launch_kv_attend(const AttendArgs &call, float scale, int D, bcq_dtype dt,
+                            hipStream_t s) {
+  // The scores' unit is kept positive, so that -inf stays a hidden token's score
+  // whatever the scale: a negative one turns the queries, a zero becomes tiny.
+  AttendArgs a = call;
+  a.negate = scale < 0.f;
+  a.unit = fmaxf(fabsf(scale) * 1.44269504088896340736f * kCodeScale, 1e-30f);
   if (dt == BCQ_F32)
     return D == 64    ? launch_dim<64, true>(a, s)
            : D == 128 ? launch_dim<128, true>(a, s)

@@ -99,7 +99,9 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k
     lo = nan_min(lo, __shfl_xor(lo, d));
     hi = nan_max(hi, __shfl_xor(hi, d));
   }
-  const _Float16 zh = (_Float16)lo, sh = (_Float16)((hi - lo) * (1.f / 15.f));
+  float step = (hi - lo) * (1.f / 15.f);
+  asm volatile("" : "+v"(step));  // rounded to fp32 first: one instruction could do both at once
+  const _Float16 zh = (_Float16)lo, sh = (_Float16)step;
   const float zero = (float)zh, scale = (float)sh;
   uint32_t word = 0;
 #pragma unroll
@@ -206,8 +208,7 @@ __device__ __forceinline__ uint32_t order_of(float w, bool late) {
 }
 
 constexpr int kEvictThreads = 1024, kEvictWaves = kEvictThreads / 64;
-constexpr int kCopies = 16;       // of the histogram, so that lanes rarely meet in a counter
-constexpr int kEvictKeys = 32768;  // slots whose orders shared memory holds
+constexpr int kCopies = 16;  // of the histogram, so that lanes rarely meet in a counter
 
 struct EvictArgs {
   KvView c;
@@ -222,57 +223,125 @@ struct EvictArgs {
   int most;
 };
 
-// One workgroup a row.  A radix select over the orders, eight bits a pass,
-// finds the last one kept; then the waves, each with its own stretch of slots,
-// count and lay out what moves, in slot order.
-template <bool HELD>
+// Set bits of a ballot below the lane.
+__device__ __forceinline__ uint32_t below(uint64_t ballot) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(ballot >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)ballot, 0));
+}
+
+// One workgroup a row.  A wave has 256 Q slots in a row, a thread the orders of 4 Q
+// of them in registers, slot 256 q + 4 lane + e of the wave's, so that reads are
+// wide and coalesced; rows with room for more than the workgroup holds (ONCE is
+// false) go through all steps in rounds, which read weights and positions again.
+// A radix select over the orders, eight bits a pass, finds the last one kept and
+// ends early where a whole bin is; ballots then number what moves in slot order.
+template <int Q, bool ONCE>
 __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
-  extern __shared__ uint32_t keys[];
+  constexpr int kRound = 4 * Q * kEvictThreads;
   __shared__ uint32_t hist[256 * kCopies];
   __shared__ uint32_t total[256];
-  __shared__ int tmp[kEvictWaves], base[3][kEvictWaves + 1];
-  __shared__ uint32_t picked, above;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ int tmp[kEvictWaves];
+  __shared__ uint32_t sums[3][kEvictWaves];
+  __shared__ uint32_t picked, above, inside;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = blockIdx.x, b = row / a.c.H;
   const int64_t at = (int64_t)row * a.c.room();
   const int L = kv_len(a.c, b), m = min(L, a.keep);
+  const int end = ONCE ? 1 : L;  // of the rounds' first slots
   const float *w = a.weights + at;
   const int32_t *pos = a.pos + at;
-  if (L <= a.keep) {
-    for (int s = tid; s < L; s += kEvictThreads) {
-      a.weights_out[at + s] = w[s];
-      a.pos_out[at + s] = pos[s];
-    }
-    if (tid == 0) a.count[row] = 0;
-    return;
-  }
+  const int first = wave * 256 * Q + lane * 4;  // of the thread's slots, in a round
+
+  // Rows start at multiples of 16 slots and end at one, so a read of 4 from a
+  // multiple of 4 below L stays in its row.
   int newest = INT32_MIN;
-  for (int s = tid; s < L; s += kEvictThreads) newest = max(newest, pos[s]);
+  for (int s0 = first; s0 < end + first; s0 += kRound) {
+    int4 v[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (s0 + 256 * q < L) v[q] = *reinterpret_cast<const int4 *>(pos + s0 + 256 * q);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int s = s0 + 256 * q;
+      if (s < L) newest = max(newest, v[q].x);
+      if (s + 1 < L) newest = max(newest, v[q].y);
+      if (s + 2 < L) newest = max(newest, v[q].z);
+      if (s + 3 < L) newest = max(newest, v[q].w);
+    }
+  }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
   if (lane == 0) tmp[wave] = newest;
+  for (int i = tid; i < 256 * kCopies; i += kEvictThreads) hist[i] = 0;
   __syncthreads();
   for (int i = 0; i < kEvictWaves; ++i) newest = max(newest, tmp[i]);
   const int64_t late_from = (int64_t)newest - a.recent;
-  auto key = [&](int s) { return HELD ? keys[s] : order_of(w[s], pos[s] > late_from); };
-  if (HELD)
-    for (int s = tid; s < L; s += kEvictThreads) keys[s] = order_of(w[s], pos[s] > late_from);
+
+  // The orders of the round whose slots start at s0 for this thread.  On the
+  // way what is in front goes to the output; what is evicted of it is
+  // overwritten by the moves.
+  uint32_t key[Q][4];
+  auto orders = [&](int s0, bool write) {
+    float4 x[Q];
+    int4 y[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (s0 + 256 * q < L) {
+        x[q] = *reinterpret_cast<const float4 *>(w + s0 + 256 * q);
+        y[q] = *reinterpret_cast<const int4 *>(pos + s0 + 256 * q);
+      }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float xs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+      const int32_t ys[4] = {y[q].x, y[q].y, y[q].z, y[q].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int s = s0 + 256 * q + e;
+        key[q][e] = order_of(xs[e], ys[e] > late_from);
+        if (write && s < m) {
+          a.weights_out[at + s] = xs[e];
+          a.pos_out[at + s] = ys[e];
+        }
+      }
+    }
+  };
+  const bool apart = a.weights_out != a.weights || a.pos_out != a.pos;
+  if (ONCE)
+    orders(first, apart);
+  else if (apart)
+    for (int s0 = first; s0 < end + first; s0 += kRound) orders(s0, true);
+  if (L <= a.keep) {
+    if (tid == 0) a.count[row] = 0;
+    return;
+  }
 
   uint32_t prefix = 0;
   int left = m;  // still to be taken among the slots whose order starts with prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * kCopies; i += kEvictThreads) hist[i] = 0;
-    __syncthreads();
-    for (int s = tid; s < L; s += kEvictThreads) {
-      const uint32_t k = key(s);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+  int shift = 24;
+  for (;; shift -= 8) {
+    for (int s0 = first; s0 < end + first; s0 += kRound) {
+      if (!ONCE) orders(s0, false);
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t k = key[q][e];
+          if (s0 + 256 * q + e < L &&
+              (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))))
+            atomicAdd(&hist[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+        }
     }
     __syncthreads();
-    if (tid < 256) {
-      uint32_t t = 0;
-      for (int i = 0; i < kCopies; ++i) t += hist[tid * kCopies + i];
-      total[tid] = t;
+    {
+      // 4 threads a bin, which also clear the counters for the next pass
+      uint4 *h = reinterpret_cast<uint4 *>(hist) + tid;
+      const uint4 x = *h;
+      uint32_t t = x.x + x.y + x.z + x.w;
+      *h = make_uint4(0, 0, 0, 0);
+      t += __shfl_xor(t, 1);
+      t += __shfl_xor(t, 2);
+      if ((tid & 3) == 0) total[tid >> 2] = t;
     }
     __syncthreads();
     if (wave == 0) {
@@ -290,6 +359,7 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
         if (over < (uint32_t)left && over + t[i] >= (uint32_t)left) {
           picked = lane * 4 + i;
           above = over;
+          inside = t[i];
         }
         over += t[i];
       }
@@ -297,66 +367,97 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
     __syncthreads();
     prefix |= picked << shift;
     left -= (int)above;
-    __syncthreads();
+    if (shift == 0 || (int)inside == left) break;
   }
-  // kept: every order above prefix, and the first `left` slots at it
-  const int span = (L + kEvictThreads - 1) / kEvictThreads * 64;  // slots of a wave
-  const int s0 = wave * span, s1 = min(L, s0 + span);
-  int ties = 0;
-  for (int s = s0; s < s1; s += 64)
-    ties += __popcll(__ballot(s + lane < s1 && key(s + lane) == prefix));
-  if (lane == 0) base[0][wave] = ties;
-  __syncthreads();
-  int tie0 = 0;
-  for (int i = 0; i < wave; ++i) tie0 += base[0][i];
-  const uint64_t before = (1ull << lane) - 1;
-  auto walk = [&](auto &&visit) {
-    int tie = tie0;
-    for (int s = s0; s < s1; s += 64) {
-      const bool in = s + lane < s1;
-      const uint32_t k = in ? key(s + lane) : 0;
-      const uint64_t eq = __ballot(in && k == prefix);
-      const bool kept = in && (k > prefix || (k == prefix && tie + __popcll(eq & before) < left));
-      tie += __popcll(eq);
-      const int slot = s + lane;
-      visit(slot, kept, __ballot(in && slot < m && !kept), __ballot(slot >= m && kept));
-    }
-  };
-  int holes = 0, fills = 0;
-  walk([&](int, bool, uint64_t hole, uint64_t fill) {
-    holes += __popcll(hole);
-    fills += __popcll(fill);
-  });
-  if (lane == 0) {
-    base[1][wave] = holes;
-    base[2][wave] = fills;
-  }
-  __syncthreads();
-  int hole_at = 0, fill_at = 0, moves = 0;
-  for (int i = 0; i < kEvictWaves; ++i) {
-    if (i < wave) {
-      hole_at += base[1][i];
-      fill_at += base[2][i];
-    }
-    moves += base[1][i];
-  }
+
+  // kept: every order above prefix's leading bits, and the first `left` slots at them
+  const uint32_t edge = prefix >> shift;
   int2 *mv = a.moves + (int64_t)row * a.most;
-  walk([&](int slot, bool kept, uint64_t hole, uint64_t fill) {
-    const uint64_t bit = 1ull << lane;
-    if (hole & bit) mv[hole_at + __popcll(hole & before)].y = slot;
-    if (fill & bit) mv[fill_at + __popcll(fill & before)].x = slot;
-    if (kept && slot < m) {
-      a.weights_out[at + slot] = w[slot];
-      a.pos_out[at + slot] = pos[slot];
+  uint32_t ties = 0, holes = 0, fills = 0;  // before this round
+  for (int s0 = first; s0 < end + first; s0 += kRound) {
+    if (!ONCE) orders(s0, false);
+    uint32_t n = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        n += __popcll(__ballot(s0 + 256 * q + e < L && (key[q][e] >> shift) == edge));
+    if (lane == 0) sums[0][wave] = n;
+    __syncthreads();
+    uint32_t tie = ties;
+    for (int i = 0; i < kEvictWaves; ++i) {
+      const uint32_t x = sums[0][i];
+      tie += i < wave ? x : 0;
+      ties += x;
     }
-    hole_at += __popcll(hole);
-    fill_at += __popcll(fill);
-  });
-  if (tid == 0) a.count[row] = moves;
+    uint32_t hole = 0, fill = 0;  // 4 bits a q
+    uint32_t n_holes = 0, n_fills = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      uint64_t eq[4];
+      uint32_t before = tie;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        eq[e] = __ballot(s0 + 256 * q + e < L && (key[q][e] >> shift) == edge);
+        before += below(eq[e]);
+        tie += __popcll(eq[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int s = s0 + 256 * q + e;
+        const uint32_t k = key[q][e] >> shift;
+        const bool same = k == edge;
+        const bool kept = s < L && (k > edge || (same && before < (uint32_t)left));
+        before += s < L && same;
+        const bool ho = s < m && !kept, fi = s >= m && kept;
+        hole |= (uint32_t)ho << (4 * q + e);
+        fill |= (uint32_t)fi << (4 * q + e);
+        n_holes += __popcll(__ballot(ho));
+        n_fills += __popcll(__ballot(fi));
+      }
+    }
+    if (lane == 0) {
+      sums[1][wave] = n_holes;
+      sums[2][wave] = n_fills;
+    }
+    __syncthreads();
+    uint32_t at_hole = holes, at_fill = fills;
+    for (int i = 0; i < kEvictWaves; ++i) {
+      const uint32_t x = sums[1][i], y = sums[2][i];
+      at_hole += i < wave ? x : 0;
+      at_fill += i < wave ? y : 0;
+      holes += x;
+      fills += y;
+    }
+    if (n_holes + n_fills > 0) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        uint32_t h = at_hole, f = at_fill;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t hb = __ballot(hole >> (4 * q + e) & 1);
+          const uint64_t fb = __ballot(fill >> (4 * q + e) & 1);
+          h += below(hb);
+          f += below(fb);
+          at_hole += __popcll(hb);
+          at_fill += __popcll(fb);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = s0 + 256 * q + e;
+          if (hole >> (4 * q + e) & 1) mv[h++].y = s;
+          if (fill >> (4 * q + e) & 1) mv[f++].x = s;
+        }
+      }
+    }
+  }
+  if (tid == 0) a.count[row] = (int)holes;
 }
 
-// D/4 lanes a move.  A stride of the grid over the row's moves, so that the
-// host need not know their number.
+// D/4 lanes a group of moves: four in a row, whose loads are all in flight before
+// the first is stored (they go to neighbouring slots, mostly).  A stride of the
+// grid over the row's moves, so that the host need not know their number.
+constexpr int kMoves = 4;
 template <int D>
 __global__ __launch_bounds__(256) void move_kernel(EvictArgs a) {
   constexpr int L = D / 4;
@@ -369,21 +470,44 @@ __global__ __launch_bounds__(256) void move_kernel(EvictArgs a) {
   }
   const int64_t at = (int64_t)row * a.c.room();
   const int count = a.count[row];
-  for (int k = blockIdx.y * (256 / L) + threadIdx.x / L; k < count; k += gridDim.y * (256 / L)) {
-    const int2 mv = a.moves[(int64_t)row * a.most + k];
-    const int64_t from = kv_token(a.c, b, h, mv.x), to = kv_token(a.c, b, h, mv.y);
-    if (from >= 0 && to >= 0) {
-      *reinterpret_cast<uint16_t *>(a.c.k + k_byte<D>(to, i)) =
-          *reinterpret_cast<const uint16_t *>(a.c.k + k_byte<D>(from, i));
-      *reinterpret_cast<uint16_t *>(a.c.v + v_byte<D>(to, i)) =
-          *reinterpret_cast<const uint16_t *>(a.c.v + v_byte<D>(from, i));
-      if (i == 0)
-        *reinterpret_cast<uint2 *>(a.c.scales + to * 4) =
-            *reinterpret_cast<const uint2 *>(a.c.scales + from * 4);
+  const int2 *moves = a.moves + (int64_t)row * a.most;
+  const int group = blockIdx.y * (256 / L) + threadIdx.x / L;
+  for (int k0 = group * kMoves; k0 < count; k0 += gridDim.y * (256 / L) * kMoves) {
+    int2 mv[kMoves];
+    int64_t from[kMoves], to[kMoves];
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k) mv[k] = moves[min(k0 + k, count - 1)];
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k) {
+      from[k] = kv_token(a.c, b, h, mv[k].x);
+      to[k] = kv_token(a.c, b, h, mv[k].y);
+      if (to[k] < 0) from[k] = -1;
     }
-    if (i == 0) {
-      a.weights_out[at + mv.y] = a.weights[at + mv.x];
-      a.pos_out[at + mv.y] = a.pos[at + mv.x];
+    uint16_t ck[kMoves], cv[kMoves];
+    uint2 cs[kMoves];
+    float cw[kMoves];
+    int32_t cp[kMoves];
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k) {
+      const int64_t t = max(from[k], (int64_t)0);
+      ck[k] = *reinterpret_cast<const uint16_t *>(a.c.k + k_byte<D>(t, i));
+      cv[k] = *reinterpret_cast<const uint16_t *>(a.c.v + v_byte<D>(t, i));
+      cs[k] = *reinterpret_cast<const uint2 *>(a.c.scales + t * 4);
+      cw[k] = a.weights[at + mv[k].x];
+      cp[k] = a.pos[at + mv[k].x];
+    }
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k) {
+      if (k0 + k >= count) break;
+      if (from[k] >= 0) {
+        *reinterpret_cast<uint16_t *>(a.c.k + k_byte<D>(to[k], i)) = ck[k];
+        *reinterpret_cast<uint16_t *>(a.c.v + v_byte<D>(to[k], i)) = cv[k];
+        if (i == 0) *reinterpret_cast<uint2 *>(a.c.scales + to[k] * 4) = cs[k];
+      }
+      if (i == 0) {
+        a.weights_out[at + mv[k].y] = cw[k];
+        a.pos_out[at + mv[k].y] = cp[k];
+      }
     }
   }
 }
@@ -429,15 +553,19 @@ hipError_t launch_kv_evict(const KvView &c, int D, int keep, int recent, const f
   a.most = keep < room ? most_moves(room, keep) : 0;
   a.moves = static_cast<int2 *>(ws);
   a.count = reinterpret_cast<int32_t *>(a.moves + (size_t)BH * a.most);
-  if (room <= kEvictKeys)
-    select_kernel<true><<<BH, kEvictThreads, (size_t)room * 4, s>>>(a);
+  if (room <= 4 * kEvictThreads)
+    select_kernel<1, true><<<BH, kEvictThreads, 0, s>>>(a);
+  else if (room <= 32 * kEvictThreads)
+    select_kernel<8, true><<<BH, kEvictThreads, 0, s>>>(a);
   else
-    select_kernel<false><<<BH, kEvictThreads, 0, s>>>(a);
+    select_kernel<4, false><<<BH, kEvictThreads, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int per = 256 / (D / 4);
+  const int per = 256 / (D / 4) * kMoves;
+  // about 4096 workgroups in all: enough to fill the card several times over
+  const int most_chunks = BH >= 4096 ? 1 : 4096 / BH;
   int chunks = (a.most + per - 1) / per;
-  chunks = chunks < 1 ? 1 : (chunks > 64 ? 64 : chunks);
+  chunks = chunks < 1 ? 1 : (chunks > most_chunks ? most_chunks : chunks);
   const dim3 grid(BH, chunks);
   if (D == 64)
     move_kernel<64><<<grid, 256, 0, s>>>(a);

@@ -200,9 +200,14 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
 size_t bcq_kv_workspace_bytes(const bcq_kv_cache *cache, int32_t n, int32_t q_heads,
                               int32_t with_weights) {
   if (check_attend(cache, n, q_heads) != BCQ_OK || n == 0) return 0;
-  return bcq::attend_plan(cache->batch, cache->heads, cache->head_dim, room(cache), n, q_heads,
-                          with_weights != 0)
-      .bytes;
+  size_t most = 0;  // of the two types
+  for (int f32 = 0; f32 < 2; ++f32) {
+    const size_t b = bcq::attend_plan(cache->batch, cache->heads, cache->head_dim, room(cache), n,
+                                      q_heads, f32 != 0, with_weights != 0)
+                         .bytes;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 bcq_status bcq_kv_attend(const bcq_kv_cache *cache, const void *Q, int32_t n, int32_t q_heads,
@@ -227,10 +232,11 @@ bcq_status bcq_kv_attend(const bcq_kv_cache *cache, const void *Q, int32_t n, in
   a.os = {o_batch, o_token, o_head};
   a.n = n;
   a.G = q_heads / cache->heads;
-  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.q_wide = aligned(Q, 16) && (q_batch * es) % 16 == 0 && (q_token * es) % 16 == 0 &&
+             (q_head * es) % 16 == 0;
   a.weights = weights;
   a.ws = workspace;
-  return hip_status(bcq::launch_kv_attend(a, cache->head_dim, dtype, stream));
+  return hip_status(bcq::launch_kv_attend(a, scale, cache->head_dim, dtype, stream));
 }
 
 size_t bcq_kv_evict_workspace_bytes(const bcq_kv_cache *cache, int32_t keep) {

@@ -64,7 +64,7 @@ struct AttendPlan {
   bool scores;     // the weights are summed from stored scores, not from recomputed ones
   size_t off_o, off_scores, bytes;  // workspace: (m, l) pairs, then outputs, then scores
 };
-AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool weights);
+AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool f32, bool weights);
 
 struct AttendArgs {
   KvView c;
@@ -72,11 +72,15 @@ struct AttendArgs {
   void *out;
   KvStrides qs, os;
   int n, G;          // queries of a sequence; query heads of a cached head
-  float scale_log2;  // softmax scale times log2(e)
+  bool q_wide;       // 8 channels of q can be read at once
+  bool negate;       // the softmax's scale is negative
+  float unit;        // its size times log2(e), for scores in the unit 2^-24
   float *weights;    // [B][H][room] or null
   void *ws;
 };
-hipError_t launch_kv_attend(const AttendArgs &a, int D, bcq_dtype dt, hipStream_t s);
+// negate and unit of `call` are filled in from the softmax's scale.
+hipError_t launch_kv_attend(const AttendArgs &call, float scale, int D, bcq_dtype dt,
+                            hipStream_t s);
 
 size_t evict_workspace_bytes(int B, int H, int room, int keep);
 hipError_t launch_kv_evict(const KvView &c, int D, int keep, int recent, const float *weights,

@@ -6,7 +6,6 @@ key/value cache (append, read, attend, evict).  Names and semantics are those of
 from __future__ import annotations
 
 import ctypes
-import math
 
 BCQ_KV_MAX_TOKENS = 1 << 24
 
@@ -42,29 +41,42 @@ SIGNATURES = {
 EXPORTS = tuple(SIGNATURES)
 
 
-def _pkg():
+# The loaded library and torch, bound at the first call: these operators are called once a layer
+# and token, so a call does no more than read its tensors' descriptions and pass them on.
+_lib = None
+torch = None
+
+
+def _bind():
+    global _lib, torch
+    import torch as _torch
+
     import binary_coded_precision_amd as pkg
 
-    return pkg
+    torch = _torch
+    _lib = pkg.load()
+    return _lib
+
+
+def _fail(fn: str, status: int):
+    import binary_coded_precision_amd as pkg
+
+    raise pkg.BCQError(fn, status)
 
 
 def _pad16(n: int) -> int:
     return (n + 15) // 16 * 16
 
 
-def _handle(t, stream) -> int:
+def _raw(t, stream) -> int:
     """The raw stream a call goes to: the given one, or the current one of t's device."""
-    import torch
-
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _workspace(n_bytes: int, device, stream):
     """A workspace of n_bytes for a call on `stream`; the allocator learns of its use there."""
-    import torch
-
     w = torch.empty(max(n_bytes, 1), dtype=torch.uint8, device=device)
     if stream is not None:
         w.record_stream(stream)
@@ -73,34 +85,35 @@ def _workspace(n_bytes: int, device, stream):
 
 def _float(name: str, t) -> int:
     """The dtype code of a device tensor of fp16 or fp32."""
-    import torch
-
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    if t.dtype is torch.float16:
+    d = t.dtype
+    if d is torch.float16:
         return 1
-    if t.dtype is torch.float32:
+    if d is torch.float32:
         return 2
-    raise TypeError("%s must be float16 or float32, got %s" % (name, t.dtype))
+    raise TypeError("%s must be float16 or float32, got %s" % (name, d))
 
 
-def _plain(name: str, t, dtype, shape) -> None:
-    """A contiguous device tensor of this dtype and shape."""
-    if not t.is_cuda or t.dtype is not dtype or tuple(t.shape) != tuple(shape) or \
-            not t.is_contiguous():
+def _plain(name: str, t, dtype, shape) -> int:
+    """The address of a contiguous device tensor of this dtype and shape."""
+    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s device tensor of shape %s, got %s of %s" %
                          (name, dtype, tuple(shape), tuple(t.shape), t.dtype))
+    return t.data_ptr()
 
 
 def _rows(name: str, t, rows: int, cols: int, read: int) -> int:
     """The leading dimension of a [rows][cols] matrix with unit inner stride whose every row
     can be read up to column `read`."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError("%s must be %d x %d, got %s" % (name, rows, cols, tuple(t.shape)))
-    if cols > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError("%s must have unit inner stride" % name)
-    ld = t.stride(0) if rows > 1 else max(t.stride(0), read)
-    if rows and read > cols:
+    if rows < 2 and ld < read:
+        ld = read
+    if read > cols and rows:
         room = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
         if (rows - 1) * ld + read > room:
             raise ValueError("%s: the last row must be readable up to column %d" % (name, read))
@@ -111,7 +124,7 @@ def _rows(name: str, t, rows: int, cols: int, read: int) -> int:
 
 
 def bcq_int_workspace_bytes(T: int, M: int, K: int) -> int:
-    return int(_pkg().load().bcq_int_workspace_bytes(T, M, K))
+    return int((_lib or _bind()).bcq_int_workspace_bytes(T, M, K))
 
 
 def new_int_workspace(T: int, M: int, K: int, device="cuda"):
@@ -125,9 +138,7 @@ def bcq_int_quantize(X, codes=None, scales=None, stream=None):
 
     Returns ``(codes, scales)``: int8 [rows][K] (a view of rows padded to 16 bytes with zeros)
     and fp32 [rows], allocated unless given."""
-    import torch
-
-    pkg = _pkg()
+    lib = _lib or _bind()
     dt = _float("X", X)
     rows, K = X.shape
     ldx = _rows("X", X, rows, K, K)
@@ -137,60 +148,53 @@ def bcq_int_quantize(X, codes=None, scales=None, stream=None):
         scales = torch.empty(rows, dtype=torch.float32, device=X.device)
     if codes.dtype is not torch.int8 or not codes.is_cuda:
         raise ValueError("codes must be an int8 device tensor")
-    ldc = _rows("codes", codes, rows, K, _pad16(K))
-    _plain("scales", scales, torch.float32, (rows,))
-    pkg._check("bcq_int_quantize",
-               pkg.load().bcq_int_quantize(X.data_ptr(), dt, rows, K, ldx, codes.data_ptr(), ldc,
-                                           scales.data_ptr(), _handle(X, stream)))
+    if rows == 1:
+        ldx = _pad16(ldx)  # a single row has no next one to be aligned with
+    r = lib.bcq_int_quantize(X.data_ptr(), dt, rows, K, ldx, codes.data_ptr(),
+                             _rows("codes", codes, rows, K, _pad16(K)),
+                             _plain("scales", scales, torch.float32, (rows,)), _raw(X, stream))
+    if r:
+        _fail("bcq_int_quantize", r)
     return codes, scales
 
 
 def _product(W, w_scales, Y, T: int, bias):
-    """Checks what the two products share; (M, K, ldw, ldy, dtype, bias pointer)."""
-    import torch
-
-    M, K = W.shape
+    """Checks what the two products share; (M, K, ldw, ldy, dtype, scales', bias' address)."""
     if W.dtype is not torch.int8 or not W.is_cuda:
         raise ValueError("W must be an int8 device tensor")
-    dt = _float("Y", Y)
-    ldw = _rows("W", W, M, K, _pad16(K))
-    ldy = _rows("Y", Y, T, M, M)
-    _plain("w_scales", w_scales, torch.float32, (M,))
-    if bias is not None:
-        _plain("bias", bias, Y.dtype, (M,))
-    return M, K, ldw, ldy, dt, 0 if bias is None else bias.data_ptr()
+    M, K = W.shape
+    return (M, K, _rows("W", W, M, K, _pad16(K)), _rows("Y", Y, T, M, M), _float("Y", Y),
+            _plain("w_scales", w_scales, torch.float32, (M,)),
+            0 if bias is None else _plain("bias", bias, Y.dtype, (M,)))
 
 
 def bcq_int_gemm(A, a_scales, W, w_scales, Y, bias=None, workspace=None, stream=None) -> None:
     """``Y[t][m] = (A[t] . W[m]) * (a_scales[t] * w_scales[m]) + bias[m]`` from 8-bit codes as
     :func:`bcq_int_quantize` returns them.  ``workspace`` as in :func:`bcq_int_linear`."""
-    import torch
-
-    pkg = _pkg()
+    lib = _lib or _bind()
     T = A.shape[0]
-    M, K, ldw, ldy, dt, bp = _product(W, w_scales, Y, T, bias)
+    M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias)
     if A.dtype is not torch.int8 or not A.is_cuda:
         raise ValueError("A must be an int8 device tensor")
     lda = _rows("A", A, T, K, _pad16(K))
-    _plain("a_scales", a_scales, torch.float32, (T,))
     if workspace is None:
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
-    pkg._check("bcq_int_gemm",
-               pkg.load().bcq_int_gemm(A.data_ptr(), a_scales.data_ptr(), T, lda, W.data_ptr(),
-                                       w_scales.data_ptr(), M, K, ldw, bp, Y.data_ptr(), ldy, dt,
-                                       workspace.data_ptr(), workspace.nbytes,
-                                       _handle(W, stream)))
+    r = lib.bcq_int_gemm(A.data_ptr(), _plain("a_scales", a_scales, torch.float32, (T,)), T, lda,
+                         W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(), ldy, dt,
+                         workspace.data_ptr(), workspace.nbytes, _raw(W, stream))
+    if r:
+        _fail("bcq_int_gemm", r)
 
 
 def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) -> None:
-    """``Y = X W^T`` with the tokens ``X`` [T][K] rounded to 8 bits on the way and ``W`` [M][K]
-    held in 8 bits with the scales ``w_scales`` [M] (see ``include/bcq.h``).
+    """``Y = X W^T + bias`` with the tokens ``X`` [T][K] rounded to 8 bits on the way and ``W``
+    [M][K] held in 8 bits with the scales ``w_scales`` [M] (see ``include/bcq.h``).
 
     ``workspace=None`` allocates one through torch; :func:`new_int_workspace` keeps that out of
     a hot loop."""
-    pkg = _pkg()
+    lib = _lib or _bind()
     T = X.shape[0]
-    M, K, ldw, ldy, dt, bp = _product(W, w_scales, Y, T, bias)
+    M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias)
     if X.dtype is not Y.dtype or not X.is_cuda:
         raise ValueError("X and Y must be device tensors of one dtype")
     ldx = _rows("X", X, T, K, K)
@@ -198,11 +202,10 @@ def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) ->
         ldx = _pad16(ldx)  # a single row has no next one to be aligned with
     if workspace is None:
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
-    pkg._check("bcq_int_linear",
-               pkg.load().bcq_int_linear(X.data_ptr(), T, ldx, W.data_ptr(), w_scales.data_ptr(),
-                                         M, K, ldw, bp, Y.data_ptr(), ldy, dt,
-                                         workspace.data_ptr(), workspace.nbytes,
-                                         _handle(W, stream)))
+    r = lib.bcq_int_linear(X.data_ptr(), T, ldx, W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(),
+                           ldy, dt, workspace.data_ptr(), workspace.nbytes, _raw(W, stream))
+    if r:
+        _fail("bcq_int_linear", r)
 
 
 # ----------------------------------------------------------------------------- 4-bit cache
@@ -217,32 +220,30 @@ class KVCache:
     changed in place; the descriptor holds their addresses."""
 
     def __init__(self, k_codes, v_codes, scales, page_table, lens):
-        import torch
-
+        _lib or _bind()
         if k_codes.dim() != 4 or page_table.dim() != 2:
             raise ValueError("k_codes must be [pages][heads][page][D/2] and page_table 2-D")
         P, H, page, half = k_codes.shape
         D = 2 * half
-        _plain("k_codes", k_codes, torch.uint8, (P, H, page, half))
-        _plain("v_codes", v_codes, torch.uint8, (P, H, page // 4, 2 * D))
-        _plain("scales", scales, torch.float16, (P, H, page, 4))
         B, width = page_table.shape
-        _plain("page_table", page_table, torch.int32, (B, width))
-        _plain("lens", lens, torch.int32, (B,))
+        self._st = _KVCache(
+            B, H, D, page, P, width, _plain("k_codes", k_codes, torch.uint8, (P, H, page, half)),
+            _plain("v_codes", v_codes, torch.uint8, (P, H, page // 4, 2 * D)),
+            _plain("scales", scales, torch.float16, (P, H, page, 4)),
+            _plain("page_table", page_table, torch.int32, (B, width)),
+            _plain("lens", lens, torch.int32, (B,)))
+        self._ref = ctypes.byref(self._st)
         self.k_codes, self.v_codes, self.scales = k_codes, v_codes, scales
         self.page_table, self.lens = page_table, lens
         self.batch, self.heads, self.head_dim, self.page_tokens = B, H, D, page
         self.room = width * page
-        self._st = _KVCache(B, H, D, page, P, width, k_codes.data_ptr(), v_codes.data_ptr(),
-                            scales.data_ptr(), page_table.data_ptr(), lens.data_ptr())
-        self._ref = ctypes.byref(self._st)
+        self._slots = (B, H, self.room)  # of weights and positions
 
     @classmethod
     def new(cls, batch: int, tokens: int, heads: int, head_dim: int, page_tokens: int = 64,
             device="cuda") -> "KVCache":
         """An empty cache with room for `tokens` tokens of each sequence, pages in order."""
-        import torch
-
+        _lib or _bind()
         width = -(-tokens // page_tokens)
         P = batch * width
         z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)  # noqa: E731
@@ -254,42 +255,28 @@ class KVCache:
 
     def tracking(self):
         """Zeroed ``(weights, pos)`` for this cache, as append, attend and evict take them."""
-        import torch
-
-        shape = (self.batch, self.heads, self.room)
-        return (torch.zeros(shape, dtype=torch.float32, device=self.lens.device),
-                torch.zeros(shape, dtype=torch.int32, device=self.lens.device))
+        return (torch.zeros(self._slots, dtype=torch.float32, device=self.lens.device),
+                torch.zeros(self._slots, dtype=torch.int32, device=self.lens.device))
 
     def ref(self):
         return self._ref
 
 
-def _vectors(name: str, t, cache: KVCache):
-    """(dtype, strides) of K or V vectors [batch][n][heads][D] with contiguous channels."""
-    dt = _float(name, t)
-    s = t.shape
-    if len(s) != 4 or s[0] != cache.batch or s[2] != cache.heads or s[3] != cache.head_dim:
-        raise ValueError("%s must be [%d][n][%d][%d], got %s" %
-                         (name, cache.batch, cache.heads, cache.head_dim, tuple(s)))
-    st = t.stride()
-    if st[3] != 1:
-        raise ValueError("%s must have contiguous channels" % name)
-    return dt, st[:3]
-
-
 def _pair(K, V, cache: KVCache):
-    dt, ks = _vectors("K", K, cache)
-    dv, vs = _vectors("V", V, cache)
-    if dt != dv or K.shape[1] != V.shape[1]:
-        raise ValueError("K and V must share their dtype and number of tokens")
-    return dt, ks, vs
-
-
-def _slots(name: str, t, dtype, cache: KVCache) -> int:
-    if t is None:
-        return 0
-    _plain(name, t, dtype, (cache.batch, cache.heads, cache.room))
-    return t.data_ptr()
+    """(n, dtype, strides of K, of V) of vectors [batch][n][heads][D] with contiguous channels."""
+    shape = K.shape
+    if len(shape) != 4 or shape[0] != cache.batch or shape[2] != cache.heads or \
+            shape[3] != cache.head_dim or V.shape != shape:
+        raise ValueError("K and V must be [%d][n][%d][%d], got %s and %s" %
+                         (cache.batch, cache.heads, cache.head_dim, tuple(shape),
+                          tuple(V.shape)))
+    dt = _float("K", K)
+    if V.dtype is not K.dtype or not V.is_cuda:
+        raise ValueError("K and V must be device tensors of one dtype")
+    ks, vs = K.stride(), V.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("K and V must have contiguous channels")
+    return shape[1], dt, ks, vs
 
 
 def bcq_kv_append(cache: KVCache, K, V, positions=None, weights=None, pos=None,
@@ -297,39 +284,35 @@ def bcq_kv_append(cache: KVCache, K, V, positions=None, weights=None, pos=None,
     """Quantizes ``K`` and ``V`` [batch][n][heads][D] into the last n slots of every sequence;
     ``cache.lens`` must count them already.  ``weights`` and ``pos`` [batch][heads][room] get 0
     and the token's position (``positions`` int32 [batch][n], or its slot)."""
-    import torch
-
-    pkg = _pkg()
-    dt, ks, vs = _pair(K, V, cache)
-    n = K.shape[1]
-    if positions is not None:
-        _plain("positions", positions, torch.int32, (cache.batch, n))
-    pkg._check("bcq_kv_append",
-               pkg.load().bcq_kv_append(cache._ref, n, K.data_ptr(), *ks, V.data_ptr(), *vs, dt,
-                                        0 if positions is None else positions.data_ptr(),
-                                        _slots("weights", weights, torch.float32, cache),
-                                        _slots("pos", pos, torch.int32, cache),
-                                        _handle(K, stream)))
+    n, dt, ks, vs = _pair(K, V, cache)
+    r = _lib.bcq_kv_append(
+        cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2], V.data_ptr(), vs[0], vs[1], vs[2], dt,
+        0 if positions is None else _plain("positions", positions, torch.int32,
+                                           (cache.batch, n)),
+        0 if weights is None else _plain("weights", weights, torch.float32, cache._slots),
+        0 if pos is None else _plain("pos", pos, torch.int32, cache._slots), _raw(K, stream))
+    if r:
+        _fail("bcq_kv_append", r)
 
 
 def bcq_kv_read(cache: KVCache, K, V, stream=None) -> None:
     """Writes the values of the last n cached tokens to ``K`` and ``V`` [batch][n][heads][D]."""
-    pkg = _pkg()
-    dt, ks, vs = _pair(K, V, cache)
-    pkg._check("bcq_kv_read",
-               pkg.load().bcq_kv_read(cache._ref, K.shape[1], K.data_ptr(), *ks, V.data_ptr(),
-                                      *vs, dt, _handle(K, stream)))
+    n, dt, ks, vs = _pair(K, V, cache)
+    r = _lib.bcq_kv_read(cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2], V.data_ptr(), vs[0],
+                         vs[1], vs[2], dt, _raw(K, stream))
+    if r:
+        _fail("bcq_kv_read", r)
 
 
 def bcq_kv_workspace_bytes(cache: KVCache, n: int, q_heads: int, with_weights: bool) -> int:
-    return int(_pkg().load().bcq_kv_workspace_bytes(cache._ref, n, q_heads, bool(with_weights)))
+    return int(_lib.bcq_kv_workspace_bytes(cache._ref, n, q_heads, bool(with_weights)))
 
 
 def new_kv_workspace(cache: KVCache, n: int, q_heads: int, weights: bool = False):
-    """A device workspace for :func:`bcq_kv_attend` with n queries a sequence, or None when the
-    call needs none; calls that may overlap need separate ones."""
-    b = bcq_kv_workspace_bytes(cache, n, q_heads, weights)
-    return _workspace(b, cache.lens.device, None) if b else None
+    """A device workspace for :func:`bcq_kv_attend` with n queries a sequence; calls that may
+    overlap need separate ones."""
+    return _workspace(bcq_kv_workspace_bytes(cache, n, q_heads, weights), cache.lens.device,
+                      None)
 
 
 def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None,
@@ -337,32 +320,30 @@ def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None
     """Causal attention of ``Q`` [batch][n][q_heads][D], the queries of the last n cached tokens,
     over the cache into ``O`` (same shape); ``scale`` defaults to 1/sqrt(D).  ``weights``
     [batch][heads][room] float32 accumulates each cached token's probabilities."""
-    import torch
-
-    pkg = _pkg()
     dt = _float("Q", Q)
-    s = Q.shape
-    if len(s) != 4 or s[0] != cache.batch or s[3] != cache.head_dim or O.shape != s or \
-            O.dtype is not Q.dtype or not O.is_cuda:
+    shape = Q.shape
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim or \
+            O.shape != shape or O.dtype is not Q.dtype or not O.is_cuda:
         raise ValueError("Q and O must be [%d][n][q_heads][%d] of one dtype" %
                          (cache.batch, cache.head_dim))
-    qs, os_ = Q.stride(), O.stride()
-    if qs[3] != 1 or os_[3] != 1:
+    n, heads = shape[1], shape[2]
+    qs, os = Q.stride(), O.stride()
+    if qs[3] != 1 or os[3] != 1:
         raise ValueError("Q and O must have contiguous channels")
-    w = _slots("weights", weights, torch.float32, cache)
     if workspace is None:
-        b = bcq_kv_workspace_bytes(cache, s[1], s[2], w != 0)
-        workspace = _workspace(b, Q.device, stream)
-    pkg._check("bcq_kv_attend",
-               pkg.load().bcq_kv_attend(cache._ref, Q.data_ptr(), s[1], s[2], *qs[:3],
-                                        O.data_ptr(), *os_[:3], dt,
-                                        1.0 / math.sqrt(s[3]) if scale is None else scale, w,
-                                        workspace.data_ptr(), workspace.nbytes,
-                                        _handle(Q, stream)))
+        workspace = _workspace(bcq_kv_workspace_bytes(cache, n, heads, weights is not None),
+                               Q.device, stream)
+    r = _lib.bcq_kv_attend(
+        cache._ref, Q.data_ptr(), n, heads, qs[0], qs[1], qs[2], O.data_ptr(), os[0], os[1],
+        os[2], dt, shape[3] ** -0.5 if scale is None else scale,
+        0 if weights is None else _plain("weights", weights, torch.float32, cache._slots),
+        workspace.data_ptr(), workspace.nbytes, _raw(Q, stream))
+    if r:
+        _fail("bcq_kv_attend", r)
 
 
 def bcq_kv_evict_workspace_bytes(cache: KVCache, keep: int) -> int:
-    return int(_pkg().load().bcq_kv_evict_workspace_bytes(cache._ref, keep))
+    return int(_lib.bcq_kv_evict_workspace_bytes(cache._ref, keep))
 
 
 def new_kv_evict_workspace(cache: KVCache, keep: int):
@@ -375,23 +356,16 @@ def bcq_kv_evict(cache: KVCache, keep: int, recent: int, weights, pos, lens_out=
     """Shrinks every sequence to at most ``keep`` tokens a head, the ``recent`` newest and those of
     the largest ``weights``.  In place unless ``lens_out``, ``weights_out``, ``pos_out`` are
     given (the codes always are: see ``include/bcq.h``)."""
-    import torch
-
-    pkg = _pkg()
-    lens_out = cache.lens if lens_out is None else lens_out
-    weights_out = weights if weights_out is None else weights_out
-    pos_out = pos if pos_out is None else pos_out
-    if weights is None or pos is None:
-        raise ValueError("weights and pos are needed")
-    _plain("lens_out", lens_out, torch.int32, (cache.batch,))
+    slots, f32, i32 = cache._slots, torch.float32, torch.int32
+    w, p = _plain("weights", weights, f32, slots), _plain("pos", pos, i32, slots)
     if workspace is None:
         workspace = _workspace(bcq_kv_evict_workspace_bytes(cache, keep), weights.device, stream)
-    pkg._check("bcq_kv_evict",
-               pkg.load().bcq_kv_evict(cache._ref, keep, recent,
-                                       _slots("weights", weights, torch.float32, cache),
-                                       _slots("pos", pos, torch.int32, cache),
-                                       lens_out.data_ptr(),
-                                       _slots("weights_out", weights_out, torch.float32, cache),
-                                       _slots("pos_out", pos_out, torch.int32, cache),
-                                       workspace.data_ptr(), workspace.nbytes,
-                                       _handle(weights, stream)))
+    r = _lib.bcq_kv_evict(
+        cache._ref, keep, recent, w, p,
+        cache.lens.data_ptr() if lens_out is None
+        else _plain("lens_out", lens_out, i32, (cache.batch,)),
+        w if weights_out is None else _plain("weights_out", weights_out, f32, slots),
+        p if pos_out is None else _plain("pos_out", pos_out, i32, slots),
+        workspace.data_ptr(), workspace.nbytes, _raw(weights, stream))
+    if r:
+        _fail("bcq_kv_evict", r)
