@@ -40,25 +40,39 @@ template <typename T>
 __device__ __forceinline__ void load_row8(float (&x)[8], const T *row, int k, int K) {
   if (k + 8 <= K) {
     load8(x, row + k);
+  } else if (k >= K) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = k + e < K ? (float)row[k + e] : 0.f;
   }
 }
 
-__device__ __forceinline__ uint32_t code_of(float x, float s) {
-  const float q = s > 0.f && s < INFINITY ? rintf(x / s) : 0.f;
-  return (uint32_t)(int)fminf(fmaxf(q, -127.f), 127.f) & 255u;
-}
-
+// Codes of eight elements.  The quotient's neighbour x * (1/s), at most 5e-5 off
+// it, rounds to the same integer unless it lies that close to a half; only then
+// is the division done.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
-  uint2 c = {0, 0};
+  const bool some = s > 0.f && s < INFINITY;
+  const float inv = some ? 1.f / s : 0.f;
+  float q[8];
+  bool near = false;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    c.x |= code_of(x[e], s) << (8 * e);
-    c.y |= code_of(x[4 + e], s) << (8 * e);
+  for (int e = 0; e < 8; ++e) {
+    const float y = x[e] * inv;
+    q[e] = rintf(y);
+    near |= !(fabsf(y - q[e]) < 0.4999f);
   }
-  return c;
+  if (__builtin_expect(near, 0) && some) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = rintf(x[e] / s);
+  }
+  uint32_t c[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    c[e] = some ? (uint32_t)(int)fminf(fmaxf(q[e], -127.f), 127.f) & 255u : 0u;
+  return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+                    c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
 }
 
 // A row's scale; NaN for a row that holds an infinity or NaN (its codes are 0),
@@ -67,18 +81,28 @@ __device__ __forceinline__ float row_scale(float top) {
   return top < INFINITY ? top * (1.f / 127.f) : NAN;
 }
 
-// One workgroup a row, read twice (the second time from the caches).
-template <typename T>
+// One workgroup a row.  Rows of up to 2048 N elements are held in registers
+// between the two passes, longer ones (N = 0) read again from the caches.
+template <typename T, int N>
 __global__ __launch_bounds__(256) void quantize_kernel(const T *X, int K, int ldx, int8_t *codes,
                                                        int ldc, float *scales) {
   __shared__ float red[4];
   const T *x = X + (int64_t)blockIdx.x * ldx;
   const int tid = threadIdx.x;
-  float v[8], top = 0.f;
-  for (int k = tid * 8; k < K; k += 256 * 8) {
-    load_row8(v, x, k, K);
+  float v[N > 0 ? N : 1][8], top = 0.f;
+  if constexpr (N > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(v[e]));
+    for (int n = 0; n < N; ++n) load_row8(v[n], x, (n * 256 + tid) * 8, K);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(v[n][e]));
+  } else {
+    for (int k = tid * 8; k < K; k += 256 * 8) {
+      load_row8(v[0], x, k, K);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(v[0][e]));
+    }
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = nan_max(top, __shfl_xor(top, d));
@@ -89,82 +113,126 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T *X, int K, int ld
   if (tid == 0) scales[blockIdx.x] = s;
   int8_t *c = codes + (int64_t)blockIdx.x * ldc;
   const int end = (K + 15) / 16 * 16;  // zeros up to the next 16 bytes
-  for (int k = tid * 8; k < end; k += 256 * 8) {
-    load_row8(v, x, k, K);
-    *reinterpret_cast<uint2 *>(c + k) = codes8(v, s);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_y(const IntProduct &p, int t, int m, const float (&v)[4]) {
-  T *y = static_cast<T *>(p.y) + (int64_t)t * p.ldy + m;
-  if (m + 4 <= p.M && ((uintptr_t)y & (4 * sizeof(T) - 1)) == 0) {
-    struct __attribute__((aligned(4 * sizeof(T)))) V4 {
-      T x[4];
-    } o;
+  if constexpr (N > 0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o.x[e] = (T)v[e];
-    *reinterpret_cast<V4 *>(y) = o;
+    for (int n = 0; n < N; ++n) {
+      const int k = (n * 256 + tid) * 8;
+      if (k < end) *reinterpret_cast<uint2 *>(c + k) = codes8(v[n], s);
+    }
   } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (m + e < p.M) y[e] = (T)v[e];
+    for (int k = tid * 8; k < end; k += 256 * 8) {
+      load_row8(v[0], x, k, K);
+      *reinterpret_cast<uint2 *>(c + k) = codes8(v[0], s);
+    }
   }
 }
 
-// Outputs (t, m..m+3) from their exact sums.
 template <typename T>
-__device__ __forceinline__ void finish(const IntProduct &p, int t, int m, float a_scale,
-                                       const int (&acc)[4]) {
-  float v[4];
+struct __attribute__((aligned(4 * sizeof(T)))) Four {
+  T x[4];
+};
+
+// Four outputs of token t from row m on: their scales and biases, from their exact sums.
+struct RowFactors {
+  float scale[4], bias[4];
+};
+template <typename T>
+__device__ __forceinline__ RowFactors row_factors(const IntProduct &p, int m) {
+  RowFactors f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int mm = min(m + e, p.M - 1);
-    v[e] = (float)acc[e] * (a_scale * p.w_scale[mm]);
-    if (p.bias != nullptr) v[e] += (float)static_cast<const T *>(p.bias)[mm];
+    f.scale[e] = p.w_scale[mm];
+    f.bias[e] = p.bias != nullptr ? (float)static_cast<const T *>(p.bias)[mm] : 0.f;
   }
-  store_y<T>(p, t, m, v);
+  return f;
+}
+template <typename T>
+__device__ __forceinline__ Four<T> finish(const RowFactors &f, float a_scale, const int (&acc)[4]) {
+  Four<T> y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    y.x[e] = (T)fmaf((float)acc[e], a_scale * f.scale[e], f.bias[e]);
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ void store_y(const IntProduct &p, int t, int m, const Four<T> &v) {
+  T *y = static_cast<T *>(p.y) + (int64_t)t * p.ldy + m;
+  if (m + 4 <= p.M && ((uintptr_t)y & (4 * sizeof(T) - 1)) == 0) {
+    *reinterpret_cast<Four<T> *>(y) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (m + e < p.M) y[e] = v.x[e];
+  }
+}
+
+// Sums of rows m..m+3 of one token of a slice.
+__device__ __forceinline__ void store_sums(int32_t *token, int m, int M, int4v s) {
+  int32_t *o = token + m;
+  if (m + 4 <= M && (M & 3) == 0) {
+    *reinterpret_cast<int4v *>(o) = s;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (m + e < M) o[e] = s[e];
+  }
 }
 
 // ---- few tokens: one launch
 //
 // 16 rows of W a workgroup, its four waves taking turns over K in steps of 128
 // bytes; W goes from memory to the matrix operands without passing through
-// shared memory, eight loads of 16 bytes a lane in flight, the first of them
-// asked for before the tokens are quantized.  Every workgroup quantizes the
-// tokens for itself: T * K is at most kFusedElements, a fraction of a
-// microsecond, where a launch of its own costs several.
+// shared memory, and a wave has up to eight steps (16 KB) in flight, asked for
+// before the tokens are quantized.  Every workgroup quantizes the tokens for
+// itself: T * K is at most kFusedElements, a fraction of a microsecond, where a
+// launch of its own costs several.
 constexpr int kFusedTokens = 16, kFusedElements = 16384;
-constexpr int kFusedDepth = 4;  // steps in flight
+constexpr int kFusedDepth = 8;  // steps in flight
 
 template <typename T>
 __global__ __launch_bounds__(256) void fused_kernel(IntProduct p, const T *X, int ldx) {
   extern __shared__ __align__(16) int8_t xs[];  // [T][row]
   __shared__ float red[kFusedTokens][4];
   __shared__ int4v part[4][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int m0 = blockIdx.x * 16;
   const int K16 = (p.K + 15) / 16 * 16, steps = (p.K + 127) / 128;
   const int row = steps * 128 + 16;  // 16 past a multiple of 128: rows start in other banks
   const int8_t *w = p.w + (int64_t)min(m0 + r, p.M - 1) * p.ldw + g * 32;
 
+  // the first elements of the first token, ahead of the flood of weights
+  constexpr int kHeld = 2;
+  float held[kHeld][8];
+#pragma unroll
+  for (int n = 0; n < kHeld; ++n) load_row8(held[n], X, (n * 256 + tid) * 8, p.K);
   int4v wf[kFusedDepth][2];
   auto fetch = [&](int4v(&f)[2], int step) {
     const int k = step * 128 + g * 32;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      f[e] = k + 16 * e < K16 && step < steps
-                 ? *reinterpret_cast<const int4v *>(w + (int64_t)step * 128 + 16 * e)
-                 : int4v{0, 0, 0, 0};
+      f[e] = k + 16 * e < K16 ? *reinterpret_cast<const int4v *>(w + (int64_t)step * 128 + 16 * e)
+                              : int4v{0, 0, 0, 0};
   };
 #pragma unroll
-  for (int d = 0; d < kFusedDepth; ++d) fetch(wf[d], wave + 4 * d);
+  for (int d = 0; d < kFusedDepth; ++d)
+    if (wave + 4 * d < steps) fetch(wf[d], wave + 4 * d);
 
+  auto values = [&](float(&v)[8], int t, int n) {
+    if (t == 0 && n < kHeld) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = n == 0 ? held[0][e] : held[1][e];
+    } else {
+      load_row8(v, X + (int64_t)t * ldx, (n * 256 + tid) * 8, p.K);
+    }
+  };
+  const int parts = (p.K + 2047) / 2048;
   for (int t = 0; t < p.T; ++t) {
     float v[8], top = 0.f;
-    for (int k = tid * 8; k < p.K; k += 256 * 8) {
-      load_row8(v, X + (int64_t)t * ldx, k, p.K);
+    for (int n = 0; n < parts; ++n) {
+      values(v, t, n);
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(v[e]));
     }
@@ -177,8 +245,10 @@ __global__ __launch_bounds__(256) void fused_kernel(IntProduct p, const T *X, in
     const float s =
         row_scale(nan_max(nan_max(red[t][0], red[t][1]), nan_max(red[t][2], red[t][3])));
     float v[8];
-    for (int k = tid * 8; k < steps * 128; k += 256 * 8) {
-      load_row8(v, X + (int64_t)t * ldx, k, p.K);
+    for (int n = 0; n < parts; ++n) {
+      const int k = (n * 256 + tid) * 8;
+      if (k >= steps * 128) break;
+      values(v, t, n);
       *reinterpret_cast<uint2 *>(xs + t * row + k) = codes8(v, s);
     }
   }
@@ -195,7 +265,7 @@ __global__ __launch_bounds__(256) void fused_kernel(IntProduct p, const T *X, in
         for (int e = 0; e < 2; ++e)
           acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
               wf[d][e], *reinterpret_cast<const int4v *>(xr + st * 128 + 16 * e), acc, 0, 0, 0);
-        fetch(wf[d], st + 4 * kFusedDepth);
+        if (st + 4 * kFusedDepth < steps) fetch(wf[d], st + 4 * kFusedDepth);
       }
     }
   }
@@ -208,33 +278,149 @@ __global__ __launch_bounds__(256) void fused_kernel(IntProduct p, const T *X, in
       sum[e] = part[0][lane][e] + part[1][lane][e] + part[2][lane][e] + part[3][lane][e];
     const float s =
         row_scale(nan_max(nan_max(red[r][0], red[r][1]), nan_max(red[r][2], red[r][3])));
-    if (m0 + 4 * g < p.M) finish<T>(p, r, m0 + 4 * g, s, sum);
+    const int m = m0 + 4 * g;
+    if (m < p.M) store_y<T>(p, r, m, finish<T>(row_factors<T>(p, m), s, sum));
+  }
+}
+
+// ---- up to 64 tokens
+//
+// Bound by reading W once.  32 rows of W by all the tokens a workgroup; its four
+// waves share a step's four products of 32 bytes of K between them, one each, and
+// add up at the end.  Shared memory holds a ring of kRing steps that memory fills
+// directly, so that a compute unit's two or three workgroups have 30 KB of W and
+// more in flight; a step waits for its own loads only (loads return in order),
+// and loads past the end of K come from 16 bytes of zeros, which keeps the count
+// the same.
+constexpr int kRing = 5;
+
+template <typename T, int BT, bool SPLIT>
+__global__ __launch_bounds__(256) void few_kernel(IntProduct p, int tiles_m, int slice_steps,
+                                                  int32_t *partial) {
+  constexpr int BM = 32, kT = BT / 32;
+  constexpr int kLoads = (BM + BT) / 8 / 4;  // of 1 KB, a wave and step
+  constexpr int kStage = (BM + BT) * 128;
+  __shared__ __align__(16) int8_t lds[kRing][kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slice = SPLIT ? blockIdx.x / tiles_m : 0;
+  const int m0 = (blockIdx.x - slice * tiles_m) * BM;
+  const int K16 = (p.K + 15) / 16 * 16, all = (p.K + 127) / 128;
+  const int first = SPLIT ? slice * slice_steps : 0;
+  const int steps = SPLIT ? min(all - first, slice_steps) : all;
+
+  const int8_t *src[kLoads];
+  int chunk[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int row = (wave * kLoads + j) * 8 + (lane >> 3);
+    chunk[j] = ((lane & 7) ^ (row & 7)) * 16;
+    src[j] = row < BM ? p.w + (int64_t)min(m0 + row, p.M - 1) * p.ldw
+                      : p.a + (int64_t)min(row - BM, p.T - 1) * p.lda;
+  }
+  auto stage = [&](int step) {
+    int8_t *to = lds[step % kRing];
+    const int k = (first + step) * 128;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const void *from = step < steps && k + chunk[j] < K16 ? (const void *)(src[j] + k + chunk[j])
+                                            : (const void *)&kZeros;
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void *)from,
+          (__attribute__((address_space(3))) void *)(to + (wave * kLoads + j) * 1024), 16, 0, 0);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) stage(s);
+
+  const int r = lane & 31, hi = lane >> 5;
+  const int at = ((wave * 2 + hi) ^ (r & 7)) * 16;
+  int16v acc[kT];
+#pragma unroll
+  for (int j = 0; j < kT; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[j][e] = 0;
+  for (int step = 0; step < steps; ++step) {
+    // this step's loads are the oldest kLoads of (kRing - 1) * kLoads
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRing - 2) * kLoads) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    stage(step + kRing - 1);  // over the step before, which every wave has read
+    const int8_t *from = lds[step % kRing];
+    const int4v wf = *reinterpret_cast<const int4v *>(from + r * 128 + at);
+#pragma unroll
+    for (int j = 0; j < kT; ++j)
+      acc[j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+          wf, *reinterpret_cast<const int4v *>(from + (BM + j * 32 + r) * 128 + at), acc[j], 0, 0,
+          0);
+    // reads are done before the barrier that lets the next load overwrite them
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+
+  // the waves' sums: wave w adds up and writes rows 8w..8w+7 of every token
+  int *part = reinterpret_cast<int *>(&lds[0][0]);  // [wave][token tile][row / 4][token][4]
+#pragma unroll
+  for (int j = 0; j < kT; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<int4v *>(part + (((wave * kT + j) * 8 + 2 * q + hi) * 32 + r) * 4) =
+          int4v{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+  __syncthreads();
+  const int m = m0 + 8 * wave + 4 * hi;
+  if (m >= p.M) return;
+  RowFactors f;
+  if constexpr (!SPLIT) f = row_factors<T>(p, m);
+#pragma unroll
+  for (int j = 0; j < kT; ++j) {
+    const int t = j * 32 + r;
+    if (t >= p.T) continue;
+    int4v s = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      s += *reinterpret_cast<const int4v *>(
+          part + (((w * kT + j) * 8 + 2 * wave + hi) * 32 + r) * 4);
+    if constexpr (SPLIT) {
+      store_sums(partial + ((int64_t)slice * p.T + t) * p.M, m, p.M, s);
+    } else {
+      const int sum[4] = {s[0], s[1], s[2], s[3]};
+      store_y<T>(p, t, m, finish<T>(f, p.a_scale[t], sum));
+    }
   }
 }
 
 // ---- tiles
 //
-// BM rows of W by BT tokens a workgroup of four waves, 128 bytes of K a step,
-// two stages in shared memory that memory fills directly.  A row's eight
-// 16-byte chunks lie in the order chunk ^ (row mod 8), so that the eight lanes
-// that share a cycle of a 16-byte read are in different banks; the order is
-// made by which chunk each lane asks memory for.
+// BM rows of W by BT tokens a workgroup, 128 bytes of K a step, two stages in
+// shared memory that memory fills directly.  A row's eight 16-byte chunks lie in
+// the order chunk ^ (row mod 8), so that the eight lanes that share a cycle of a
+// 16-byte read are in different banks; the order is made by which chunk each
+// lane asks memory for.
+//
+// A step is four products of 32 bytes.  Their operands are read one product
+// ahead, and the barrier stands before the last of them: its operands are in
+// registers by then, so it runs while the next step's first are read and the
+// stage just finished is asked for again, a whole step ahead of its use.
 constexpr int kStep = 128;
 
 template <int BM, int BT, int WM, int WT>
 struct TileShape {
   static constexpr int kThreads = WM * WT * 64;
-  static constexpr int kM = BM / WM / 32, kT = BT / WT / 32;  // 32x32 tiles of a wave
+  static constexpr int kRows = BM / WM, kTokens = BT / WT;    // of a wave
+  static constexpr int kM = kRows / 32, kT = kTokens / 32;    // its 32x32 tiles
   static constexpr int kLoads = (BM + BT) / 8 / (WM * WT);    // of 1 KB, a wave and stage
   static constexpr int kStageBytes = (BM + BT) * kStep;
+  static constexpr int kOutStride = kRows * 2 + 16;           // of a token's fp16 outputs
 };
 
 template <typename T, int BM, int BT, int WM, int WT, bool SPLIT>
-__global__ __launch_bounds__(WM *WT * 64) void tile_kernel(IntProduct p, int tiles_m, int tiles_t,
+__global__ __launch_bounds__(WM *WT * 64, BM * BT <= 128 * 128 ? 2 : 1) void tile_kernel(IntProduct p, int tiles_m, int tiles_t,
                                                            int slices, int slice_steps,
                                                            int32_t *partial) {
   using S = TileShape<BM, BT, WM, WT>;
   __shared__ __align__(16) int8_t lds[2][S::kStageBytes];
+  __shared__ __align__(16) float row_scales[BM], row_bias[BM];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // workgroups go to the 8 XCDs in turn: each XCD gets a run of tiles that
@@ -280,55 +466,125 @@ __global__ __launch_bounds__(WM *WT * 64) void tile_kernel(IntProduct p, int til
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  const int wm = wave / WT * (BM / WM), wt = wave % WT * (BT / WT);
+  const int wm = wave / WT * S::kRows, wt = wave % WT * S::kTokens;
   const int r = lane & 31, hi = lane >> 5;
-  if (first < last) stage(0, first);
-  for (int step = first; step < last; ++step) {
-    const int buf = (step - first) & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (step + 1 < last) stage(buf ^ 1, step + 1);
+  int4v wf[2][S::kM], af[2][S::kT];
+  auto operands = [&](int buf, int ks, int into) {
+    const int at = ((ks * 2 + hi) ^ (r & 7)) * 16;
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      int4v wf[S::kM], af[S::kT];
-      const int at = ((ks * 2 + hi) ^ (r & 7)) * 16;
+    for (int i = 0; i < S::kM; ++i)
+      wf[into][i] = *reinterpret_cast<const int4v *>(&lds[buf][(wm + i * 32 + r) * kStep + at]);
 #pragma unroll
-      for (int i = 0; i < S::kM; ++i)
-        wf[i] = *reinterpret_cast<const int4v *>(&lds[buf][(wm + i * 32 + r) * kStep + at]);
+    for (int j = 0; j < S::kT; ++j)
+      af[into][j] =
+          *reinterpret_cast<const int4v *>(&lds[buf][(BM + wt + j * 32 + r) * kStep + at]);
+  };
+  auto multiply = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < S::kM; ++i)
 #pragma unroll
       for (int j = 0; j < S::kT; ++j)
-        af[j] = *reinterpret_cast<const int4v *>(&lds[buf][(BM + wt + j * 32 + r) * kStep + at]);
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[from][i], af[from][j], acc[i][j], 0,
+                                                          0, 0);
+  };
+  // all of this wave's loads have landed and its reads are done, then all waves'
+  auto meet = [&]() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+  };
+  if (first < last) {
+    stage(0, first);
+    meet();
+    if (first + 1 < last) stage(1, first + 1);
+    operands(0, 0, 0);
+  }
+  for (int step = first; step < last; ++step) {
+    const int buf = (step - first) & 1;
+#pragma unroll
+    for (int ks = 0; ks < 3; ++ks) {
+      operands(buf, ks + 1, (ks + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(ks & 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    meet();
+    if (step + 2 < last) stage(buf, step + 2);
+    if (step + 1 < last) operands(buf ^ 1, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) {
+      const int t = t0 + wt + j * 32 + r;
+      if (t >= p.T) continue;
 #pragma unroll
       for (int i = 0; i < S::kM; ++i)
 #pragma unroll
-        for (int j = 0; j < S::kT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i], af[j], acc[i][j], 0, 0, 0);
+        for (int q = 0; q < 4; ++q) {
+          const int m = m0 + wm + i * 32 + 8 * q + 4 * hi;
+          store_sums(partial + ((int64_t)slice * p.T + t) * p.M, m, p.M,
+                     int4v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                           acc[i][j][4 * q + 3]});
+        }
     }
+    return;
   }
-
+  float a_scale[S::kT];
+#pragma unroll
+  for (int j = 0; j < S::kT; ++j) a_scale[j] = p.a_scale[min(t0 + wt + j * 32 + r, p.T - 1)];
+  // fp16 outputs that can be written 16 bytes at a time turn in shared memory,
+  // each wave its own: a lane holds 4 rows of one token, a write wants 8
+  const bool turn = sizeof(T) == 2 && ((uintptr_t)p.y & 15) == 0 && p.ldy % 8 == 0;
+  int8_t *out = &lds[0][0] + wave * (S::kOutStride * 32);
+  if (tid < BM) {
+    const int m = min(m0 + tid, p.M - 1);
+    row_scales[tid] = p.w_scale[m];
+    row_bias[tid] = p.bias != nullptr ? (float)static_cast<const T *>(p.bias)[m] : 0.f;
+  }
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < S::kT; ++j) {
     const int t = t0 + wt + j * 32 + r;
-    if (t >= p.T) continue;
-    const float s = SPLIT ? 0.f : p.a_scale[t];
+    asm volatile("" ::: "memory");  // the factors are read again, not kept in registers
 #pragma unroll
     for (int i = 0; i < S::kM; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int m = m0 + wm + i * 32 + 8 * q + 4 * hi;
-        if (m >= p.M) continue;
+        const int row = i * 32 + 8 * q + 4 * hi, m = m0 + wm + row;
         int sum[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] = acc[i][j][4 * q + e];
-        if constexpr (SPLIT) {
-          int32_t *o = partial + ((int64_t)slice * p.T + t) * p.M + m;
+        RowFactors f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (m + e < p.M) o[e] = sum[e];
-        } else {
-          finish<T>(p, t, m, s, sum);
+        for (int e = 0; e < 4; ++e) {
+          f.scale[e] = row_scales[wm + row + e];
+          f.bias[e] = row_bias[wm + row + e];
+        }
+        const Four<T> y = finish<T>(f, a_scale[j], sum);
+        if (turn)
+          *reinterpret_cast<Four<T> *>(out + r * S::kOutStride + row * 2) = y;
+        else if (t < p.T && m < p.M)
+          store_y<T>(p, t, m, y);
+      }
+    if (turn) {
+      constexpr int kPer = S::kRows / 8;  // 16-byte pieces of a token
+#pragma unroll
+      for (int k = 0; k < 32 * kPer / 64; ++k) {
+        const int piece = k * 64 + lane, tt = t0 + wt + j * 32 + piece / kPer;
+        const int row = piece % kPer * 8, m = m0 + wm + row;
+        const int8_t *from = out + piece / kPer * S::kOutStride + row * 2;
+        T *y = static_cast<T *>(p.y) + (int64_t)tt * p.ldy + m;
+        if (tt < p.T && m + 8 <= p.M) {
+          *reinterpret_cast<int4v *>(y) = *reinterpret_cast<const int4v *>(from);
+        } else if (tt < p.T) {
+          for (int e = 0; e < 8; ++e)
+            if (m + e < p.M) y[e] = reinterpret_cast<const T *>(from)[e];
         }
       }
+    }
   }
 }
 
@@ -347,49 +603,87 @@ __global__ __launch_bounds__(256) void join_kernel(IntProduct p, int slices,
     for (int e = 0; e < 4; ++e)
       if (m + e < p.M) sum[e] += o[e];
   }
-  finish<T>(p, t, m, p.a_scale[t], sum);
+  store_y<T>(p, t, m, finish<T>(row_factors<T>(p, m), p.a_scale[t], sum));
 }
 
-// The tile and the split of K for a product: the large tile once it fills the
-// 256 compute units, else the small one, with K split until the card is full
-// (never under four steps a slice).
+// The tile and the split of K for a product.  A tile of side b costs each compute
+// unit b * b over what it reaches of the largest one's rate (measured at
+// 4096 x 4096 x 14336 on 256 compute units: 2118, 1669 and 1128 TOP/s with 256,
+// 128 and 64), and the compute unit with the most tiles ends last.  Where even
+// the small tiles leave compute units idle K is split, never under eight steps.
+// Up to kFewTokens tokens go through the ring instead (side 32 or 64, their
+// number rounded up).
+constexpr int kFewTokens = 64;
 struct TilePlan {
-  bool large;
-  int tiles_m, tiles_t, slices, slice_steps;
+  int side, tiles_m, tiles_t, slices, slice_steps;
+  bool few;
 };
 TilePlan tile_plan(int T, int M, int K) {
-  TilePlan q;
-  auto tiles = [&](int b) { return (int64_t)((M + b - 1) / b) * ((T + b - 1) / b); };
-  q.large = tiles(128) >= 256;
-  const int b = q.large ? 128 : 64;
+  TilePlan q{};
+  const int steps = (K + kStep - 1) / kStep;
+  auto split = [&](int64_t want) {
+    int64_t slices = want / ((int64_t)q.tiles_m * q.tiles_t);
+    slices = slices > steps / 8 ? steps / 8 : slices;
+    slices = slices < 1 ? 1 : slices;
+    q.slice_steps = (int)((steps + slices - 1) / slices);
+    q.slices = (steps + q.slice_steps - 1) / q.slice_steps;
+  };
+  if (T <= kFewTokens) {
+    q.few = true;
+    q.side = T <= 32 ? 32 : 64;
+    q.tiles_m = (M + 31) / 32;
+    q.tiles_t = 1;
+    split(256);
+    return q;
+  }
+  double best = 0;
+  const int sides[3] = {256, 128, 64};
+  const double rate[3] = {1.0, 0.79, 0.53};
+  for (int i = 0; i < 3; ++i) {
+    const int b = sides[i];
+    const int64_t tiles = (int64_t)((M + b - 1) / b) * ((T + b - 1) / b);
+    const double cost = (double)((tiles + 255) / 256) * b * b / rate[i];
+    if (i == 0 || cost < best) {
+      best = cost;
+      q.side = b;
+    }
+  }
+  const int b = q.side;
   q.tiles_m = (M + b - 1) / b;
   q.tiles_t = (T + b - 1) / b;
-  const int steps = (K + kStep - 1) / kStep;
-  int slices = q.large ? 1 : (int)(512 / tiles(b));
-  const int most = steps / 4;
-  slices = slices > most ? most : slices;
-  slices = slices < 1 ? 1 : slices;
-  q.slice_steps = (steps + slices - 1) / slices;
-  q.slices = (steps + q.slice_steps - 1) / q.slice_steps;
+  split(b > 64 ? 0 : 512);
   return q;
 }
 
-template <typename T, int B, bool SPLIT>
+template <typename T, int B, int WM, int WT, bool SPLIT>
 void run_tiles(const IntProduct &p, const TilePlan &q, int32_t *partial, hipStream_t s) {
   const unsigned grid = (unsigned)(((int64_t)q.tiles_m * q.tiles_t * q.slices + 7) / 8 * 8);
-  tile_kernel<T, B, B, 2, 2, SPLIT><<<grid, 256, 0, s>>>(p, q.tiles_m, q.tiles_t, q.slices,
-                                                         q.slice_steps, partial);
+  tile_kernel<T, B, B, WM, WT, SPLIT><<<grid, WM * WT * 64, 0, s>>>(
+      p, q.tiles_m, q.tiles_t, q.slices, q.slice_steps, partial);
 }
 
 template <typename T>
 hipError_t gemm_type(const IntProduct &p, int32_t *partial, hipStream_t s) {
   const TilePlan q = tile_plan(p.T, p.M, p.K);
-  if (q.large)
-    run_tiles<T, 128, false>(p, q, partial, s);
-  else if (q.slices == 1)
-    run_tiles<T, 64, false>(p, q, partial, s);
-  else
-    run_tiles<T, 64, true>(p, q, partial, s);
+  if (q.few) {
+    const unsigned grid = (unsigned)q.tiles_m * q.slices;
+    if (q.side == 32 && q.slices == 1)
+      few_kernel<T, 32, false><<<grid, 256, 0, s>>>(p, q.tiles_m, q.slice_steps, partial);
+    else if (q.side == 32)
+      few_kernel<T, 32, true><<<grid, 256, 0, s>>>(p, q.tiles_m, q.slice_steps, partial);
+    else if (q.slices == 1)
+      few_kernel<T, 64, false><<<grid, 256, 0, s>>>(p, q.tiles_m, q.slice_steps, partial);
+    else
+      few_kernel<T, 64, true><<<grid, 256, 0, s>>>(p, q.tiles_m, q.slice_steps, partial);
+  } else if (q.side == 256) {
+    run_tiles<T, 256, 4, 2, false>(p, q, partial, s);
+  } else if (q.side == 128) {
+    run_tiles<T, 128, 2, 2, false>(p, q, partial, s);
+  } else if (q.slices == 1) {
+    run_tiles<T, 64, 2, 2, false>(p, q, partial, s);
+  } else {
+    run_tiles<T, 64, 2, 2, true>(p, q, partial, s);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || q.slices == 1) return e;
   const int64_t quads = (int64_t)((p.M + 3) / 4) * p.T;
@@ -406,13 +700,24 @@ hipError_t fused_type(const IntProduct &p, const void *X, int ldx, hipStream_t s
 
 }  // namespace
 
+template <typename T>
+static hipError_t quantize_type(const void *X, int rows, int K, int ldx, int8_t *codes, int ldc,
+                                float *scales, hipStream_t s) {
+  const T *x = static_cast<const T *>(X);
+  if (K <= 2048)
+    quantize_kernel<T, 1><<<rows, 256, 0, s>>>(x, K, ldx, codes, ldc, scales);
+  else if (K <= 4096)
+    quantize_kernel<T, 2><<<rows, 256, 0, s>>>(x, K, ldx, codes, ldc, scales);
+  else if (K <= 8192)
+    quantize_kernel<T, 4><<<rows, 256, 0, s>>>(x, K, ldx, codes, ldc, scales);
+  else
+    quantize_kernel<T, 0><<<rows, 256, 0, s>>>(x, K, ldx, codes, ldc, scales);
+  return hipGetLastError();
+}
 hipError_t launch_int_quantize(const void *X, bcq_dtype dt, int rows, int K, int ldx,
                                int8_t *codes, int ldc, float *scales, hipStream_t s) {
-  if (dt == BCQ_F16)
-    quantize_kernel<<<rows, 256, 0, s>>>((const _Float16 *)X, K, ldx, codes, ldc, scales);
-  else
-    quantize_kernel<<<rows, 256, 0, s>>>((const float *)X, K, ldx, codes, ldc, scales);
-  return hipGetLastError();
+  return dt == BCQ_F16 ? quantize_type<_Float16>(X, rows, K, ldx, codes, ldc, scales, s)
+                       : quantize_type<float>(X, rows, K, ldx, codes, ldc, scales, s);
 }
 
 size_t int_partial_bytes(int T, int M, int K) {

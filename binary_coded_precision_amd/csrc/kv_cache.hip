@@ -64,14 +64,13 @@ struct Place {
   int b, i, h, slot;
   bool v;
 };
-__device__ __forceinline__ Place place(const KvView &c, int n, int64_t vec) {
+__device__ __forceinline__ Place place(const KvView &c, int n, uint32_t vec) {
   Place p;
   p.v = vec & 1;
-  vec >>= 1;
-  p.h = (int)(vec % c.H);
-  vec /= c.H;
-  p.i = (int)(vec % n);
-  p.b = (int)(vec / n);
+  const uint32_t at = (vec >> 1) / (uint32_t)c.H;
+  p.h = (int)((vec >> 1) - at * (uint32_t)c.H);
+  p.b = (int)(at / (uint32_t)n);
+  p.i = (int)(at - (uint32_t)p.b * (uint32_t)n);
   p.slot = kv_len(c, p.b) - n + p.i;
   return p;
 }
@@ -82,9 +81,9 @@ template <int D, typename T, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k, KvStrides ks,
                                                      const T *v, KvStrides vs,
                                                      const int32_t *positions, float *weights,
-                                                     int32_t *pos, int64_t vecs) {
+                                                     int32_t *pos, uint32_t vecs) {
   constexpr int L = D / 4;
-  const int64_t vec = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
   const int i = threadIdx.x % L;
   if (vec >= vecs) return;  // whole groups of L lanes leave together
   const Place p = place(c, n, vec);
@@ -104,12 +103,24 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k
   const _Float16 zh = (_Float16)lo, sh = (_Float16)step;
   const float zero = (float)zh, scale = (float)sh;
   uint32_t word = 0;
+  // the quotient's neighbour y * (1 / scale) is less than 1e-5 off it and rounds
+  // to the same integer unless it lies that close to a half
+  const float inv = scale > 0.f ? 1.f / scale : 0.f;
+  float q[4];
+  bool near = false;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float q = scale > 0.f ? rintf((x[e] - zero) / scale) : 0.f;
-    q = fminf(fmaxf(q, 0.f), 15.f);
-    word |= (uint32_t)q << (4 * e);
+    const float y = (x[e] - zero) * inv;
+    q[e] = rintf(y);
+    near |= !(fabsf(y - q[e]) < 0.4999f);
   }
+  if (__builtin_expect(near, 0) && scale > 0.f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = rintf((x[e] - zero) / scale);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    word |= (scale > 0.f ? (uint32_t)fminf(fmaxf(q[e], 0.f), 15.f) : 0u) << (4 * e);
   if (p.slot < 0) return;
   const int64_t token = kv_token(c, p.b, p.h, p.slot);
   if (token < 0) return;
@@ -134,9 +145,9 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k
 
 template <int D, typename T, bool VEC>
 __global__ __launch_bounds__(256) void read_kernel(KvView c, int n, T *k, KvStrides ks, T *v,
-                                                   KvStrides vs, int64_t vecs) {
+                                                   KvStrides vs, uint32_t vecs) {
   constexpr int L = D / 4;
-  const int64_t vec = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
   const int i = threadIdx.x % L;
   if (vec >= vecs) return;
   const Place p = place(c, n, vec);
@@ -168,8 +179,8 @@ template <int D, typename T>
 hipError_t append_dim(const KvView &c, int n, const void *k, KvStrides ks, const void *v,
                       KvStrides vs, const int32_t *positions, float *weights, int32_t *pos,
                       hipStream_t s) {
-  const int64_t vecs = (int64_t)c.B * n * c.H * 2, per = 256 / (D / 4);
-  const unsigned grid = (unsigned)((vecs + per - 1) / per);
+  const uint32_t vecs = (uint32_t)c.B * n * c.H * 2, per = 256 / (D / 4);
+  const uint32_t grid = (vecs + per - 1) / per;
   if (vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T)))
     append_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, (const T *)k, ks, (const T *)v, vs,
                                                    positions, weights, pos, vecs);
@@ -182,8 +193,8 @@ hipError_t append_dim(const KvView &c, int n, const void *k, KvStrides ks, const
 template <int D, typename T>
 hipError_t read_dim(const KvView &c, int n, void *k, KvStrides ks, void *v, KvStrides vs,
                     hipStream_t s) {
-  const int64_t vecs = (int64_t)c.B * n * c.H * 2, per = 256 / (D / 4);
-  const unsigned grid = (unsigned)((vecs + per - 1) / per);
+  const uint32_t vecs = (uint32_t)c.B * n * c.H * 2, per = 256 / (D / 4);
+  const uint32_t grid = (vecs + per - 1) / per;
   if (vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T)))
     read_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, (T *)k, ks, (T *)v, vs, vecs);
   else
