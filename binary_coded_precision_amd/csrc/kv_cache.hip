@@ -59,20 +59,31 @@ __device__ __forceinline__ void store4(T *p, const float (&x)[4]) {
   }
 }
 
-// Vector `vec` of a call over n tokens: K and V of (sequence, token, head), V last.
+// Vector `vec` of a call over n tokens of every sequence.  Four tokens that share a
+// block of V are neighbours, K before V, then heads: a block is written (and
+// read) by one wave or two of one workgroup.  A call of n tokens has quads_of(n)
+// quads a sequence, the first and last of which may be partly or wholly outside.
 struct Place {
   int b, i, h, slot;
-  bool v;
+  bool v, in;
 };
+__host__ __device__ __forceinline__ uint32_t quads_of(int n) { return ((uint32_t)n + 6) / 4; }
 __device__ __forceinline__ Place place(const KvView &c, int n, uint32_t vec) {
   Place p;
-  p.v = vec & 1;
-  const uint32_t at = (vec >> 1) / (uint32_t)c.H;
-  p.h = (int)((vec >> 1) - at * (uint32_t)c.H);
-  p.b = (int)(at / (uint32_t)n);
-  p.i = (int)(at - (uint32_t)p.b * (uint32_t)n);
-  p.slot = kv_len(c, p.b) - n + p.i;
+  const uint32_t quads = n == 1 ? 1 : quads_of(n);
+  const uint32_t t = n == 1 ? 0 : vec & 3, head = n == 1 ? vec : vec >> 2;
+  p.v = head & 1;
+  const uint32_t quad = (head >> 1) / (uint32_t)c.H;
+  p.h = (int)((head >> 1) - quad * (uint32_t)c.H);
+  p.b = (int)(quad / quads);
+  const int first = kv_len(c, p.b) - n;  // slot of token 0
+  p.i = (int)(quad - (uint32_t)p.b * quads) * 4 + (int)t - (n == 1 ? 0 : first & 3);
+  p.slot = first + p.i;
+  p.in = p.i >= 0 && p.i < n;
   return p;
+}
+__host__ __forceinline__ uint32_t vectors_of(const KvView &c, int n) {
+  return (uint32_t)c.B * c.H * 2 * (n == 1 ? 1 : quads_of(n) * 4);
 }
 
 // Bound by the bytes of the vectors read; every lane converts what it loads,
@@ -87,6 +98,7 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k
   const int i = threadIdx.x % L;
   if (vec >= vecs) return;  // whole groups of L lanes leave together
   const Place p = place(c, n, vec);
+  if (!p.in) return;
   const KvStrides st = p.v ? vs : ks;
   const T *src = (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4;
   float x[4];
@@ -151,6 +163,7 @@ __global__ __launch_bounds__(256) void read_kernel(KvView c, int n, T *k, KvStri
   const int i = threadIdx.x % L;
   if (vec >= vecs) return;
   const Place p = place(c, n, vec);
+  if (!p.in) return;
   const KvStrides st = p.v ? vs : ks;
   T *dst = (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4;
   const int64_t token = p.slot < 0 ? -1 : kv_token(c, p.b, p.h, p.slot);
@@ -179,7 +192,7 @@ template <int D, typename T>
 hipError_t append_dim(const KvView &c, int n, const void *k, KvStrides ks, const void *v,
                       KvStrides vs, const int32_t *positions, float *weights, int32_t *pos,
                       hipStream_t s) {
-  const uint32_t vecs = (uint32_t)c.B * n * c.H * 2, per = 256 / (D / 4);
+  const uint32_t vecs = vectors_of(c, n), per = 256 / (D / 4);
   const uint32_t grid = (vecs + per - 1) / per;
   if (vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T)))
     append_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, (const T *)k, ks, (const T *)v, vs,
@@ -193,7 +206,7 @@ hipError_t append_dim(const KvView &c, int n, const void *k, KvStrides ks, const
 template <int D, typename T>
 hipError_t read_dim(const KvView &c, int n, void *k, KvStrides ks, void *v, KvStrides vs,
                     hipStream_t s) {
-  const uint32_t vecs = (uint32_t)c.B * n * c.H * 2, per = 256 / (D / 4);
+  const uint32_t vecs = vectors_of(c, n), per = 256 / (D / 4);
   const uint32_t grid = (vecs + per - 1) / per;
   if (vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T)))
     read_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, (T *)k, ks, (T *)v, vs, vecs);
@@ -219,7 +232,10 @@ __device__ __forceinline__ uint32_t order_of(float w, bool late) {
 }
 
 constexpr int kEvictThreads = 1024, kEvictWaves = kEvictThreads / 64;
-constexpr int kCopies = 16;  // of the histogram, so that lanes rarely meet in a counter
+constexpr int kDigit = 12, kBins = 1 << kDigit;
+constexpr int kRank = 256;   // slots left that are ranked against each other
+constexpr int kFew = 4;      // evicted slots that are looked for one by one
+constexpr int kInPlace = 64;  // moves that the selecting workgroup makes itself
 
 struct EvictArgs {
   KvView c;
@@ -240,20 +256,81 @@ __device__ __forceinline__ uint32_t below(uint64_t ballot) {
                                    __builtin_amdgcn_mbcnt_lo((uint32_t)ballot, 0));
 }
 
+// A slot's rank value: its order, then the lower slot; no two are alike.
+__device__ __forceinline__ uint64_t rank_of(uint32_t order, int slot) {
+  return (uint64_t)order << 32 | (0xffffffffu - (uint32_t)slot);
+}
+
+// Moves [k0, k0 + N) of a row of `count`, D/4 lanes (lane i of them): all loads are
+// in flight before the first is stored.  What is read lies in slots that no
+// move writes.
+template <int D, int N>
+__device__ __forceinline__ void move_tokens(const EvictArgs &a, int row, const int2 *moves, int k0,
+                                            int count, int i) {
+  const int b = row / a.c.H, h = row % a.c.H;
+  const int64_t at = (int64_t)row * a.c.room();
+  int2 mv[N];
+  int64_t from[N], to[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) mv[k] = moves[min(k0 + k, count - 1)];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    from[k] = kv_token(a.c, b, h, mv[k].x);
+    to[k] = kv_token(a.c, b, h, mv[k].y);
+    if (to[k] < 0) from[k] = -1;
+  }
+  uint16_t ck[N], cv[N];
+  uint2 cs[N];
+  float cw[N];
+  int32_t cp[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int64_t t = max(from[k], (int64_t)0);
+    ck[k] = *reinterpret_cast<const uint16_t *>(a.c.k + k_byte<D>(t, i));
+    cv[k] = *reinterpret_cast<const uint16_t *>(a.c.v + v_byte<D>(t, i));
+    cs[k] = *reinterpret_cast<const uint2 *>(a.c.scales + t * 4);
+    cw[k] = a.weights[at + mv[k].x];
+    cp[k] = a.pos[at + mv[k].x];
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (k0 + k >= count) break;
+    if (from[k] >= 0) {
+      *reinterpret_cast<uint16_t *>(a.c.k + k_byte<D>(to[k], i)) = ck[k];
+      *reinterpret_cast<uint16_t *>(a.c.v + v_byte<D>(to[k], i)) = cv[k];
+      if (i == 0) *reinterpret_cast<uint2 *>(a.c.scales + to[k] * 4) = cs[k];
+    }
+    if (i == 0) {
+      a.weights_out[at + mv[k].y] = cw[k];
+      a.pos_out[at + mv[k].y] = cp[k];
+    }
+  }
+}
+
 // One workgroup a row.  A wave has 256 Q slots in a row, a thread the orders of 4 Q
 // of them in registers, slot 256 q + 4 lane + e of the wave's, so that reads are
 // wide and coalesced; rows with room for more than the workgroup holds (ONCE is
 // false) go through all steps in rounds, which read weights and positions again.
-// A radix select over the orders, eight bits a pass, finds the last one kept and
-// ends early where a whole bin is; ballots then number what moves in slot order.
-template <int Q, bool ONCE>
+//
+// The row's smallest kept rank value is found, and ballots then number what
+// moves in slot order.  Up to kFew evicted slots (a decode loop's step) are found
+// as so many minima.  Otherwise a radix select takes 12 bits a pass, until
+// a bin is kept whole or holds at most kRank slots, which are ranked against each
+// other; one pass is the rule, and ties of all bits only add passes over the slots.
+// One compute unit's vector ALUs bound it (an operation on each of 32768 slots
+// takes 0.2 us), hence few operations a slot and pass.
+//
+// D > 0: there are at most kInPlace moves, made here; lens_out is then not lens.
+template <int Q, bool ONCE, int D>
 __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   constexpr int kRound = 4 * Q * kEvictThreads;
-  __shared__ uint32_t hist[256 * kCopies];
-  __shared__ uint32_t total[256];
+  __shared__ __align__(16) uint32_t hist[kBins];
+  __shared__ uint64_t cand[kRank];
+  __shared__ uint64_t least[kEvictWaves];
   __shared__ int tmp[kEvictWaves];
-  __shared__ uint32_t sums[3][kEvictWaves];
-  __shared__ uint32_t picked, above, inside;
+  __shared__ uint32_t sums[2][kEvictWaves];
+  __shared__ uint32_t picked, above, inside, listed;
+  __shared__ uint64_t edge_at;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = blockIdx.x, b = row / a.c.H;
@@ -263,28 +340,36 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   const float *w = a.weights + at;
   const int32_t *pos = a.pos + at;
   const int first = wave * 256 * Q + lane * 4;  // of the thread's slots, in a round
+  if (D > 0 && tid == 0 && row % a.c.H == 0) a.lens_out[b] = m;
 
   // Rows start at multiples of 16 slots and end at one, so a read of 4 from a
   // multiple of 4 below L stays in its row.
-  int newest = INT32_MIN;
-  for (int s0 = first; s0 < end + first; s0 += kRound) {
-    int4 v[Q];
+  float4 wv[Q];
+  int4 pv[Q];
+  auto read = [&](int s0, bool both) {
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-      if (s0 + 256 * q < L) v[q] = *reinterpret_cast<const int4 *>(pos + s0 + 256 * q);
+      if (s0 + 256 * q < L) {
+        pv[q] = *reinterpret_cast<const int4 *>(pos + s0 + 256 * q);
+        if (both) wv[q] = *reinterpret_cast<const float4 *>(w + s0 + 256 * q);
+      }
+  };
+  int newest = INT32_MIN;
+  for (int s0 = first; s0 < end + first; s0 += kRound) {
+    read(s0, ONCE);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int s = s0 + 256 * q;
-      if (s < L) newest = max(newest, v[q].x);
-      if (s + 1 < L) newest = max(newest, v[q].y);
-      if (s + 2 < L) newest = max(newest, v[q].z);
-      if (s + 3 < L) newest = max(newest, v[q].w);
+      if (s < L) newest = max(newest, pv[q].x);
+      if (s + 1 < L) newest = max(newest, pv[q].y);
+      if (s + 2 < L) newest = max(newest, pv[q].z);
+      if (s + 3 < L) newest = max(newest, pv[q].w);
     }
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) newest = max(newest, __shfl_xor(newest, d));
   if (lane == 0) tmp[wave] = newest;
-  for (int i = tid; i < 256 * kCopies; i += kEvictThreads) hist[i] = 0;
+  reinterpret_cast<uint4 *>(hist)[tid] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   for (int i = 0; i < kEvictWaves; ++i) newest = max(newest, tmp[i]);
   const int64_t late_from = (int64_t)newest - a.recent;
@@ -294,18 +379,11 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   // overwritten by the moves.
   uint32_t key[Q][4];
   auto orders = [&](int s0, bool write) {
-    float4 x[Q];
-    int4 y[Q];
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (s0 + 256 * q < L) {
-        x[q] = *reinterpret_cast<const float4 *>(w + s0 + 256 * q);
-        y[q] = *reinterpret_cast<const int4 *>(pos + s0 + 256 * q);
-      }
+    if (!ONCE) read(s0, true);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const float xs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
-      const int32_t ys[4] = {y[q].x, y[q].y, y[q].z, y[q].w};
+      const float xs[4] = {wv[q].x, wv[q].y, wv[q].z, wv[q].w};
+      const int32_t ys[4] = {pv[q].x, pv[q].y, pv[q].z, pv[q].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int s = s0 + 256 * q + e;
@@ -326,201 +404,230 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
     if (tid == 0) a.count[row] = 0;
     return;
   }
+  int2 *mv = a.moves + (int64_t)row * a.most;
+  const int evicted = L - m;
 
-  uint32_t prefix = 0;
-  int left = m;  // still to be taken among the slots whose order starts with prefix
-  int shift = 24;
-  for (;; shift -= 8) {
-    for (int s0 = first; s0 < end + first; s0 += kRound) {
-      if (!ONCE) orders(s0, false);
+  // ---- the smallest rank value kept
+  uint64_t edge = 0;  // kept: rank values from here on
+  if (evicted <= kFew) {
+    for (int n = 0; n < evicted; ++n) {
+      uint64_t low = ~0ull;
+      for (int s0 = first; s0 < end + first; s0 += kRound) {
+        if (!ONCE) orders(s0, false);
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
+        for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t k = key[q][e];
-          if (s0 + 256 * q + e < L &&
-              (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))))
-            atomicAdd(&hist[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
-        }
-    }
-    __syncthreads();
-    {
-      // 4 threads a bin, which also clear the counters for the next pass
-      uint4 *h = reinterpret_cast<uint4 *>(hist) + tid;
-      const uint4 x = *h;
-      uint32_t t = x.x + x.y + x.z + x.w;
-      *h = make_uint4(0, 0, 0, 0);
-      t += __shfl_xor(t, 1);
-      t += __shfl_xor(t, 2);
-      if ((tid & 3) == 0) total[tid >> 2] = t;
-    }
-    __syncthreads();
-    if (wave == 0) {
-      // lane l sums bins 4l..4l+3; the bin where the count from the top passes `left`
-      uint32_t t[4], sum = 0;
-      for (int i = 0; i < 4; ++i) sum += t[i] = total[lane * 4 + i];
-      uint32_t up = sum;  // of this lane's bins and all above
+          for (int e = 0; e < 4; ++e) {
+            const int s = s0 + 256 * q + e;
+            const uint64_t v = rank_of(key[q][e], s);
+            if (s < L && v >= edge && v < low) low = v;
+          }
+      }
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = __shfl_down(up, d);
-        if (lane + d < 64) up += o;
+        const uint64_t o = __shfl_xor(low, d);
+        low = o < low ? o : low;
       }
-      uint32_t over = up - sum;
-      for (int i = 3; i >= 0; --i) {
-        if (over < (uint32_t)left && over + t[i] >= (uint32_t)left) {
-          picked = lane * 4 + i;
-          above = over;
-          inside = t[i];
+      __syncthreads();
+      if (lane == 0) least[wave] = low;
+      __syncthreads();
+      for (int i = 0; i < kEvictWaves; ++i) low = least[i] < low ? least[i] : low;
+      edge = low + 1;
+    }
+  } else {
+    uint32_t left = m;  // still to be taken among the values that start with edge
+    // the fifth pass at the latest ends it: its bins are of 16 values, all distinct
+    for (int shift = 64 - kDigit;; shift -= kDigit) {
+      const bool top = shift == 64 - kDigit;
+      for (int s0 = first; s0 < end + first; s0 += kRound) {
+        if (!ONCE) orders(s0, false);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int s = s0 + 256 * q + e;
+            if (top) {
+              if (s < L) atomicAdd(&hist[key[q][e] >> (32 - kDigit)], 1u);
+            } else {
+              const uint64_t v = rank_of(key[q][e], s);
+              if (s < L && (v >> shift) >> kDigit == (edge >> shift) >> kDigit)
+                atomicAdd(&hist[(v >> shift) & (kBins - 1)], 1u);
+            }
+          }
+      }
+      __syncthreads();
+      {
+        // from the top: thread t has bins 4 (1023 - t) .. + 3, and clears them
+        uint4 *h = reinterpret_cast<uint4 *>(hist) + (kEvictThreads - 1 - tid);
+        const uint4 x = *h;
+        *h = make_uint4(0, 0, 0, 0);
+        const uint32_t t[4] = {x.w, x.z, x.y, x.x};
+        const uint32_t sum = t[0] + t[1] + t[2] + t[3];
+        uint32_t up = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const uint32_t o = __shfl_up(up, d);
+          if (lane >= d) up += o;
         }
-        over += t[i];
+        if (lane == 63) sums[0][wave] = up;
+        if (tid == 0) listed = 0;
+        __syncthreads();
+        uint32_t over = up - sum;
+        for (int i = 0; i < wave; ++i) over += sums[0][i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (over < left && over + t[i] >= left) {
+            picked = 4 * (kEvictThreads - 1 - tid) + 3 - i;
+            above = over;
+            inside = t[i];
+          }
+          over += t[i];
+        }
+      }
+      __syncthreads();
+      edge |= (uint64_t)picked << shift;
+      left -= above;
+      if (inside == left) break;
+      if (inside <= kRank) {
+        // list what starts with edge; the left-th of them from the top is the last kept
+        for (int s0 = first; s0 < end + first; s0 += kRound) {
+          if (!ONCE) orders(s0, false);
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int s = s0 + 256 * q + e;
+              const uint64_t v = rank_of(key[q][e], s);
+              if (s < L && v >> shift == edge >> shift) cand[atomicAdd(&listed, 1u)] = v;
+            }
+        }
+        __syncthreads();
+        const uint32_t n = listed;
+        if (tid < (int)n) {
+          const uint64_t v = cand[tid];
+          uint32_t higher = 0;
+          for (uint32_t i = 0; i < n; ++i) higher += cand[i] > v;
+          if (higher == left - 1) edge_at = v;
+        }
+        __syncthreads();
+        edge = edge_at;
+        break;
       }
     }
-    __syncthreads();
-    prefix |= picked << shift;
-    left -= (int)above;
-    if (shift == 0 || (int)inside == left) break;
   }
 
-  // kept: every order above prefix's leading bits, and the first `left` slots at them
-  const uint32_t edge = prefix >> shift;
-  int2 *mv = a.moves + (int64_t)row * a.most;
-  uint32_t ties = 0, holes = 0, fills = 0;  // before this round
+  // ---- what moves, in slot order
+  const uint32_t edge_key = (uint32_t)(edge >> 32);
+  const int edge_slot = (int)min(0xffffffffu - (uint32_t)edge, 0x7fffffffu);
+  uint32_t holes = 0, fills = 0;  // before this round
   for (int s0 = first; s0 < end + first; s0 += kRound) {
     if (!ONCE) orders(s0, false);
-    uint32_t n = 0;
+    // 4 bits a q: evicted in front of m, kept behind it
+    uint32_t hole = 0, fill = 0, n_holes = 0, n_fills = 0;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        n += __popcll(__ballot(s0 + 256 * q + e < L && (key[q][e] >> shift) == edge));
-    if (lane == 0) sums[0][wave] = n;
-    __syncthreads();
-    uint32_t tie = ties;
-    for (int i = 0; i < kEvictWaves; ++i) {
-      const uint32_t x = sums[0][i];
-      tie += i < wave ? x : 0;
-      ties += x;
-    }
-    uint32_t hole = 0, fill = 0;  // 4 bits a q
-    uint32_t n_holes = 0, n_fills = 0;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      uint64_t eq[4];
-      uint32_t before = tie;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        eq[e] = __ballot(s0 + 256 * q + e < L && (key[q][e] >> shift) == edge);
-        before += below(eq[e]);
-        tie += __popcll(eq[e]);
-      }
-#pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int s = s0 + 256 * q + e;
-        const uint32_t k = key[q][e] >> shift;
-        const bool same = k == edge;
-        const bool kept = s < L && (k > edge || (same && before < (uint32_t)left));
-        before += s < L && same;
-        const bool ho = s < m && !kept, fi = s >= m && kept;
+        const uint32_t k = key[q][e];
+        const bool kept = k > edge_key || (k == edge_key && s <= edge_slot);
+        const bool ho = s < m && !kept, fi = s >= m && s < L && kept;
         hole |= (uint32_t)ho << (4 * q + e);
         fill |= (uint32_t)fi << (4 * q + e);
         n_holes += __popcll(__ballot(ho));
         n_fills += __popcll(__ballot(fi));
       }
-    }
+    __syncthreads();
     if (lane == 0) {
-      sums[1][wave] = n_holes;
-      sums[2][wave] = n_fills;
+      sums[0][wave] = n_holes;
+      sums[1][wave] = n_fills;
     }
     __syncthreads();
     uint32_t at_hole = holes, at_fill = fills;
     for (int i = 0; i < kEvictWaves; ++i) {
-      const uint32_t x = sums[1][i], y = sums[2][i];
+      const uint32_t x = sums[0][i], y = sums[1][i];
       at_hole += i < wave ? x : 0;
       at_fill += i < wave ? y : 0;
       holes += x;
       fills += y;
     }
-    if (n_holes + n_fills > 0) {
+    auto number = [&](uint32_t bits, uint32_t place, bool to) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        uint32_t h = at_hole, f = at_fill;
+        uint32_t n = place;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint64_t hb = __ballot(hole >> (4 * q + e) & 1);
-          const uint64_t fb = __ballot(fill >> (4 * q + e) & 1);
-          h += below(hb);
-          f += below(fb);
-          at_hole += __popcll(hb);
-          at_fill += __popcll(fb);
+          const uint64_t x = __ballot(bits >> (4 * q + e) & 1);
+          n += below(x);
+          place += __popcll(x);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int s = s0 + 256 * q + e;
-          if (hole >> (4 * q + e) & 1) mv[h++].y = s;
-          if (fill >> (4 * q + e) & 1) mv[f++].x = s;
-        }
+        for (int e = 0; e < 4; ++e)
+          if (bits >> (4 * q + e) & 1) {
+            (to ? mv[n].y : mv[n].x) = s0 + 256 * q + e;
+            ++n;
+          }
       }
-    }
+    };
+    if (n_holes > 0) number(hole, at_hole, true);
+    if (n_fills > 0) number(fill, at_fill, false);
   }
   if (tid == 0) a.count[row] = (int)holes;
+  if constexpr (D > 0) {
+    __syncthreads();  // the moves are this workgroup's own writes
+    const int count = (int)holes;
+    constexpr int kLanes = D / 4;
+    for (int k = tid / kLanes; k < count; k += kEvictThreads / kLanes)
+      move_tokens<D, 1>(a, row, mv, k, count, tid % kLanes);
+  }
 }
 
-// D/4 lanes a group of moves: four in a row, whose loads are all in flight before
-// the first is stored (they go to neighbouring slots, mostly).  A stride of the
-// grid over the row's moves, so that the host need not know their number.
+// D/4 lanes a group of moves: four in a row (they go to neighbouring slots,
+// mostly).  A stride of the grid over the row's moves, so that the host need not
+// know their number.
 constexpr int kMoves = 4;
 template <int D>
 __global__ __launch_bounds__(256) void move_kernel(EvictArgs a) {
   constexpr int L = D / 4;
-  const int row = blockIdx.x, b = row / a.c.H, h = row % a.c.H;
-  const int i = threadIdx.x % L;
-  if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+  const int row = blockIdx.x, b = row / a.c.H;
+  if (row % a.c.H == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     // the only place that reads lens after the selection, so it may be lens_out
     const int len = kv_len(a.c, b);
     a.lens_out[b] = min(len, a.keep);
   }
-  const int64_t at = (int64_t)row * a.c.room();
   const int count = a.count[row];
   const int2 *moves = a.moves + (int64_t)row * a.most;
   const int group = blockIdx.y * (256 / L) + threadIdx.x / L;
-  for (int k0 = group * kMoves; k0 < count; k0 += gridDim.y * (256 / L) * kMoves) {
-    int2 mv[kMoves];
-    int64_t from[kMoves], to[kMoves];
-#pragma unroll
-    for (int k = 0; k < kMoves; ++k) mv[k] = moves[min(k0 + k, count - 1)];
-#pragma unroll
-    for (int k = 0; k < kMoves; ++k) {
-      from[k] = kv_token(a.c, b, h, mv[k].x);
-      to[k] = kv_token(a.c, b, h, mv[k].y);
-      if (to[k] < 0) from[k] = -1;
-    }
-    uint16_t ck[kMoves], cv[kMoves];
-    uint2 cs[kMoves];
-    float cw[kMoves];
-    int32_t cp[kMoves];
-#pragma unroll
-    for (int k = 0; k < kMoves; ++k) {
-      const int64_t t = max(from[k], (int64_t)0);
-      ck[k] = *reinterpret_cast<const uint16_t *>(a.c.k + k_byte<D>(t, i));
-      cv[k] = *reinterpret_cast<const uint16_t *>(a.c.v + v_byte<D>(t, i));
-      cs[k] = *reinterpret_cast<const uint2 *>(a.c.scales + t * 4);
-      cw[k] = a.weights[at + mv[k].x];
-      cp[k] = a.pos[at + mv[k].x];
-    }
-#pragma unroll
-    for (int k = 0; k < kMoves; ++k) {
-      if (k0 + k >= count) break;
-      if (from[k] >= 0) {
-        *reinterpret_cast<uint16_t *>(a.c.k + k_byte<D>(to[k], i)) = ck[k];
-        *reinterpret_cast<uint16_t *>(a.c.v + v_byte<D>(to[k], i)) = cv[k];
-        if (i == 0) *reinterpret_cast<uint2 *>(a.c.scales + to[k] * 4) = cs[k];
-      }
-      if (i == 0) {
-        a.weights_out[at + mv[k].y] = cw[k];
-        a.pos_out[at + mv[k].y] = cp[k];
-      }
-    }
+  for (int k0 = group * kMoves; k0 < count; k0 += gridDim.y * (256 / L) * kMoves)
+    move_tokens<D, kMoves>(a, row, moves, k0, count, threadIdx.x % L);
+}
+
+template <int D>
+hipError_t evict_dim(const EvictArgs &a, hipStream_t s) {
+  const int BH = a.c.B * a.c.H, room = a.c.room();
+  const bool once = room <= 32 * kEvictThreads, small = room <= 4 * kEvictThreads;
+  if (a.most <= kInPlace && once && a.lens_out != a.c.lens) {
+    if (small)
+      select_kernel<1, true, D><<<BH, kEvictThreads, 0, s>>>(a);
+    else
+      select_kernel<8, true, D><<<BH, kEvictThreads, 0, s>>>(a);
+    return hipGetLastError();
   }
+  if (small)
+    select_kernel<1, true, 0><<<BH, kEvictThreads, 0, s>>>(a);
+  else if (once)
+    select_kernel<8, true, 0><<<BH, kEvictThreads, 0, s>>>(a);
+  else
+    select_kernel<4, false, 0><<<BH, kEvictThreads, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int per = 256 / (D / 4) * kMoves;
+  // about 4096 workgroups in all: enough to fill the card several times over
+  const int most_chunks = BH >= 4096 ? 1 : 4096 / BH;
+  int chunks = (a.most + per - 1) / per;
+  chunks = chunks < 1 ? 1 : (chunks > most_chunks ? most_chunks : chunks);
+  move_kernel<D><<<dim3(BH, chunks), 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 int most_moves(int room, int keep) { return keep < room - keep ? keep : room - keep; }
@@ -564,27 +671,7 @@ hipError_t launch_kv_evict(const KvView &c, int D, int keep, int recent, const f
   a.most = keep < room ? most_moves(room, keep) : 0;
   a.moves = static_cast<int2 *>(ws);
   a.count = reinterpret_cast<int32_t *>(a.moves + (size_t)BH * a.most);
-  if (room <= 4 * kEvictThreads)
-    select_kernel<1, true><<<BH, kEvictThreads, 0, s>>>(a);
-  else if (room <= 32 * kEvictThreads)
-    select_kernel<8, true><<<BH, kEvictThreads, 0, s>>>(a);
-  else
-    select_kernel<4, false><<<BH, kEvictThreads, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int per = 256 / (D / 4) * kMoves;
-  // about 4096 workgroups in all: enough to fill the card several times over
-  const int most_chunks = BH >= 4096 ? 1 : 4096 / BH;
-  int chunks = (a.most + per - 1) / per;
-  chunks = chunks < 1 ? 1 : (chunks > most_chunks ? most_chunks : chunks);
-  const dim3 grid(BH, chunks);
-  if (D == 64)
-    move_kernel<64><<<grid, 256, 0, s>>>(a);
-  else if (D == 128)
-    move_kernel<128><<<grid, 256, 0, s>>>(a);
-  else
-    move_kernel<256><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  return D == 64 ? evict_dim<64>(a, s) : D == 128 ? evict_dim<128>(a, s) : evict_dim<256>(a, s);
 }
 
 }  // namespace bcq

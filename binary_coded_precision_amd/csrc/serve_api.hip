@@ -96,7 +96,8 @@ bcq_status check_vectors(const bcq_kv_cache *c, int32_t n, const void *k, const 
                          bcq_dtype dtype) {
   BCQ_TRY(check_cache(c));
   if (!dtype_valid(dtype) || n < 0 || n > BCQ_KV_MAX_TOKENS) return BCQ_ERR_INVALID_ARG;
-  if ((int64_t)c->batch * c->heads * n >= (int64_t)1 << 30) return BCQ_ERR_INVALID_ARG;
+  // vectors are counted in 32 bits
+  if ((int64_t)c->batch * c->heads * ((int64_t)n + 6) > (int64_t)1 << 30) return BCQ_ERR_INVALID_ARG;
   if (n > 0 && (k == nullptr || v == nullptr)) return BCQ_ERR_INVALID_ARG;
   if (!aligned(k, dtype_size(dtype)) || !aligned(v, dtype_size(dtype))) return BCQ_ERR_ALIGNMENT;
   return BCQ_OK;
