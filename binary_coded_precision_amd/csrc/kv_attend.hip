@@ -95,16 +95,19 @@ __device__ __forceinline__ void load_words(uint32_t (&dst)[N], const uint8_t *sr
 
 // Where the two tiles of tokens t..t+31 lie.  The second is the first again where
 // the sequence ends before it; an entry that names no page is never followed.
+// The table is read through the scalar cache: as a vector load it would return
+// behind the tiles asked for before it.
 struct Where {
   int64_t at[2];
 };
+typedef const __attribute__((address_space(4))) int32_t *ScalarInts;
 __device__ __forceinline__ Where where(const KvView &c, int b, int h, int t, int len) {
+  const ScalarInts table = (ScalarInts)(uintptr_t)(c.table + (int64_t)b * c.max_pages);
   Where w;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const int tok = t + 16 * s < len ? t + 16 * s : t;
-    const int page = __builtin_amdgcn_readfirstlane(
-        c.table[(int64_t)b * c.max_pages + (tok >> c.page_log)]);
+    const int tok = __builtin_amdgcn_readfirstlane(t + 16 * s < len ? t + 16 * s : t);
+    const int page = table[tok >> c.page_log];
     const int safe = (unsigned)page < (unsigned)c.num_pages ? page : 0;
     w.at[s] = (((int64_t)safe * c.H + h) << c.page_log) + (tok & ((1 << c.page_log) - 1));
   }
@@ -522,10 +525,15 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
     for (int d = 0; d < D / 16; ++d) A.o[ct][d] = float4v{0.f, 0.f, 0.f, 0.f};
   }
 
-  // the next tiles are asked for as soon as the registers of these are free
+  // the next tiles are asked for as soon as the registers of these are free, and
+  // the place of those after them is looked up a step earlier still
+  auto place_of = [&](int ti) { return where(a.c, b, h, (ti < tile_end ? ti : tile) * 32, L); };
+  Where ahead{};
+  if (tile < tile_end) ahead = place_of(tile + WT);
   while (tile < tile_end) {
     const int next = tile + WT;
-    const Where w = where(a.c, b, h, (next < tile_end ? next : tile) * 32, L);
+    const Where w = ahead;
+    ahead = place_of(next + WT);
     float4v S[2][CT];
     raw_scores<D, CT, F32>(S, T, Q);
     load_k(T, a.c, w, lane);

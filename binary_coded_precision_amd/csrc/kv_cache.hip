@@ -233,6 +233,7 @@ __device__ __forceinline__ uint32_t order_of(float w, bool late) {
 
 constexpr int kEvictThreads = 1024, kEvictWaves = kEvictThreads / 64;
 constexpr int kDigit = 12, kBins = 1 << kDigit;
+constexpr int kList = 2048;  // slots left that are listed and further passes go over
 constexpr int kRank = 256;   // slots left that are ranked against each other
 constexpr int kFew = 4;      // evicted slots that are looked for one by one
 constexpr int kInPlace = 64;  // moves that the selecting workgroup makes itself
@@ -316,7 +317,8 @@ __device__ __forceinline__ void move_tokens(const EvictArgs &a, int row, const i
 // moves in slot order.  Up to kFew evicted slots (a decode loop's step) are found
 // as so many minima.  Otherwise a radix select takes 12 bits a pass, until
 // a bin is kept whole or holds at most kRank slots, which are ranked against each
-// other; one pass is the rule, and ties of all bits only add passes over the slots.
+// other; passes after the first go over a list of the slots left once it holds
+// them, so that one pass over all slots is the rule.
 // One compute unit's vector ALUs bound it (an operation on each of 32768 slots
 // takes 0.2 us), hence few operations a slot and pass.
 //
@@ -325,12 +327,13 @@ template <int Q, bool ONCE, int D>
 __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   constexpr int kRound = 4 * Q * kEvictThreads;
   __shared__ __align__(16) uint32_t hist[kBins];
-  __shared__ uint64_t cand[kRank];
+  __shared__ uint64_t list[kList], cand[kRank];
   __shared__ uint64_t least[kEvictWaves];
   __shared__ int tmp[kEvictWaves];
   __shared__ uint32_t sums[2][kEvictWaves];
-  __shared__ uint32_t picked, above, inside, listed;
+  __shared__ uint32_t picked, above, inside, listed, ranked;
   __shared__ uint64_t edge_at;
+  __shared__ int few_count;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = blockIdx.x, b = row / a.c.H;
@@ -372,12 +375,15 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   reinterpret_cast<uint4 *>(hist)[tid] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   for (int i = 0; i < kEvictWaves; ++i) newest = max(newest, tmp[i]);
-  const int64_t late_from = (int64_t)newest - a.recent;
+  // newest is at least every position, so their distance fits 32 bits
+  auto is_late = [&](int32_t p) { return (uint32_t)newest - (uint32_t)p < (uint32_t)a.recent; };
 
   // The orders of the round whose slots start at s0 for this thread.  On the
   // way what is in front goes to the output; what is evicted of it is
   // overwritten by the moves.
   uint32_t key[Q][4];
+  const bool apart = a.weights_out != a.weights || a.pos_out != a.pos;
+  const bool wide = (((uintptr_t)a.weights_out | (uintptr_t)a.pos_out) & 15) == 0;
   auto orders = [&](int s0, bool write) {
     if (!ONCE) read(s0, true);
 #pragma unroll
@@ -385,17 +391,21 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
       const float xs[4] = {wv[q].x, wv[q].y, wv[q].z, wv[q].w};
       const int32_t ys[4] = {pv[q].x, pv[q].y, pv[q].z, pv[q].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int s = s0 + 256 * q + e;
-        key[q][e] = order_of(xs[e], ys[e] > late_from);
-        if (write && s < m) {
-          a.weights_out[at + s] = xs[e];
-          a.pos_out[at + s] = ys[e];
-        }
+      for (int e = 0; e < 4; ++e) key[q][e] = order_of(xs[e], is_late(ys[e]));
+      const int s = s0 + 256 * q;
+      if (write && s + 3 < m && wide) {
+        *reinterpret_cast<float4 *>(a.weights_out + at + s) = wv[q];
+        *reinterpret_cast<int4 *>(a.pos_out + at + s) = pv[q];
+      } else if (write) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (s + e < m) {
+            a.weights_out[at + s + e] = xs[e];
+            a.pos_out[at + s + e] = ys[e];
+          }
       }
     }
   };
-  const bool apart = a.weights_out != a.weights || a.pos_out != a.pos;
   if (ONCE)
     orders(first, apart);
   else if (apart)
@@ -410,6 +420,8 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   // ---- the smallest rank value kept
   uint64_t edge = 0;  // kept: rank values from here on
   if (evicted <= kFew) {
+    uint32_t out = 0;  // evicted slots behind m, by their distance from it
+    int front[kFew], fronts = 0;
     for (int n = 0; n < evicted; ++n) {
       uint64_t low = ~0ull;
       for (int s0 = first; s0 < end + first; s0 += kRound) {
@@ -433,12 +445,37 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
       __syncthreads();
       for (int i = 0; i < kEvictWaves; ++i) low = least[i] < low ? least[i] : low;
       edge = low + 1;
+      const int s = (int)(0xffffffffu - (uint32_t)low);
+      if (s >= m)
+        out |= 1u << (s - m);
+      else if (tid == 0) {
+        int k = fronts++;  // into place among the lower ones
+        for (; k > 0 && front[k - 1] > s; --k) front[k] = front[k - 1];
+        front[k] = s;
+      }
     }
+    if (tid == 0) {
+      for (int k = 0, s = 0; k < fronts; ++k, ++s) {
+        while (out >> s & 1) ++s;
+        mv[k] = make_int2(m + s, front[k]);
+      }
+      a.count[row] = few_count = fronts;
+    }
+    if constexpr (D > 0) {
+      __syncthreads();
+      for (int k = tid / (D / 4); k < few_count; k += kEvictThreads / (D / 4))
+        move_tokens<D, 1>(a, row, mv, k, few_count, tid % (D / 4));
+    }
+    return;
   } else {
-    uint32_t left = m;  // still to be taken among the values that start with edge
-    // the fifth pass at the latest ends it: its bins are of 16 values, all distinct
-    for (int shift = 64 - kDigit;; shift -= kDigit) {
-      const bool top = shift == 64 - kDigit;
+    uint32_t left = m;      // still to be taken among the values that start with edge
+    bool in_list = false;   // those are in `list`
+    // every slot's rank value, or those listed
+    auto each = [&](auto &&visit) {
+      if (in_list) {
+        for (int i = tid; i < (int)listed; i += kEvictThreads) visit(list[i]);
+        return;
+      }
       for (int s0 = first; s0 < end + first; s0 += kRound) {
         if (!ONCE) orders(s0, false);
 #pragma unroll
@@ -446,15 +483,19 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int s = s0 + 256 * q + e;
-            if (top) {
-              if (s < L) atomicAdd(&hist[key[q][e] >> (32 - kDigit)], 1u);
-            } else {
-              const uint64_t v = rank_of(key[q][e], s);
-              if (s < L && (v >> shift) >> kDigit == (edge >> shift) >> kDigit)
-                atomicAdd(&hist[(v >> shift) & (kBins - 1)], 1u);
-            }
+            if (s < L) visit(rank_of(key[q][e], s));
           }
       }
+    };
+    // the fifth pass at the latest ends it: its bins are of 16 values, all distinct
+    for (int shift = 64 - kDigit;; shift -= kDigit) {
+      if (shift == 64 - kDigit)
+        each([&](uint64_t v) { atomicAdd(&hist[v >> (64 - kDigit)], 1u); });
+      else
+        each([&](uint64_t v) {
+          if ((v >> shift) >> kDigit == (edge >> shift) >> kDigit)
+            atomicAdd(&hist[(v >> shift) & (kBins - 1)], 1u);
+        });
       __syncthreads();
       {
         // from the top: thread t has bins 4 (1023 - t) .. + 3, and clears them
@@ -470,7 +511,8 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
           if (lane >= d) up += o;
         }
         if (lane == 63) sums[0][wave] = up;
-        if (tid == 0) listed = 0;
+        if (tid == 0) ranked = 0;
+        if (tid == 0 && !in_list) listed = 0;
         __syncthreads();
         uint32_t over = up - sum;
         for (int i = 0; i < wave; ++i) over += sums[0][i];
@@ -489,20 +531,12 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
       left -= above;
       if (inside == left) break;
       if (inside <= kRank) {
-        // list what starts with edge; the left-th of them from the top is the last kept
-        for (int s0 = first; s0 < end + first; s0 += kRound) {
-          if (!ONCE) orders(s0, false);
-#pragma unroll
-          for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int s = s0 + 256 * q + e;
-              const uint64_t v = rank_of(key[q][e], s);
-              if (s < L && v >> shift == edge >> shift) cand[atomicAdd(&listed, 1u)] = v;
-            }
-        }
+        // the left-th from the top of what starts with edge is the last kept
+        each([&](uint64_t v) {
+          if (v >> shift == edge >> shift) cand[atomicAdd(&ranked, 1u)] = v;
+        });
         __syncthreads();
-        const uint32_t n = listed;
+        const uint32_t n = ranked;
         if (tid < (int)n) {
           const uint64_t v = cand[tid];
           uint32_t higher = 0;
@@ -512,6 +546,13 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
         __syncthreads();
         edge = edge_at;
         break;
+      }
+      if (inside <= kList && !in_list) {
+        each([&](uint64_t v) {
+          if (v >> shift == edge >> shift) list[atomicAdd(&listed, 1u)] = v;
+        });
+        __syncthreads();
+        in_list = true;
       }
     }
   }
@@ -618,7 +659,7 @@ hipError_t evict_dim(const EvictArgs &a, hipStream_t s) {
   else if (once)
     select_kernel<8, true, 0><<<BH, kEvictThreads, 0, s>>>(a);
   else
-    select_kernel<4, false, 0><<<BH, kEvictThreads, 0, s>>>(a);
+    select_kernel<2, false, 0><<<BH, kEvictThreads, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int per = 256 / (D / 4) * kMoves;
