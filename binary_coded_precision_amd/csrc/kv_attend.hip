@@ -48,7 +48,7 @@ namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef float float2v __attribute__((ext_vector_type(2)));
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr float kNegInf = -INFINITY;
@@ -201,48 +201,70 @@ struct Queries {
   float row_scale[F32 ? CT : 1];
 };
 
+// The queries as they lie in memory: their loads can be under way long before
+// what converts them.
 template <int D, int CT, bool F32>
-__device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q, const AttendArgs &a, int b,
-                                             int h, int row0, int R, int lane) {
-  const int g = lane >> 4;
+struct RawQueries {
+  float4v f[F32 ? CT : 1][F32 ? D / 16 : 1];
+  half8 h[F32 ? 1 : CT][F32 ? 1 : D / 32];
+};
+template <int D, int CT, bool F32>
+__device__ __forceinline__ void fetch_queries(RawQueries<D, CT, F32> &raw, const AttendArgs &a,
+                                              int b, int h, int row0, int R, int lane) {
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int row = min(row0 + ct * 16 + (lane & 15), R - 1);
+    const int i = row / a.G, hq = h * a.G + row - i * a.G;
+    const int64_t at = b * a.qs.batch + i * a.qs.token + hq * a.qs.head + (lane >> 4) * (D / 4);
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      if constexpr (F32) {
+        const float *q = static_cast<const float *>(a.q) + at + w * 8;
+        if (a.q_wide) {
+          raw.f[ct][2 * w] = reinterpret_cast<const float4v *>(q)[0];
+          raw.f[ct][2 * w + 1] = reinterpret_cast<const float4v *>(q)[1];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) raw.f[ct][2 * w + (e >> 2)][e & 3] = q[e];
+        }
+      } else {
+        const _Float16 *q = static_cast<const _Float16 *>(a.q) + at + w * 8;
+        if (a.q_wide) {
+          raw.h[ct][w] = *reinterpret_cast<const half8 *>(q);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) raw.h[ct][w][e] = q[e];
+        }
+      }
+    }
+  }
+}
+
+// Rows past R become zeros: a tile's spare columns.
+template <int D, int CT, bool F32>
+__device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q,
+                                             const RawQueries<D, CT, F32> &raw, bool negate,
+                                             int row0, int R, int lane) {
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     const int row = row0 + ct * 16 + (lane & 15);
     float x[D / 32][8];
-    if (row < R) {
-      const int i = row / a.G, hq = h * a.G + row % a.G;
-      const int64_t at = b * a.qs.batch + i * a.qs.token + hq * a.qs.head + g * (D / 4);
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        if (a.q_wide && F32) {
-          const float4v *p =
-              reinterpret_cast<const float4v *>(static_cast<const float *>(a.q) + at + w * 8);
+    for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[w][e] = p[e >> 2][e & 3];
-        } else if (a.q_wide) {
-          const half8 v =
-              *reinterpret_cast<const half8 *>(static_cast<const _Float16 *>(a.q) + at + w * 8);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[w][e] = (float)v[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[w][e] = F32 ? static_cast<const float *>(a.q)[at + w * 8 + e]
-                          : (float)static_cast<const _Float16 *>(a.q)[at + w * 8 + e];
-        }
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (F32)
+          x[w][e] = raw.f[ct][2 * w + (e >> 2)][e & 3];
+        else
+          x[w][e] = (float)raw.h[ct][w][e];
+        if (row >= R) x[w][e] = 0.f;
       }
-    } else {
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[w][e] = 0.f;
-    }
     float sum = 0.f, top = 0.f;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[w][e] = a.negate ? -x[w][e] : x[w][e];
+        x[w][e] = negate ? -x[w][e] : x[w][e];
         sum += x[w][e];
         top = fmaxf(top, fabsf(x[w][e]));
       }
@@ -353,6 +375,27 @@ __device__ __forceinline__ void mask_scores(float4v (&S)[2][CT], Tiles<D> &T, in
     }
 }
 
+// log2 of an fp16 from its bits, to a tenth, plus 15 (the exponent's bias).
+__device__ __forceinline__ float rough_log2(uint32_t half) { return (float)half * (1.f / 1024.f); }
+
+__device__ __forceinline__ ushort2v pair16(uint32_t w) {
+  union {
+    uint32_t u;
+    ushort2v h;
+  } x;
+  x.u = w;
+  return x.h;
+}
+
+// fp16(p * the lower half of w) to the lower or upper half of `to`, one rounding
+// and one instruction.
+__device__ __forceinline__ void scaled_low(uint32_t &to, float p, uint32_t w) {
+  asm("v_fma_mixlo_f16 %0, %1, %2, 0 op_sel_hi:[0,1,0]" : "=v"(to) : "v"(p), "v"(w));
+}
+__device__ __forceinline__ void scaled_high(uint32_t &to, float p, uint32_t w) {
+  asm("v_fma_mixhi_f16 %0, %1, %2, 0 op_sel_hi:[0,1,0]" : "+v"(to) : "v"(p), "v"(w));
+}
+
 // The softmax's step over 32 tokens: raises the rows' references, rescales, adds
 // to their sums and leaves probability times V scale in P.
 template <int D, int CT, bool TWO>
@@ -360,26 +403,36 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, half8 (&P)[CT],
                                               half8 (&Plo)[TWO ? CT : 1],
                                               const float4v (&S)[2][CT], const Tiles<D> &T,
                                               float unit) {
-  float top[CT];
+  // The tile's largest score and largest V scale together bound its terms; only
+  // where that asks for it are the terms themselves looked at.
+  ushort2v scales = pair16(T.m[0][1]);
+  float high[CT];
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) top[ct] = kNegInf;
+  for (int ct = 0; ct < CT; ++ct) high[ct] = S[0][ct][0];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // the V scale's bits over 1024: its log2 to a tenth, plus 15
-      const float lv = (float)(T.m[s][2 * i + 1] & 0xffffu) * (1.f / 1024.f);
+      scales = __builtin_elementwise_max(scales, pair16(T.m[s][2 * i + 1]));
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) top[ct] = fmaxf(top[ct], fmaf(S[s][ct][i], unit, lv));
+      for (int ct = 0; ct < CT; ++ct) high[ct] = fmaxf(high[ct], S[s][ct][i]);
     }
+  const float lv_most = rough_log2((uint32_t)scales[0]);
   bool raise = false;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) raise |= top[ct] > A.m[ct] + (kRaise + kSlack);
+  for (int ct = 0; ct < CT; ++ct)
+    raise |= fmaf(high[ct], unit, lv_most) > A.m[ct] + (kRaise + kSlack);
   if (__any(raise)) {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
+      float top = kNegInf;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = fmaxf(top, fmaf(S[s][ct][i], unit, rough_log2(T.m[s][2 * i + 1] & 0xffffu)));
       // each row by its own scores, so that no row depends on its neighbours
-      const float z = group_max(top[ct]);
+      const float z = group_max(top);
       const float m = z > A.m[ct] + (kRaise + kSlack) ? z - kRaise : A.m[ct];
       const float f = m == A.m[ct] ? 1.f : exp2f(A.m[ct] - m);
       A.m[ct] = m;
@@ -395,6 +448,7 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, half8 (&P)[CT],
   float m[CT];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) m[ct] = fmaxf(A.m[ct], -3.0e38f);
+  Frag single[CT];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -406,18 +460,24 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, half8 (&P)[CT],
         const float p = __builtin_amdgcn_exp2f(fmaf(S[s][ct][i], unit, -m[ct]));
         A.l[ct] += p;
         A.z[ct] = fmaf(p, mid, A.z[ct]);
-        float pv = p * (float)f[0];
         if constexpr (TWO) {
+          float pv = p * (float)f[0];
           // one value for both parts: the product and its rounding could be fused
           asm volatile("" : "+v"(pv));
-          const _Float16 high = (_Float16)pv;
-          P[ct][4 * s + i] = high;
-          Plo[ct][4 * s + i] = (_Float16)(pv - (float)high);
+          const _Float16 part = (_Float16)pv;
+          P[ct][4 * s + i] = part;
+          Plo[ct][4 * s + i] = (_Float16)(pv - (float)part);
+        } else if (i & 1) {
+          scaled_high(single[ct].w[2 * s + (i >> 1)], p, T.m[s][2 * i + 1]);
         } else {
-          P[ct][4 * s + i] = (_Float16)pv;
+          scaled_low(single[ct].w[2 * s + (i >> 1)], p, T.m[s][2 * i + 1]);
         }
       }
     }
+  if constexpr (!TWO) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) P[ct] = single[ct].h;
+  }
 }
 
 template <int D, int CT, bool F32, bool TWO>
@@ -488,8 +548,10 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
   const int h = blockIdx.x % BH % a.c.H;
   const int b = (blockIdx.x % BH / a.c.H + split * ((a.c.B + splits - 1) / splits)) % a.c.B;
   const int bh = b * a.c.H + h;
-  const int L = kv_len(a.c, b);
   const int row0 = (rb * WR + wr) * CT * 16;
+  RawQueries<D, CT, F32> raw;
+  fetch_queries<D, CT, F32>(raw, a, b, h, row0, R, lane);
+  const int L = kv_len(a.c, b);
 
   // tokens of these rows and of this split
   int tile_end = 0, tile = 0, free_end = 0;
@@ -510,7 +572,7 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
   }
 
   Queries<D, CT, F32> Q;
-  load_queries<D, CT, F32>(Q, a, b, h, row0, R, lane);
+  load_queries<D, CT, F32>(Q, raw, a.negate, row0, R, lane);
   Sums<D, CT> A;
   int last[CT];
   float *sc[CT];
@@ -685,11 +747,25 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
   if ((int)blockIdx.x < join) {
     const int64_t row = (int64_t)blockIdx.x * 4 + wave;
     if (row >= rows) return;
+    // the first splits' outputs are on their way while the factors are worked out
+    constexpr int kAhead = 8;
+    float early[kAhead][D / 64];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        early[s][c] = ws.o[(min(s, splits - 1) * rows + row) * D + c * 64 + lane];
     const RowJoin j = join_row(ws, splits, rows, row, lane);
     const int bh = (int)(row / R), r = (int)(row % R);
     const int64_t at = out_at(a, bh / a.c.H, bh % a.c.H, r);
     float o[D / 64] = {};
-    for (int s0 = 0; s0 < splits; s0 += 4) {  // four splits' reads in flight
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const float f = s < splits ? __shfl(j.f, s) : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) o[c] += f * early[s][c];
+    }
+    for (int s0 = kAhead; s0 < splits; s0 += 4) {  // four splits' reads in flight
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int s = min(s0 + k, splits - 1);
@@ -709,6 +785,22 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
   const int t = blk / BH * kSumTokens + threadIdx.x * 4;
   const int L = kv_len(a.c, bh / a.c.H);
   if (blk / BH * kSumTokens >= L) return;
+  // four rows' scores at a time in flight, the first of them and the weights while
+  // the sums of exponentials are worked out (t is in the row for every thread:
+  // rows have room for multiples of 16, this block's first token is one of them)
+  const int tt = min(t, (L - 1) & ~3);
+  auto fetch = [&](float4v(&s)[4], int r0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      s[k] = *reinterpret_cast<const float4v *>(
+          ws.scores + ((int64_t)bh * R + min(r0 + k, R - 1)) * a.c.room() + tt);
+  };
+  float4v s[4];
+  fetch(s, 0);
+  float4v *w = reinterpret_cast<float4v *>(a.weights + (int64_t)bh * a.c.room() + tt);
+  const bool wide = ((uintptr_t)a.weights & 15) == 0 && t + 4 <= L;
+  float4v was = {0.f, 0.f, 0.f, 0.f};
+  if (wide) was = *w;
   for (int r = wave; r < R; r += 4) {
     const float e = lse_of(join_row(ws, splits, rows, (int64_t)bh * R + r, lane));
     if (lane == 0) lse[r] = e;
@@ -717,11 +809,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
   if (t >= L) return;
   float4v sum = {0.f, 0.f, 0.f, 0.f};
   for (int r0 = 0; r0 < R; r0 += 4) {
-    float4v s[4];  // four rows' reads in flight
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      s[k] = *reinterpret_cast<const float4v *>(
-          ws.scores + ((int64_t)bh * R + min(r0 + k, R - 1)) * a.c.room() + t);
+    float4v next[4];
+    if (r0 + 4 < R) fetch(next, r0 + 4);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = min(r0 + k, R - 1);
@@ -732,9 +821,15 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
       for (int i = 0; i < 4; ++i)
         sum[i] += t + i > seen ? 0.f : __builtin_amdgcn_exp2f(s[k][i] - e);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = next[k];
   }
-  float *w = a.weights + (int64_t)bh * a.c.room() + t;
-  for (int i = 0; i < 4 && t + i < L; ++i) w[i] += sum[i];
+  if (wide) {
+    *w = was + sum;
+  } else {
+    float *one = a.weights + (int64_t)bh * a.c.room() + t;
+    for (int i = 0; i < 4 && t + i < L; ++i) one[i] += sum[i];
+  }
 }
 
 // The same of one row in every lane, for the few splits that calls with many rows have.
@@ -775,7 +870,9 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
   const int first = max(0, t - (L - a.n)) * a.G / 16;
   for (int rt = first + wave; rt * 16 < R; rt += 4) {
     Queries<D, 1, F32> Q;
-    load_queries<D, 1, F32>(Q, a, b, h, rt * 16, R, lane);
+    RawQueries<D, 1, F32> raw;
+    fetch_queries<D, 1, F32>(raw, a, b, h, rt * 16, R, lane);
+    load_queries<D, 1, F32>(Q, raw, a.negate, rt * 16, R, lane);
     const int row = rt * 16 + (lane & 15);
     const float lse = row < R ? row_lse(ws, splits, rows, (int64_t)bh * R + row) : INFINITY;
     const int last = row < R ? L - a.n + row / a.G : -1;
@@ -808,9 +905,6 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
 
 // Tiles of rows that a wave holds when the waves have rows of their own.
 constexpr int many_rows_ct(int D) { return D <= 128 ? 2 : 1; }
-// Waves of a wide workgroup: what its joining area in shared memory and its
-// registers allow.
-constexpr int wide_waves(int D, bool f32) { return D == 256 || f32 ? 8 : 16; }
 
 template <int D, int CT, int WT, int WR, bool F32>
 void launch_attend(const AttendArgs &a, const AttendPlan &p, const Ws &ws, hipStream_t s) {
@@ -830,8 +924,7 @@ void launch_attend(const AttendArgs &a, const AttendPlan &p, const Ws &ws, hipSt
 template <int D, bool F32>
 hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
   const int BH = a.c.B * a.c.H, R = a.n * a.G, room = a.c.room();
-  const AttendPlan p =
-      attend_plan(a.c.B, a.c.H, D, room, a.n, a.G * a.c.H, F32, a.weights != nullptr);
+  const AttendPlan p = attend_plan(a.c.B, a.c.H, D, room, a.n, a.G * a.c.H, a.weights != nullptr);
   char *w = static_cast<char *>(a.ws);
   Ws ws{};
   if (p.splits > 1 || a.weights != nullptr) ws.ml = reinterpret_cast<float2 *>(w);
@@ -841,10 +934,9 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
     launch_attend<D, many_rows_ct(D), 1, 4, F32>(a, p, ws, s);
   else if (p.ct == 2) {
     if constexpr (D <= 128) launch_attend<D, 2, 4, 1, F32>(a, p, ws, s);
-  } else if (p.wt == 4)
+  } else {
     launch_attend<D, 1, 4, 1, F32>(a, p, ws, s);
-  else
-    launch_attend<D, 1, wide_waves(D, F32), 1, F32>(a, p, ws, s);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.splits > 1 || p.scores) {
@@ -863,8 +955,7 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
 
 }  // namespace
 
-AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool f32,
-                       bool weights) {
+AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool weights) {
   AttendPlan p{};
   const int64_t R = (int64_t)n * (q_heads / H), BH = (int64_t)B * H;
   // Up to 16 rows (32 up to 128 channels) a workgroup holds them all and its
@@ -883,13 +974,6 @@ AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool f
   splits = splits > most ? most : splits;
   splits = splits > kMaxSplits ? kMaxSplits : splits;
   p.splits = (int)(splits < 1 ? 1 : splits);
-  // Short caches: one wide workgroup a head, of up to 4 steps a wave, rather
-  // than splits and a second launch that joins them.
-  const int wide = wide_waves(D, f32);
-  if (p.wt == 4 && p.ct == 1 && p.splits > 1 && room <= wide * 32 * 4) {
-    p.wt = wide;
-    p.splits = 1;
-  }
   p.scores = weights && p.wt != 1;
   const size_t rows = (size_t)(BH * R);
   size_t at = 0;

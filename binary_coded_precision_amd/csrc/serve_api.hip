@@ -201,14 +201,9 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
 size_t bcq_kv_workspace_bytes(const bcq_kv_cache *cache, int32_t n, int32_t q_heads,
                               int32_t with_weights) {
   if (check_attend(cache, n, q_heads) != BCQ_OK || n == 0) return 0;
-  size_t most = 0;  // of the two types
-  for (int f32 = 0; f32 < 2; ++f32) {
-    const size_t b = bcq::attend_plan(cache->batch, cache->heads, cache->head_dim, room(cache), n,
-                                      q_heads, f32 != 0, with_weights != 0)
-                         .bytes;
-    most = b > most ? b : most;
-  }
-  return most;
+  return bcq::attend_plan(cache->batch, cache->heads, cache->head_dim, room(cache), n, q_heads,
+                          with_weights != 0)
+      .bytes;
 }
 
 bcq_status bcq_kv_attend(const bcq_kv_cache *cache, const void *Q, int32_t n, int32_t q_heads,

@@ -64,7 +64,7 @@ struct AttendPlan {
   bool scores;     // the weights are summed from stored scores, not from recomputed ones
   size_t off_o, off_scores, bytes;  // workspace: (m, l) pairs, then outputs, then scores
 };
-AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool f32, bool weights);
+AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool weights);
 
 struct AttendArgs {
   KvView c;
