@@ -85,9 +85,10 @@ def build(extra_flags=(), verbose: bool = False) -> str:
 
 # Host-side checking build: the library's host code instrumented with
 # AddressSanitizer and UndefinedBehaviorSanitizer (each flag after -Xarch_host,
-# so the GPU code is compiled as usual), and a driver that calls every entry
-# point's argument validation (tests/host_sanitize/validate.cpp).  Used by
-# tests/test_host_sanitizers.py on the CPU; nothing in it runs a kernel.
+# so the GPU code is compiled as usual), and a driver that calls the entry
+# points' argument validation (tests/host_sanitize/validate.cpp, lowbit.cpp).
+# Used by tests/test_host_sanitizers.py and tests/test_lowbit_sanitizers.py on
+# the CPU; nothing in it runs a kernel.
 SANITIZE_DIR = os.path.join(OBJ_DIR, "host_sanitize")
 SANITIZE_HOST = ("-Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined "
                  "-Xarch_host -fno-sanitize-recover=undefined "
@@ -98,12 +99,15 @@ def build_host_sanitized(driver_src: str) -> str:
     """Build the sanitized library and the validation driver; returns the
     driver's path.  Rebuilds only when a source is newer than the driver."""
     os.makedirs(SANITIZE_DIR, exist_ok=True)
-    exe = os.path.join(SANITIZE_DIR, "validate")
+    exe = os.path.join(SANITIZE_DIR, os.path.splitext(os.path.basename(driver_src))[0])
     srcs = [os.path.join(CSRC, s) for s in SOURCES] + [driver_src]
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".h")]
     headers.append(os.path.join(os.path.dirname(HERE), "include", "bcq.h"))
-    if os.path.exists(exe) and all(os.path.getmtime(f) < os.path.getmtime(exe)
-                                   for f in srcs + headers):
+
+    def newest(out, of):
+        return os.path.exists(out) and all(os.path.getmtime(f) < os.path.getmtime(out) for f in of)
+
+    if newest(exe, srcs + headers):
         return exe
 
     def comp(src):
@@ -115,14 +119,15 @@ def build_host_sanitized(driver_src: str) -> str:
             raise RuntimeError("hipcc failed for %s:\n%s" % (src, r.stderr))
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(comp, SOURCES))
     lib = os.path.join(SANITIZE_DIR, "libbcq_host_sanitize.so")
-    cmd = ([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC"] + SANITIZE_HOST[:4] +
-           ["-o", lib] + objs)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    if not newest(lib, srcs[:-1] + headers):
+        with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
+            objs = list(ex.map(comp, SOURCES))
+        cmd = ([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC"] + SANITIZE_HOST[:4] +
+               ["-o", lib] + objs)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     clang = os.path.join(os.path.dirname(os.path.realpath(hipcc())), "..", "llvm", "bin", "clang++")
     if not os.path.exists(clang):
         clang = "/opt/rocm/llvm/bin/clang++"
