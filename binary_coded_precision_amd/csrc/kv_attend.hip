@@ -41,6 +41,8 @@
 // one load; K needs one load of D/8 bytes a lane for 16 tokens.  No shared
 // memory is used in the loop and no barrier: the waves of a workgroup either
 // take turns over the tokens (few rows) or hold different rows.
+#include <algorithm>
+
 #include "serve_internal.h"
 
 namespace bcq {
@@ -880,53 +882,58 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int BH = a.c.B * a.c.H, R = a.n * a.G;
   const int64_t rows = (int64_t)BH * R;
-  const int bh = blockIdx.x % BH, t = blockIdx.x / BH * 32;
+  const int bh = blockIdx.x % BH, stride = gridDim.x / BH * 32;
   const int b = bh / a.c.H, h = bh % a.c.H;
   const int L = kv_len(a.c, b);
-  if (t >= L) return;
-  Tiles<D> T;
-  const Where at = where(a.c, b, h, t, L);
-  load_k(T, a.c, at, lane);
-  load_m(T, a.c, at, lane);
-  float sum[8];
+  for (int t = blockIdx.x / BH * 32; t < L; t += stride) {
+    Tiles<D> T;
+    const Where at = where(a.c, b, h, t, L);
+    load_k(T, a.c, at, lane);
+    load_m(T, a.c, at, lane);
+    float sum[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-  // the first query that sees token t
-  const int first = max(0, t - (L - a.n)) * a.G / 16;
-  for (int rt = first + wave; rt * 16 < R; rt += 4) {
-    Queries<D, 1, F32> Q;
-    RawQueries<D, 1, F32> raw;
-    fetch_queries<D, 1, F32>(raw, a, b, h, rt * 16, R, lane);
-    load_queries<D, 1, F32>(Q, raw, a.negate, rt * 16, R, lane);
-    const int row = rt * 16 + (lane & 15);
-    const float lse = row < R ? row_lse(ws, splits, rows, (int64_t)bh * R + row) : INFINITY;
-    const int last = row < R ? L - a.n + row / a.G : -1;
+    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    // the first query that sees token t
+    const int first = max(0, t - (L - a.n)) * a.G / 16;
+    for (int rt = first + wave; rt * 16 < R; rt += 4) {
+      Queries<D, 1, F32> Q;
+      RawQueries<D, 1, F32> raw;
+      fetch_queries<D, 1, F32>(raw, a, b, h, rt * 16, R, lane);
+      load_queries<D, 1, F32>(Q, raw, a.negate, rt * 16, R, lane);
+      const int row = rt * 16 + (lane & 15);
+      const float lse = row < R ? row_lse(ws, splits, rows, (int64_t)bh * R + row) : INFINITY;
+      const int last = row < R ? L - a.n + row / a.G : -1;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      float4v S[1];
-      tile_scores<D, 1, F32>(S, T, s, Q);
+      for (int s = 0; s < 2; ++s) {
+        float4v S[1];
+        tile_scores<D, 1, F32>(S, T, s, Q);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = raw_score(S[0][i], Q.sum[0], T.m[s][2 * i]);
-        sum[4 * s + i] += t + 16 * s + 4 * g + i > last
-                              ? 0.f
-                              : __builtin_amdgcn_exp2f(fmaf(x, a.unit, -lse));
+        for (int i = 0; i < 4; ++i) {
+          const float x = raw_score(S[0][i], Q.sum[0], T.m[s][2 * i]);
+          sum[4 * s + i] += t + 16 * s + 4 * g + i > last
+                                ? 0.f
+                                : __builtin_amdgcn_exp2f(fmaf(x, a.unit, -lse));
+        }
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i) {
 #pragma unroll
-    for (int k = 1; k < 16; k <<= 1) sum[i] += __shfl_xor(sum[i], k);
-    if ((lane & 15) == 0) part[wave][16 * (i >> 2) + 4 * g + (i & 3)] = sum[i];
-  }
-  __syncthreads();
-  if (threadIdx.x < 32 && t + (int)threadIdx.x < L) {
-    const int i = threadIdx.x;
-    a.weights[(int64_t)bh * a.c.room() + t + i] +=
-        part[0][i] + part[1][i] + (part[2][i] + part[3][i]);
+      for (int k = 1; k < 16; k <<= 1) sum[i] += __shfl_xor(sum[i], k);
+      if ((lane & 15) == 0) part[wave][16 * (i >> 2) + 4 * g + (i & 3)] = sum[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < 32 && t + (int)threadIdx.x < L) {
+      const int i = threadIdx.x;
+      a.weights[(int64_t)bh * a.c.room() + t + i] +=
+          part[0][i] + part[1][i] + (part[2][i] + part[3][i]);
+    }
+    __syncthreads();  // part is written again
   }
 }
+
+// Workgroups of 256 in a launch, whose work items are counted in 32 bits.
+constexpr int kMaxGroups = (1 << 24) - 1;
 
 // Tiles of rows that a wave holds when the waves have rows of their own.
 constexpr int many_rows_ct(int D) { return D <= 128 ? 2 : 1; }
@@ -972,7 +979,9 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (a.weights != nullptr && !p.scores) {
-    weights_kernel<D, F32><<<BH * ((room + 31) / 32), 256, 0, s>>>(a, p.splits, ws);
+    // a launch's work items are counted in 32 bits: longer rows take turns
+    const int chunks = (int)std::min<int64_t>((room + 31) / 32, kMaxGroups / BH);
+    weights_kernel<D, F32><<<BH * chunks, 256, 0, s>>>(a, p.splits, ws);
     e = hipGetLastError();
   }
   return e;

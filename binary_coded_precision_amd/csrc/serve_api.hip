@@ -9,7 +9,9 @@
 namespace {
 
 constexpr int32_t kMaxTokens = 1 << 20;
-constexpr int32_t kMaxRows = 1 << 24;
+// Work items of a launch are counted in 32 bits: what these limits and those
+// below let through stays under 2^24 workgroups of 256.
+constexpr int32_t kMaxRows = (1 << 24) - 1;
 constexpr int32_t kMaxIntK = 131071;  // 128 * 128 * K stays below 2^31
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -67,6 +69,8 @@ bcq_status check_cache(const bcq_kv_cache *c) {
   const int32_t p = c->page_tokens;
   if (p < 16 || p > 256 || (p & (p - 1)) != 0) return BCQ_ERR_UNSUPPORTED;
   if ((int64_t)c->max_pages * p > BCQ_KV_MAX_TOKENS) return BCQ_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)c->batch * c->heads;
+  if (rows >= 1 << 22 || rows * c->max_pages * p > (int64_t)1 << 33) return BCQ_ERR_INVALID_ARG;
   if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->scales, 16) ||
       !aligned(c->page_table, 4) || !aligned(c->lens, 4))
     return BCQ_ERR_ALIGNMENT;
@@ -96,8 +100,9 @@ bcq_status check_vectors(const bcq_kv_cache *c, int32_t n, const void *k, const 
                          bcq_dtype dtype) {
   BCQ_TRY(check_cache(c));
   if (!dtype_valid(dtype) || n < 0 || n > BCQ_KV_MAX_TOKENS) return BCQ_ERR_INVALID_ARG;
-  // vectors are counted in 32 bits
-  if ((int64_t)c->batch * c->heads * ((int64_t)n + 6) > (int64_t)1 << 30) return BCQ_ERR_INVALID_ARG;
+  // a work item takes four channels of K or V, of up to six tokens more than n
+  if ((int64_t)c->batch * c->heads * ((int64_t)n + 6) * c->head_dim >= ((int64_t)1 << 33) - 512)
+    return BCQ_ERR_INVALID_ARG;
   if (n > 0 && (k == nullptr || v == nullptr)) return BCQ_ERR_INVALID_ARG;
   if (!aligned(k, dtype_size(dtype)) || !aligned(v, dtype_size(dtype))) return BCQ_ERR_ALIGNMENT;
   return BCQ_OK;
@@ -107,8 +112,8 @@ bcq_status check_attend(const bcq_kv_cache *c, int32_t n, int32_t q_heads) {
   BCQ_TRY(check_cache(c));
   if (n < 0 || n > BCQ_KV_MAX_TOKENS) return BCQ_ERR_INVALID_ARG;
   if (q_heads < 1 || q_heads > (1 << 16) || q_heads % c->heads != 0) return BCQ_ERR_INVALID_ARG;
-  // rows are counted in 32 bits, and so are a launch's workgroups
-  if ((int64_t)n * q_heads > 1 << 28 || (int64_t)c->batch * n * q_heads > (int64_t)1 << 30)
+  // rows are counted in 32 bits
+  if ((int64_t)n * q_heads > 1 << 28 || (int64_t)c->batch * n * q_heads > (int64_t)1 << 29)
     return BCQ_ERR_INVALID_ARG;
   return BCQ_OK;
 }

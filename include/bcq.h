@@ -418,7 +418,8 @@ bcq_status bcq_quantize(const void *W, bcq_dtype w_dtype, int32_t M, int32_t K, 
  * row that holds an infinity or NaN has scale NaN, and both have codes 0.
  * codes: [rows][ldc] int8, ldc a multiple of 16 and at least K rounded up to
  * one, 16-byte aligned; zeros are written from K up to that multiple, nothing
- * past it.  It serves for tokens and, once, for weights.  rows = 0 does nothing.
+ * past it.  It serves for tokens and, once, for weights.  Up to 2^24 - 1 rows;
+ * rows = 0 does nothing.
  */
 bcq_status bcq_int_quantize(const void *X, bcq_dtype dtype, int32_t rows, int32_t K, int32_t ldx,
                             int8_t *codes, int32_t ldc, float *scales, hipStream_t stream);
@@ -431,7 +432,7 @@ bcq_status bcq_int_quantize(const void *X, bcq_dtype dtype, int32_t rows, int32_
  *   multiple of 16), a_scales: [T] fp32.
  * W: [M][ldw] codes of any value, readable up to the next multiple of 16 past
  *   K, w_scales: [M] fp32.  lda, ldw: multiples of 16, at least K rounded up
- *   to one; A and W 16-byte aligned.  1 <= K <= 131071, any M >= 1.
+ *   to one; A and W 16-byte aligned.  1 <= K <= 131071, 1 <= M < 2^24, T <= 2^20.
  * bias: [M] of dtype, or NULL.  Y: [T][ldy], ldy >= M, element aligned, dtype
  *   BCQ_F16 or BCQ_F32; columns past M are not written.
  * workspace: bcq_int_workspace_bytes(T, M, K) bytes, 16-byte aligned, contents
@@ -474,7 +475,7 @@ size_t bcq_int_workspace_bytes(int32_t T, int32_t M, int32_t K);
  *   block of 4 tokens holds channels 64h + 4r + 2c (low half) and
  *   64h + 4r + 2c + 1 of its token t in byte [r][h][t][c].
  * scales: [num_pages][heads][page_tokens][4] fp16: scale and zero of K, scale
- *   and zero of V.
+ *   and zero of V; the scales are not negative.
  * page_table: [batch][max_pages]: page of each page_tokens slots of a sequence.
  *   Entries past a sequence's length are not read.  Entries outside
  *   [0, num_pages) are never followed: nothing is written there, and what is
@@ -483,8 +484,10 @@ size_t bcq_int_workspace_bytes(int32_t T, int32_t M, int32_t K);
  *   0 .. max_pages * page_tokens).
  * k_codes, v_codes and scales 16-byte aligned, the others 4.  head_dim 64, 128
  * or 256, page_tokens a power of two from 16 to 256 (otherwise
- * BCQ_ERR_UNSUPPORTED).  The memory is the caller's; the tables may change
- * between calls, so calls may be captured in a graph.
+ * BCQ_ERR_UNSUPPORTED); batch * heads below 2^22, max_pages * page_tokens up to
+ * BCQ_KV_MAX_TOKENS and the product of the four up to 2^33.  The memory is the
+ * caller's; the tables may change between calls, so calls may be captured in a
+ * graph.
  *
  * The tokens of a call are the last n of each sequence: token i of n lies in
  * slot lens[b] - n + i, lens already counting them; tokens whose slot would be
@@ -512,7 +515,8 @@ typedef struct {
  * weights, pos: [batch][heads][max_pages * page_tokens], or NULL: for each slot
  *   written, weights becomes 0 and pos the token's position, positions[b][i]
  *   (or the slot where positions is NULL), as bcq_kv_evict reads them.
- * n = 0 does nothing.  Validation and stream behaviour as in bcq_gemv.
+ * batch * heads * n * head_dim stays below 2^33.  n = 0 does nothing.
+ * Validation and stream behaviour as in bcq_gemv.
  */
 bcq_status bcq_kv_append(const bcq_kv_cache *cache, int32_t n, const void *K, int64_t k_batch,
                          int64_t k_token, int64_t k_head, const void *V, int64_t v_batch,
@@ -543,9 +547,11 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
  *   the probabilities are added, summed over the queries and over the query
  *   heads of a cached head, in a fixed order.
  * Products run on the matrix cores with the codes as they are; softmax and
- * sums are in fp32.  In fp16 calls each token's probability times its V scale
- * is rounded once to fp16 (relative to the largest of its row); fp32 calls
- * hold it, and the queries, in 22 bits.
+ * sums are in fp32.  Each token's probability times its V scale is held in 22
+ * bits relative to the largest of its row, and in fp16 calls of more rows than
+ * share a read of the cache (n * q_heads / heads past 32, or 16 at head_dim
+ * 256) in 11; fp32 calls hold the queries in 22 bits too.  batch * n * q_heads
+ * is at most 2^29.
  * workspace: bcq_kv_workspace_bytes(cache, n, q_heads, weights != NULL) bytes,
  *   16-byte aligned, of no account before and after; calls that may run at the
  *   same time need separate ones.  NULL when that is 0.

@@ -116,17 +116,20 @@ int main() {
          bcq_kv_attend(&ok, x, 1, 4, 1, 1, 1, x, 1, 1, 1, BCQ_F16, INFINITY, nullptr, x, SIZE_MAX,
                        nullptr),
          BCQ_ERR_INVALID_ARG);
-  bcq_kv_cache wide = cache(1 << 16, 1 << 12, 256, INT_MAX, 1 << 16);
+  const bcq_kv_cache huge = cache(1 << 16, 1 << 12, 256, INT_MAX, 1 << 16);
+  expect("rows of a huge cache", bcq_kv_evict_workspace_bytes(&huge, 1 << 23), 0);
+  expect("scores of a huge cache", bcq_kv_workspace_bytes(&huge, 1, 1 << 12, 1), 0);
+  const bcq_kv_cache wide = cache(1 << 12, 8, 256, INT_MAX, 1 << 10);
   expect("vectors of a wide cache",
          bcq_kv_append(&wide, 1 << 24, x, 1, 1, 1, x, 1, 1, 1, BCQ_F16, nullptr, nullptr, nullptr,
                        nullptr),
          BCQ_ERR_INVALID_ARG);
   expect("rows of a wide cache", bcq_kv_workspace_bytes(&wide, 1 << 24, 1 << 12, 1), 0);
-  if (bcq_kv_evict_workspace_bytes(&wide, 1 << 23) < (size_t)1 << 50)
+  if (bcq_kv_evict_workspace_bytes(&wide, 1 << 17) < (size_t)1 << 34)
     expect("moves of a wide cache", 0, 1);
-  if (bcq_kv_workspace_bytes(&wide, 1, 1 << 12, 1) < (size_t)1 << 40)
+  if (bcq_kv_workspace_bytes(&wide, 1, 64, 1) < (size_t)1 << 38)
     expect("scores of a wide cache", 0, 1);
-  if (bcq_int_workspace_bytes(1 << 20, 1 << 24, 131071) < (size_t)1 << 37)
+  if (bcq_int_workspace_bytes(1 << 20, (1 << 24) - 1, 131071) < (size_t)1 << 37)
     expect("codes of the largest product", 0, 1);
 
   printf("%d failures\n", failures);

@@ -102,6 +102,15 @@ def test_linear(T, M, K, dtype):
     assert torch.equal(z, y[:T, :M])
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("T,M,K", [
+    (3, 50, 5461), (20, 70, 4100), (40, 64, 5000), (64, 8000, 1040),  # few tokens, K split or not
+    (100, 100, 4096), (300, 257, 2049),  # the small tile, K split
+    (1001, 4000, 160), (4090, 4104, 144)])  # the larger tiles, outputs of whole 16 bytes
+def test_linear_by_way(T, M, K, dtype):
+    test_linear(T, M, K, dtype)
+
+
 def test_extreme_codes_do_not_overflow():
     K = 131071
     a = torch.full((2, K + 1), -128, dtype=torch.int8, device="cuda")

@@ -148,6 +148,37 @@ def test_attend_sharp_softmax(n):
             + (L + 2 * n + 16) * 2.0**-23 * total).all()
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, -0.0, 1e-30])
+@pytest.mark.parametrize("n,dtype", [(1, "f16"), (1, "f32"), (40, "f16")])
+def test_attend_scales_of_either_sign(n, dtype, scale):
+    c = make([190], 1, 64, 32, 7, seed=3)
+    dev = device(c)
+    q = np.random.default_rng(4).normal(size=(1, n, 2, 64)).astype(DT[dtype][1])
+    o = torch.empty(q.shape, dtype=DT[dtype][0], device="cuda")
+    w = torch.zeros((1, 1, dev.room), device="cuda")
+    bcq.bcq_kv_attend(dev, torch.from_numpy(q).cuda(), o, scale=scale, weights=w)
+    ref, total, b, wb = lb.attend(c, q, np.float32(scale))
+    err = np.abs(o.cpu().numpy().astype(np.float64) - ref)
+    assert (err <= bound(ref, b, 64, 190, dtype)).all()
+    tol = 4 * 64 * 2.0**-24 * 2 * wb + (190 + n * 2 + 16) * 2.0**-23 * total
+    assert (np.abs(w.cpu().numpy()[..., :190].astype(np.float64) - total) <= tol).all()
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("n,dtype", [(2, "f16"), (2, "f32"), (40, "f16"), (40, "f32")])
+def test_queries_that_are_not_finite_stay_alone(n, dtype, value):
+    c = make([90], 1, 64, 16, 6, seed=5)
+    q = np.random.default_rng(6).normal(size=(1, n, 2, 64)).astype(DT[dtype][1])
+    ref, _, b, _ = lb.attend(c, q, np.float32(0.125))
+    q[0, n // 2, 1, 7] = value
+    o = torch.empty(q.shape, dtype=DT[dtype][0], device="cuda")
+    bcq.bcq_kv_attend(device(c), torch.from_numpy(q).cuda(), o)
+    got = o.cpu().numpy().astype(np.float64)
+    assert np.isnan(got[0, n // 2, 1]).all()
+    got[0, n // 2, 1] = ref[0, n // 2, 1]
+    assert (np.abs(got - ref) <= bound(ref, b, 64, 90, dtype)).all()
+
+
 @pytest.mark.parametrize("value", [np.nan, np.inf])
 @pytest.mark.parametrize("n", [3, 40])
 def test_hidden_tokens_do_not_reach_earlier_queries(n, value):
@@ -382,6 +413,39 @@ def test_evict(lens, keep, recent, H, D, page, room, kind):
         assert np.array_equal(wd[b, :, :m].cpu().numpy(), wo[b, :, :m].cpu().numpy(),
                               equal_nan=True)
         assert torch.equal(pd[b, :, :m], po[b, :, :m])
+
+
+# evictions of three and four tokens, moves made by the selecting workgroup at every number of
+# channels, more equal weights than are listed
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+@pytest.mark.parametrize("lens,keep,recent,H,D,page,room", [
+    ([68, 67], 64, 10, 2, 64, 16, 80), ([5003], 5000, 9, 1, 64, 64, 5056),
+    ([250], 200, 10, 1, 256, 64, 256), ([5056, 5030], 5000, 40, 1, 128, 32, 5056),
+    ([5056], 1000, 100, 1, 64, 64, 5056), ([33024], 33020, 7, 1, 64, 256, 33024)])
+def test_evict_by_way(lens, keep, recent, H, D, page, room, kind):
+    test_evict(lens, keep, recent, H, D, page, room, kind)
+
+
+def test_tracking_arrays_of_any_alignment():
+    """weights and pos one element past a multiple of 16 bytes, against aligned ones."""
+    got = []
+    for shift in (0, 1):
+        torch.manual_seed(1)
+        c = bcq.KVCache.new(2, 300, 2, 64, page_tokens=16)
+        n = c.batch * c.heads * c.room
+        w = torch.zeros(n + 1, device="cuda")[shift:n + shift].view(c._slots)
+        pos = torch.zeros(n + 1, dtype=torch.int32, device="cuda")[shift:n + shift].view(c._slots)
+        c.lens.copy_(torch.tensor([280, 140]))
+        x = torch.randn((2, 2, 280, 2, 64), dtype=torch.float16, device="cuda")
+        q = torch.randn((2, 4, 6, 64), dtype=torch.float16, device="cuda")
+        o = torch.empty_like(q)
+        bcq.bcq_kv_append(c, x[0], x[1], weights=w, pos=pos)
+        bcq.bcq_kv_attend(c, q, o, weights=w)
+        bcq.bcq_kv_evict(c, 131, 11, w, pos)
+        got.append((o, w[..., :131].clone(), pos[..., :131].clone(), c.lens, c.k_codes, c.v_codes,
+                    c.scales))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------------------ together

@@ -34,7 +34,7 @@ LINEAR = dict(X=A, T=40, ldx=104, W=A, w_scales=A, M=50, K=100, ldw=112, bias=No
 
 PRODUCT_BAD = [
     (dict(T=-1), INVALID), (dict(T=(1 << 20) + 1), INVALID), (dict(M=0), INVALID),
-    (dict(M=(1 << 24) + 1), INVALID), (dict(K=0), INVALID), (dict(K=131072, ldw=131072), INVALID),
+    (dict(M=1 << 24), INVALID), (dict(K=0), INVALID), (dict(K=131072, ldw=131072), INVALID),
     (dict(dtype=0), INVALID), (dict(dtype=3), INVALID), (dict(W=None), INVALID),
     (dict(w_scales=None), INVALID), (dict(Y=None), INVALID), (dict(ldw=96), INVALID),
     (dict(ldy=49), INVALID), (dict(W=A + 8), ALIGNMENT), (dict(ldw=120), ALIGNMENT),
@@ -44,7 +44,7 @@ PRODUCT_BAD = [
 
 
 @pytest.mark.parametrize("change,want", [
-    (dict(rows=-1), INVALID), (dict(rows=(1 << 24) + 1), INVALID), (dict(K=0), INVALID),
+    (dict(rows=-1), INVALID), (dict(rows=1 << 24), INVALID), (dict(K=0), INVALID),
     (dict(K=131072, ldx=131072, ldc=131072), INVALID), (dict(dtype=0), INVALID),
     (dict(X=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID),
     (dict(ldx=96), INVALID), (dict(ldc=96), INVALID), (dict(X=A + 2), ALIGNMENT),
@@ -81,7 +81,7 @@ def test_int_workspace(lib):
     for bad in [(-1, 50, 100), (0, 50, 100), (40, 0, 100), (40, 50, 0), (40, 50, 131072)]:
         assert size(*bad) == 0
     # the largest call's sums are counted in 64 bits
-    assert size(1 << 20, 1 << 24, 131071) > (1 << 20) * 131072
+    assert size(1 << 20, (1 << 24) - 1, 131071) > (1 << 20) * 131072
 
 
 def cache(**change):
@@ -98,6 +98,8 @@ CACHE_BAD = [
     (dict(batch=(1 << 16) + 1), INVALID), (dict(heads=0), INVALID),
     (dict(heads=(1 << 12) + 1), INVALID), (dict(num_pages=0), INVALID),
     (dict(max_pages=0), INVALID), (dict(max_pages=1 << 30), INVALID),
+    (dict(batch=1 << 11, heads=1 << 11), INVALID),  # more rows than a launch has workgroups
+    (dict(batch=1 << 10, heads=1 << 4, max_pages=1 << 14), INVALID),  # 2^34 cached vectors
     (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=512), UNSUPPORTED),
     (dict(page_tokens=8), UNSUPPORTED), (dict(page_tokens=48), UNSUPPORTED),
     (dict(page_tokens=512), UNSUPPORTED), (dict(k_codes=A + 8), ALIGNMENT),
@@ -180,8 +182,8 @@ def test_kv_workspaces(lib):
     need = lib.bcq_kv_evict_workspace_bytes(cache(), 100)
     assert call(lib, "bcq_kv_evict", EVICT, bytes=need - 1) == INVALID
     # counted in 64 bits
-    wide = cache(batch=1 << 16, heads=1 << 12, page_tokens=256, max_pages=1 << 16)
-    assert lib.bcq_kv_evict_workspace_bytes(wide, 1 << 23) > 1 << 40
+    wide = cache(batch=1 << 12, heads=8, page_tokens=256, max_pages=1 << 10)
+    assert lib.bcq_kv_evict_workspace_bytes(wide, 1 << 17) > 1 << 34
 
 
 def test_binding_refuses_host_tensors_and_other_shapes():
