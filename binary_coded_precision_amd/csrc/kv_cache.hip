@@ -5,6 +5,8 @@
 // zero + scale * code: zero = fp16(min), scale = fp16((max - min) * (1/15)),
 // code = rint((x - zero) / scale) held to 0..15, each step rounded to fp32 (the
 // constant too), so the codes are a function of the inputs alone.
+#include <type_traits>
+
 #include "serve_internal.h"
 
 namespace bcq {
@@ -223,9 +225,11 @@ hipError_t read_dim(const KvView &c, int n, void *k, KvStrides ks, void *v, KvSt
 // evicted slot in front takes the i-th kept token from behind, so that what
 // moves is the least possible and no move reads what another writes.
 
+constexpr uint32_t kLate = 0xffffffffu;  // above every weight's order
+
 // Order of a slot: recent tokens above every weight, NaN below every weight.
 __device__ __forceinline__ uint32_t order_of(float w, bool late) {
-  if (late) return 0xffffffffu;
+  if (late) return kLate;
   if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 counts as 0
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
@@ -308,6 +312,13 @@ __device__ __forceinline__ void move_tokens(const EvictArgs &a, int row, const i
   }
 }
 
+// Element i, of 4 bytes, of a row's array: a scalar base and 32 bits of offset.
+template <typename T, typename B>
+__device__ __forceinline__ T *nth(B *base, uint32_t i) {
+  using Byte = std::conditional_t<std::is_const_v<B>, const char, char>;
+  return reinterpret_cast<T *>(reinterpret_cast<Byte *>(base) + (uint32_t)(4 * i));
+}
+
 // One workgroup a row.  A wave has 256 Q slots in a row, a thread the orders of 4 Q
 // of them in registers, slot 256 q + 4 lane + e of the wave's, so that reads are
 // wide and coalesced; rows with room for more than the workgroup holds (ONCE is
@@ -315,19 +326,25 @@ __device__ __forceinline__ void move_tokens(const EvictArgs &a, int row, const i
 //
 // The row's smallest kept rank value is found, and ballots then number what
 // moves in slot order.  Up to kFew evicted slots (a decode loop's step) are found
-// as so many minima.  Otherwise a radix select takes 12 bits a pass, until
-// a bin is kept whole or holds at most kRank slots, which are ranked against each
-// other; passes after the first go over a list of the slots left once it holds
-// them, so that one pass over all slots is the rule.
+// as so many minima.  Otherwise a radix select takes 12 bits a pass of the
+// orders' distances from the smallest, until a bin is kept whole or holds at most
+// kRank slots, which are ranked against each other; once at most kList slots are
+// left they are listed and the list is gone over, so that one count over all
+// slots and one listing are the rule.  (With the orders' own bits as digits, 8
+// bins an octave, a bin of 32768 softmax sums held a thousand slots and a second
+// count followed.)
 // One compute unit's vector ALUs bound it (an operation on each of 32768 slots
-// takes 0.2 us), hence few operations a slot and pass.
+// takes 0.2 us), hence few operations a slot and pass: slots past L have a rank
+// below all others instead of a test, and blocks without a match are left after
+// one ballot.  32 rows of 32768 slots, 4096 kept: 24 us, then 21 us of moves.
 //
 // D > 0: there are at most kInPlace moves, made here; lens_out is then not lens.
 template <int Q, bool ONCE, int D>
 __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   constexpr int kRound = 4 * Q * kEvictThreads;
   __shared__ __align__(16) uint32_t hist[kBins];
-  __shared__ uint64_t list[kList], cand[kRank];
+  __shared__ uint32_t list_high[kList], list_low[kList];
+  __shared__ uint64_t cand[kRank];
   __shared__ uint64_t least[kEvictWaves];
   __shared__ int tmp[kEvictWaves];
   __shared__ uint32_t sums[2][kEvictWaves];
@@ -342,19 +359,23 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   const int end = ONCE ? 1 : L;  // of the rounds' first slots
   const float *w = a.weights + at;
   const int32_t *pos = a.pos + at;
-  const int first = wave * 256 * Q + lane * 4;  // of the thread's slots, in a round
+  float *w_out = a.weights_out + at;
+  int32_t *pos_out = a.pos_out + at;
+  // A wave's first slot in a round, its blocks of 256, and the thread's in a block
+  const int first = wave * 256 * Q, mine = lane * 4;
   if (D > 0 && tid == 0 && row % a.c.H == 0) a.lens_out[b] = m;
 
-  // Rows start at multiples of 16 slots and end at one, so a read of 4 from a
-  // multiple of 4 below L stays in its row.
+  // Rows start at multiples of 16 slots and end at one: reads of 4 slots past L
+  // come from the row's last 4 or those at L.  Blocks past L are not read.
   float4 wv[Q];
   int4 pv[Q];
   auto read = [&](int s0, bool both) {
 #pragma unroll
     for (int q = 0; q < Q; ++q)
       if (s0 + 256 * q < L) {
-        pv[q] = *reinterpret_cast<const int4 *>(pos + s0 + 256 * q);
-        if (both) wv[q] = *reinterpret_cast<const float4 *>(w + s0 + 256 * q);
+        const int s = min(s0 + 256 * q + mine, a.c.room() - 4);
+        pv[q] = *nth<const int4>(pos, s);
+        if (both) wv[q] = *nth<const float4>(w, s);
       }
   };
   int newest = INT32_MIN;
@@ -362,11 +383,15 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
     read(s0, ONCE);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int s = s0 + 256 * q;
-      if (s < L) newest = max(newest, pv[q].x);
-      if (s + 1 < L) newest = max(newest, pv[q].y);
-      if (s + 2 < L) newest = max(newest, pv[q].z);
-      if (s + 3 < L) newest = max(newest, pv[q].w);
+      if (s0 + 256 * q + 256 <= L) {
+        newest = max(newest, max(max(pv[q].x, pv[q].y), max(pv[q].z, pv[q].w)));
+      } else if (s0 + 256 * q < L) {
+        const int s = s0 + 256 * q + mine;
+        if (s < L) newest = max(newest, pv[q].x);
+        if (s + 1 < L) newest = max(newest, pv[q].y);
+        if (s + 2 < L) newest = max(newest, pv[q].z);
+        if (s + 3 < L) newest = max(newest, pv[q].w);
+      }
     }
   }
 #pragma unroll
@@ -378,8 +403,9 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   // newest is at least every position, so their distance fits 32 bits
   auto is_late = [&](int32_t p) { return (uint32_t)newest - (uint32_t)p < (uint32_t)a.recent; };
 
-  // The orders of the round whose slots start at s0 for this thread.  On the
-  // way what is in front goes to the output; what is evicted of it is
+  // The orders of the round whose slots start at s0 for this wave, 0 past L: as
+  // rank values those are below every other, so that nothing else asks for L.  On
+  // the way what is in front goes to the output; what is evicted of it is
   // overwritten by the moves.
   uint32_t key[Q][4];
   const bool apart = a.weights_out != a.weights || a.pos_out != a.pos;
@@ -388,20 +414,31 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
     if (!ONCE) read(s0, true);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
+      const int block = s0 + 256 * q;
+      if (block >= L) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) key[q][e] = 0;
+        continue;
+      }
       const float xs[4] = {wv[q].x, wv[q].y, wv[q].z, wv[q].w};
       const int32_t ys[4] = {pv[q].x, pv[q].y, pv[q].z, pv[q].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) key[q][e] = order_of(xs[e], is_late(ys[e]));
-      const int s = s0 + 256 * q;
-      if (write && s + 3 < m && wide) {
-        *reinterpret_cast<float4 *>(a.weights_out + at + s) = wv[q];
-        *reinterpret_cast<int4 *>(a.pos_out + at + s) = pv[q];
-      } else if (write) {
+      const int s = block + mine;
+      if (block + 256 > L) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) key[q][e] = s + e < L ? key[q][e] : 0;
+      }
+      if (!write || block >= m) continue;
+      if (s + 3 < m && wide) {
+        *nth<float4>(w_out, s) = wv[q];
+        *nth<int4>(pos_out, s) = pv[q];
+      } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (s + e < m) {
-            a.weights_out[at + s + e] = xs[e];
-            a.pos_out[at + s + e] = ys[e];
+            *nth<float>(w_out, s + e) = xs[e];
+            *nth<int32_t>(pos_out, s + e) = ys[e];
           }
       }
     }
@@ -419,20 +456,29 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
 
   // ---- the smallest rank value kept
   uint64_t edge = 0;  // kept: rank values from here on
+  uint32_t base = 0, late = kLate;
+  auto distances = [&] {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) key[q][e] = min(max(key[q][e], base) - base, late);
+  };
   if (evicted <= kFew) {
+    edge = rank_of(0, L - 1);  // above those past L
     uint32_t out = 0;  // evicted slots behind m, by their distance from it
     int front[kFew], fronts = 0;
     for (int n = 0; n < evicted; ++n) {
       uint64_t low = ~0ull;
       for (int s0 = first; s0 < end + first; s0 += kRound) {
         if (!ONCE) orders(s0, false);
+        uint32_t l = 0xffffffffu - (uint32_t)(s0 + mine);
+        if (Q > 1) asm volatile("" : "+v"(l));  // or 4 Q rank values would be kept
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int s = s0 + 256 * q + e;
-            const uint64_t v = rank_of(key[q][e], s);
-            if (s < L && v >= edge && v < low) low = v;
+            const uint64_t v = (uint64_t)key[q][e] << 32 | (l - 256 * q - e);
+            if (v >= edge && v < low) low = v;
           }
       }
 #pragma unroll
@@ -468,34 +514,98 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
     }
     return;
   } else {
-    uint32_t left = m;      // still to be taken among the values that start with edge
-    bool in_list = false;   // those are in `list`
-    // every slot's rank value, or those listed
-    auto each = [&](auto &&visit) {
-      if (in_list) {
-        for (int i = tid; i < (int)listed; i += kEvictThreads) visit(list[i]);
-        return;
-      }
-      for (int s0 = first; s0 < end + first; s0 += kRound) {
-        if (!ONCE) orders(s0, false);
+    // Orders as their distance from the smallest one (late ones one past the
+    // largest, NaN 0): the first digit then tells apart weights of a few octaves,
+    // whatever those are.
+    uint32_t lo = 0xffffffffu, hi = 0;  // the smallest less 1, the largest plus 1
+    for (int s0 = first; s0 < end + first; s0 += kRound) {
+      if (!ONCE) orders(s0, false);
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
+      for (int q = 0; q < Q; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int s = s0 + 256 * q + e;
-            if (s < L) visit(rank_of(key[q][e], s));
-          }
+        for (int e = 0; e < 4; ++e) {
+          lo = min(lo, key[q][e] - 1);
+          hi = max(hi, key[q][e] + 1);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
+      hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
+    }
+    if (lane == 0) {
+      sums[0][wave] = lo;
+      sums[1][wave] = hi;
+    }
+    __syncthreads();
+    for (int i = 0; i < kEvictWaves; ++i) {
+      lo = min(lo, sums[0][i]);
+      hi = max(hi, sums[1][i]);
+    }
+    base = lo < hi ? lo : 0;  // none but late ones and NaN
+    late = lo < hi ? hi - lo : 1;
+    __syncthreads();
+    if (ONCE) distances();
+
+    uint32_t left = m;     // still to be taken among the values that start with edge
+    bool in_list = false;  // those are in `list`
+    // Whether a rank value, in halves, starts with edge from bit `from` up.
+    auto starts = [&](int from) {
+      const uint64_t bits = ~0ull << from;
+      const uint32_t high = (uint32_t)(edge >> 32), low = (uint32_t)edge;
+      const uint32_t of_high = (uint32_t)(bits >> 32), of_low = (uint32_t)bits;
+      return [=](uint32_t k, uint32_t l) {
+        return (((k ^ high) & of_high) | ((l ^ low) & of_low)) == 0;
+      };
+    };
+    // Visits what does, of those listed or of all slots; a block without any is
+    // left at once.
+    auto match_listed = [&](int from, auto &&visit) {
+      const auto is = starts(from);
+      for (int i = tid; i < (int)listed; i += kEvictThreads) {
+        const uint32_t k = list_high[i], l = list_low[i];
+        if (is(k, l)) visit(k, l);
       }
     };
-    // the fifth pass at the latest ends it: its bins are of 16 values, all distinct
-    for (int shift = 64 - kDigit;; shift -= kDigit) {
-      if (shift == 64 - kDigit)
-        each([&](uint64_t v) { atomicAdd(&hist[v >> (64 - kDigit)], 1u); });
-      else
-        each([&](uint64_t v) {
-          if ((v >> shift) >> kDigit == (edge >> shift) >> kDigit)
-            atomicAdd(&hist[(v >> shift) & (kBins - 1)], 1u);
-        });
+    auto match = [&](int from, auto &&visit) {
+      const auto is = starts(from);
+      for (int s0 = first; s0 < end + first; s0 += kRound) {
+        if (!ONCE) {
+          orders(s0, false);
+          distances();
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int block = s0 + 256 * q;
+          if (block >= L) break;
+          const uint32_t l = 0xffffffffu - (uint32_t)(block + mine);
+          bool any = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) any |= is(key[q][e], l - e);
+          if (__ballot(any) == 0) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (is(key[q][e], l - e)) visit(key[q][e], l - e);
+        }
+      }
+    };
+    // Digits from the highest bit that is set in any.  Five end it at the latest:
+    // from bit 8 down a bin has at most kRank values, all distinct.
+    const int top = 32 - __clz((int)late);  // late is at least 1
+    int from = 32 + max(top, kDigit), shift = from - kDigit;
+    for (int s0 = first; s0 < end + first; s0 += kRound) {
+      if (!ONCE) {
+        orders(s0, false);
+        distances();
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        if (s0 + 256 * q >= L) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) atomicAdd(&hist[key[q][e] >> (shift - 32)], 1u);
+      }
+    }
+    for (;;) {
       __syncthreads();
       {
         // from the top: thread t has bins 4 (1023 - t) .. + 3, and clears them
@@ -530,10 +640,19 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
       edge |= (uint64_t)picked << shift;
       left -= above;
       if (inside == left) break;
+      if (inside <= kList && !in_list) {
+        match(shift, [&](uint32_t k, uint32_t l) {
+          const uint32_t i = atomicAdd(&listed, 1u);
+          list_high[i] = k;
+          list_low[i] = l;
+        });
+        __syncthreads();
+        in_list = true;
+      }
       if (inside <= kRank) {
         // the left-th from the top of what starts with edge is the last kept
-        each([&](uint64_t v) {
-          if (v >> shift == edge >> shift) cand[atomicAdd(&ranked, 1u)] = v;
+        match_listed(shift, [&](uint32_t k, uint32_t l) {
+          cand[atomicAdd(&ranked, 1u)] = (uint64_t)k << 32 | l;
         });
         __syncthreads();
         const uint32_t n = ranked;
@@ -547,13 +666,17 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
         edge = edge_at;
         break;
       }
-      if (inside <= kList && !in_list) {
-        each([&](uint64_t v) {
-          if (v >> shift == edge >> shift) list[atomicAdd(&listed, 1u)] = v;
-        });
-        __syncthreads();
-        in_list = true;
-      }
+      from = shift;
+      shift = max(shift - kDigit, 0);
+      auto count = [&](uint32_t k, uint32_t l) {
+        const uint32_t digit =
+            shift >= 32 ? k >> (shift - 32) : __builtin_amdgcn_alignbit(k, l, shift);
+        atomicAdd(&hist[digit & ((1u << (from - shift)) - 1)], 1u);
+      };
+      if (in_list)
+        match_listed(from, count);
+      else
+        match(from, count);
     }
   }
 
@@ -562,22 +685,27 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
   const int edge_slot = (int)min(0xffffffffu - (uint32_t)edge, 0x7fffffffu);
   uint32_t holes = 0, fills = 0;  // before this round
   for (int s0 = first; s0 < end + first; s0 += kRound) {
-    if (!ONCE) orders(s0, false);
+    if (!ONCE) {
+      orders(s0, false);
+      distances();
+    }
     // 4 bits a q: evicted in front of m, kept behind it
-    uint32_t hole = 0, fill = 0, n_holes = 0, n_fills = 0;
+    uint32_t hole = 0, fill = 0;
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
+    for (int q = 0; q < Q; ++q) {
+      const int s = s0 + 256 * q + mine;
+      uint32_t kept = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int s = s0 + 256 * q + e;
-        const uint32_t k = key[q][e];
-        const bool kept = k > edge_key || (k == edge_key && s <= edge_slot);
-        const bool ho = s < m && !kept, fi = s >= m && s < L && kept;
-        hole |= (uint32_t)ho << (4 * q + e);
-        fill |= (uint32_t)fi << (4 * q + e);
-        n_holes += __popcll(__ballot(ho));
-        n_fills += __popcll(__ballot(fi));
-      }
+      for (int e = 0; e < 4; ++e)
+        kept |= (uint32_t)(key[q][e] >= (s + e <= edge_slot ? edge_key : edge_key + 1)) << e;
+      const uint32_t front = (1u << max(0, min(m - s, 4))) - 1;
+      hole |= (front & ~kept) << (4 * q);
+      fill |= (kept & ~front) << (4 * q);
+    }
+    uint32_t both = __popc(hole) | __popc(fill) << 16;  // at most 256 Q each in a wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) both += __shfl_xor((int)both, d);
+    const uint32_t n_holes = both & 0xffff, n_fills = both >> 16;
     __syncthreads();
     if (lane == 0) {
       sums[0][wave] = n_holes;
@@ -595,6 +723,7 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
     auto number = [&](uint32_t bits, uint32_t place, bool to) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
+        if (__ballot(bits >> (4 * q) & 15) == 0) continue;
         uint32_t n = place;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -605,7 +734,7 @@ __global__ __launch_bounds__(kEvictThreads) void select_kernel(EvictArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (bits >> (4 * q + e) & 1) {
-            (to ? mv[n].y : mv[n].x) = s0 + 256 * q + e;
+            *nth<int32_t>(mv, 2 * n + to) = s0 + 256 * q + mine + e;
             ++n;
           }
       }
