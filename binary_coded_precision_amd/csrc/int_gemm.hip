@@ -415,9 +415,9 @@ struct TileShape {
 };
 
 template <typename T, int BM, int BT, int WM, int WT, bool SPLIT>
-__global__ __launch_bounds__(WM *WT * 64, BM * BT <= 128 * 128 ? 2 : 1) void tile_kernel(IntProduct p, int tiles_m, int tiles_t,
-                                                           int slices, int slice_steps,
-                                                           int32_t *partial) {
+__global__ __launch_bounds__(WM *WT * 64, BM * BT <= 128 * 128 ? 2 : 1) void tile_kernel(
+    IntProduct p, int begin, int count, int tiles, int tiles_t, int slice_steps,
+    int32_t *partial) {
   using S = TileShape<BM, BT, WM, WT>;
   __shared__ __align__(16) int8_t lds[2][S::kStageBytes];
   __shared__ __align__(16) float row_scales[BM], row_bias[BM];
@@ -425,12 +425,12 @@ __global__ __launch_bounds__(WM *WT * 64, BM * BT <= 128 * 128 ? 2 : 1) void til
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // workgroups go to the 8 XCDs in turn: each XCD gets a run of tiles that
   // shares rows of W
-  const int tiles = tiles_m * tiles_t;
-  const int per = (tiles * slices + 7) / 8;
-  const int id = (int)(blockIdx.x % 8) * per + (int)blockIdx.x / 8;
-  if (id >= tiles * slices) return;
-  const int slice = id / tiles, tile = id % tiles;
+  const int per = (count + 7) / 8;
+  const int nth = (int)(blockIdx.x % 8) * per + (int)blockIdx.x / 8;
+  if (nth >= count) return;
+  const int slice = (begin + nth) / tiles, tile = (begin + nth) % tiles;
   const int m0 = tile / tiles_t * BM, t0 = tile % tiles_t * BT;
+  if (t0 >= p.T) return;  // the second half of a last tile
   const int K16 = (p.K + 15) / 16 * 16;
   const int steps = (p.K + kStep - 1) / kStep;
   const int first = slice * slice_steps, last = min(steps, first + slice_steps);
@@ -613,9 +613,16 @@ __global__ __launch_bounds__(256) void join_kernel(IntProduct p, int slices,
 // the small tiles leave compute units idle K is split, never under eight steps.
 // Up to kFewTokens tokens go through the ring instead (side 32 or 64, their
 // number rounded up).
+//
+// Where the tiles of 256 fill the compute units a few times and at most half of
+// them once more, those last tiles go in halves (256 x 128, 0.88 of the rate) to
+// all of them, in a launch of their own: 4096 tokens by 14336 x 4096, 896 tiles,
+// take 293 us so and 309 in whole tiles.
 constexpr int kFewTokens = 64;
+constexpr int kUnits = 256;
 struct TilePlan {
   int side, tiles_m, tiles_t, slices, slice_steps;
+  int halves;  // of the last tiles of 256: in two halves each
   bool few;
 };
 TilePlan tile_plan(int T, int M, int K) {
@@ -642,10 +649,14 @@ TilePlan tile_plan(int T, int M, int K) {
   for (int i = 0; i < 3; ++i) {
     const int b = sides[i];
     const int64_t tiles = (int64_t)((M + b - 1) / b) * ((T + b - 1) / b);
-    const double cost = (double)((tiles + 255) / 256) * b * b / rate[i];
+    const int64_t over = tiles % kUnits;
+    const bool halved = b == 256 && tiles > kUnits && over > 0 && over <= kUnits / 2;
+    const double rounds = (double)(tiles / kUnits) + (over == 0 ? 0 : halved ? 0.6 : 1);
+    const double cost = rounds * b * b / rate[i];
     if (i == 0 || cost < best) {
       best = cost;
       q.side = b;
+      q.halves = halved ? (int)over * 2 : 0;
     }
   }
   const int b = q.side;
@@ -655,16 +666,18 @@ TilePlan tile_plan(int T, int M, int K) {
   return q;
 }
 
-template <typename T, int B, int WM, int WT, bool SPLIT>
-void run_tiles(const IntProduct &p, const TilePlan &q, int32_t *partial, hipStream_t s) {
-  const unsigned grid = (unsigned)(((int64_t)q.tiles_m * q.tiles_t * q.slices + 7) / 8 * 8);
-  tile_kernel<T, B, B, WM, WT, SPLIT><<<grid, WM * WT * 64, 0, s>>>(
-      p, q.tiles_m, q.tiles_t, q.slices, q.slice_steps, partial);
+// Tiles begin .. begin + count of the grid of BM by BT tiles.
+template <typename T, int BM, int BT, int WM, int WT, bool SPLIT>
+void run_tiles(const IntProduct &p, const TilePlan &q, int tiles_t, int begin, int count,
+               int32_t *partial, hipStream_t s) {
+  tile_kernel<T, BM, BT, WM, WT, SPLIT><<<(count + 7) / 8 * 8, WM * WT * 64, 0, s>>>(
+      p, begin, count, q.tiles_m * tiles_t, tiles_t, q.slice_steps, partial);
 }
 
 template <typename T>
 hipError_t gemm_type(const IntProduct &p, int32_t *partial, hipStream_t s) {
   const TilePlan q = tile_plan(p.T, p.M, p.K);
+  const int tiles = q.tiles_m * q.tiles_t;
   if (q.few) {
     const unsigned grid = (unsigned)q.tiles_m * q.slices;
     if (q.side == 32 && q.slices == 1)
@@ -676,13 +689,19 @@ hipError_t gemm_type(const IntProduct &p, int32_t *partial, hipStream_t s) {
     else
       few_kernel<T, 64, true><<<grid, 256, 0, s>>>(p, q.tiles_m, q.slice_steps, partial);
   } else if (q.side == 256) {
-    run_tiles<T, 256, 4, 2, false>(p, q, partial, s);
+    run_tiles<T, 256, 256, 4, 2, false>(p, q, q.tiles_t, 0, tiles - q.halves / 2, partial, s);
+    if (q.halves > 0) {
+      hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      run_tiles<T, 256, 128, 4, 2, false>(p, q, 2 * q.tiles_t, 2 * tiles - q.halves, q.halves,
+                                          partial, s);
+    }
   } else if (q.side == 128) {
-    run_tiles<T, 128, 2, 2, false>(p, q, partial, s);
+    run_tiles<T, 128, 128, 2, 2, false>(p, q, q.tiles_t, 0, tiles, partial, s);
   } else if (q.slices == 1) {
-    run_tiles<T, 64, 2, 2, false>(p, q, partial, s);
+    run_tiles<T, 64, 64, 2, 2, false>(p, q, q.tiles_t, 0, tiles, partial, s);
   } else {
-    run_tiles<T, 64, 2, 2, true>(p, q, partial, s);
+    run_tiles<T, 64, 64, 2, 2, true>(p, q, q.tiles_t, 0, tiles * q.slices, partial, s);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || q.slices == 1) return e;

@@ -106,7 +106,8 @@ def test_linear(T, M, K, dtype):
 @pytest.mark.parametrize("T,M,K", [
     (3, 50, 5461), (20, 70, 4100), (40, 64, 5000), (64, 8000, 1040),  # few tokens, K split or not
     (100, 100, 4096), (300, 257, 2049),  # the small tile, K split
-    (1001, 4000, 160), (4090, 4104, 144)])  # the larger tiles, outputs of whole 16 bytes
+    (1001, 4000, 160), (4090, 4104, 144),  # the larger tiles, outputs of whole 16 bytes
+    (4100, 5104, 144)])  # the last of 340 tiles in halves, some of them past the tokens
 def test_linear_by_way(T, M, K, dtype):
     test_linear(T, M, K, dtype)
 
