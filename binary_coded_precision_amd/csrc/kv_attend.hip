@@ -15,14 +15,15 @@
 // four bits up are 16c * 2^-24, and the queries of those channels carry 1/16.
 // Codes of V are centred: an average over many tokens is small against its
 // terms, and what the terms' roundings leave would otherwise be multiplied by
-// the 7.5 that the codes have in common (measured over 1023 tokens: 8e-4 of the
-// output's norm without centring, 3e-4 with it, of which 2e-4 is the output's
-// rounding).
+// the 7.5 that the codes have in common, which the matrix cores' sums, cut off
+// downwards at each addition (below), would show.
 //
-// Roundings below 32 bits, for fp16 calls: p_t * vs_t, once, to fp16, relative
-// to the row's largest (below).  It is as large as the output's own rounding.
-// For fp32 calls the queries (after a power of two for each row) and p_t * vs_t
-// are each held as the sum of two fp16, 22 bits; and as the matrix cores cut off
+// Roundings below 32 bits: p_t * vs_t is held as the sum of two fp16, 22 bits
+// relative to the row's largest (below), and for fp32 calls the queries are too
+// (after a power of two for each row).  One fp16 for p_t * vs_t would add an error
+// as large as an fp16 output's own rounding: 3.0e-4 to 3.4e-4 of the output's norm
+// in all, against 2.1e-4 (and 2048 queries over 6001 and 3001 tokens would take
+// 396 us, not 451).  As the matrix cores cut off
 // what they add to a running sum, 1e-7 of it each time and always downwards
 // (measured), fp32 calls start every product at zero and sum in ordinary fp32.
 //
@@ -70,6 +71,7 @@ struct Ws {
 
 union Frag {
   uint32_t w[4];
+  half2v p[4];
   half8 h;
 };
 
@@ -389,20 +391,15 @@ __device__ __forceinline__ ushort2v pair16(uint32_t w) {
   return x.h;
 }
 
-// fp16(p * the lower half of w) to the lower or upper half of `to`, one rounding
-// and one instruction.
-__device__ __forceinline__ void scaled_low(uint32_t &to, float p, uint32_t w) {
-  asm("v_fma_mixlo_f16 %0, %1, %2, 0 op_sel_hi:[0,1,0]" : "=v"(to) : "v"(p), "v"(w));
-}
-__device__ __forceinline__ void scaled_high(uint32_t &to, float p, uint32_t w) {
-  asm("v_fma_mixhi_f16 %0, %1, %2, 0 op_sel_hi:[0,1,0]" : "+v"(to) : "v"(p), "v"(w));
+__device__ __forceinline__ half2v cut(float a, float b) {
+  return __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_pkrtz(a, b));
 }
 
 // The softmax's step over 32 tokens: raises the rows' references, rescales, adds
-// to their sums and leaves probability times V scale in P.
-template <int D, int CT, bool TWO>
-__device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, half8 (&P)[CT],
-                                              half8 (&Plo)[TWO ? CT : 1],
+// to their sums and leaves probability times V scale in P, what that rounds off in
+// Plo.
+template <int D, int CT>
+__device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Frag (&Plo)[CT],
                                               const float4v (&S)[2][CT], const Tiles<D> &T,
                                               float unit) {
   // The tile's largest score and largest V scale together bound its terms; only
@@ -450,42 +447,38 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, half8 (&P)[CT],
   float m[CT];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) m[ct] = fmaxf(A.m[ct], -3.0e38f);
-  Frag single[CT];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const half2v f = pair_of(T.m[s][2 * i + 1]);
-      const float mid = fmaf(7.5f, (float)f[0], (float)f[1]);
+    for (int i = 0; i < 4; i += 2) {
+      half2v f[2];
+      float mid[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f[j] = pair_of(T.m[s][2 * (i + j) + 1]);
+        mid[j] = fmaf(7.5f, (float)f[j][0], (float)f[j][1]);
+      }
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(S[s][ct][i], unit, -m[ct]));
-        A.l[ct] += p;
-        A.z[ct] = fmaf(p, mid, A.z[ct]);
-        if constexpr (TWO) {
-          float pv = p * (float)f[0];
-          // one value for both parts: the product and its rounding could be fused
-          asm volatile("" : "+v"(pv));
-          const _Float16 part = (_Float16)pv;
-          P[ct][4 * s + i] = part;
-          Plo[ct][4 * s + i] = (_Float16)(pv - (float)part);
-        } else if (i & 1) {
-          scaled_high(single[ct].w[2 * s + (i >> 1)], p, T.m[s][2 * i + 1]);
-        } else {
-          scaled_low(single[ct].w[2 * s + (i >> 1)], p, T.m[s][2 * i + 1]);
+        float pv[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(S[s][ct][i + j], unit, -m[ct]));
+          A.l[ct] += p;
+          A.z[ct] = fmaf(p, mid[j], A.z[ct]);
+          pv[j] = p * (float)f[j][0];
         }
+        // in pairs, cut off rather than rounded: what is left goes to Plo either way
+        const half2v part = cut(pv[0], pv[1]);
+        P[ct].p[2 * s + (i >> 1)] = part;
+        Plo[ct].p[2 * s + (i >> 1)] = cut(pv[0] - (float)part[0], pv[1] - (float)part[1]);
       }
     }
-  if constexpr (!TWO) {
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) P[ct] = single[ct].h;
-  }
 }
 
-template <int D, int CT, bool F32, bool TWO>
-__device__ __forceinline__ void add_values(Sums<D, CT> &A, const half8 (&P)[CT],
-                                           const half8 (&Plo)[TWO ? CT : 1],
-                                           const Tiles<D> &T) {
+template <int D, int CT, bool F32>
+__device__ __forceinline__ void add_values(Sums<D, CT> &A, const Frag (&P)[CT],
+                                           const Frag (&Plo)[CT], const Tiles<D> &T) {
 #pragma unroll
   for (int hh = 0; hh < D / 64; ++hh) {
     half8 vf[4];  // by the channel's place in its four
@@ -496,21 +489,28 @@ __device__ __forceinline__ void add_values(Sums<D, CT> &A, const half8 (&P)[CT],
 #pragma unroll
       for (int j = 0; j < 4; ++j) vf[j][2 * e] = x[j][0], vf[j][2 * e + 1] = x[j][1];
     }
+    if constexpr (F32) {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+      for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float4v &o = A.o[ct][4 * hh + j];
-        if constexpr (F32) {
+        for (int j = 0; j < 4; ++j) {
           float4v x = {0.f, 0.f, 0.f, 0.f};
-          x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct], x, 0, 0, 0);
-          o += __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct], x, 0, 0, 0);
-        } else {
-          if constexpr (TWO)
-            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct], o, 0, 0, 0);
-          o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct], o, 0, 0, 0);
+          x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct].h, x, 0, 0, 0);
+          A.o[ct][4 * hh + j] +=
+              __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct].h, x, 0, 0, 0);
         }
-      }
+    } else {
+      // no product waits for the one before it
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float4v &o = A.o[ct][4 * hh + j];
+            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], part ? P[ct].h : Plo[ct].h, o, 0, 0, 0);
+          }
+    }
   }
 }
 
@@ -552,12 +552,11 @@ __device__ __forceinline__ int by_length(const KvView &c, int rank, int lane) {
 // each time.  Or WR waves have rows of their own: then the sequences come by length
 // and their last rows, which see the most tokens, first, as workgroups are handed
 // out in order and the longest should not be left for last (2048 queries of
-// two sequences over 6001 and 3001 tokens, on two workgroups a compute unit: 458 us
-// in turns, 399 us by length).
+// two sequences over 6001 and 3001 tokens, on two workgroups a compute unit: 15%
+// more in turns than by length).
 template <int D, int CT, int WT, int WR, bool F32, bool STORE>
 __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void attend_kernel(AttendArgs a, int splits,
                                                              int row_blocks, Ws ws) {
-  constexpr bool TWO = F32 || WT > 1;  // probability times V scale in two fp16
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WT, wt = wave % WT;
@@ -636,10 +635,10 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
             *reinterpret_cast<float4v *>(sc[ct] + tile * 32 + 16 * s + 4 * g) =
                 S[s][ct] * a.unit;
     }
-    half8 P[CT], Plo[TWO ? CT : 1];
-    softmax_tiles<D, CT, TWO>(A, P, Plo, S, T, a.unit);
+    Frag P[CT], Plo[CT];
+    softmax_tiles<D, CT>(A, P, Plo, S, T, a.unit);
     load_m(T, a.c, w, lane);
-    add_values<D, CT, F32, TWO>(A, P, Plo, T);
+    add_values<D, CT, F32>(A, P, Plo, T);
     load_v(T, a.c, w, lane);
     tile = next;
   }

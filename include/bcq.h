@@ -548,10 +548,8 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
  *   heads of a cached head, in a fixed order.
  * Products run on the matrix cores with the codes as they are; softmax and
  * sums are in fp32.  Each token's probability times its V scale is held in 22
- * bits relative to the largest of its row, and in fp16 calls of more rows than
- * share a read of the cache (n * q_heads / heads past 32, or 16 at head_dim
- * 256) in 11; fp32 calls hold the queries in 22 bits too.  batch * n * q_heads
- * is at most 2^29.
+ * bits relative to the largest of its row; fp32 calls hold the queries in 22
+ * bits too.  batch * n * q_heads is at most 2^29.
  * workspace: bcq_kv_workspace_bytes(cache, n, q_heads, weights != NULL) bytes,
  *   16-byte aligned, of no account before and after; calls that may run at the
  *   same time need separate ones.  NULL when that is 0.
