@@ -22,7 +22,7 @@
 // relative to the row's largest (below), and for fp32 calls the queries are too
 // (after a power of two for each row).  One fp16 for p_t * vs_t would add an error
 // as large as an fp16 output's own rounding: 3.0e-4 to 3.4e-4 of the output's norm
-// in all, against 2.1e-4 (and 2048 queries over 6001 and 3001 tokens would take
+// in all, against 2.1e-4 (and 2048 queries over 6001 and 4501 tokens would take
 // 396 us, not 451).  As the matrix cores cut off
 // what they add to a running sum, 1e-7 of it each time and always downwards
 // (measured), fp32 calls start every product at zero and sum in ordinary fp32.
@@ -552,8 +552,15 @@ __device__ __forceinline__ int by_length(const KvView &c, int rank, int lane) {
 // each time.  Or WR waves have rows of their own: then the sequences come by length
 // and their last rows, which see the most tokens, first, as workgroups are handed
 // out in order and the longest should not be left for last (2048 queries of
-// two sequences over 6001 and 3001 tokens, on two workgroups a compute unit: 15%
+// two sequences over 6001 and 4501 tokens, on two workgroups a compute unit: 15%
 // more in turns than by length).
+//
+// With few rows it is bound by the cache's bytes: 32 sequences of 4224 to 8192
+// tokens, 8 cached heads of 128 channels (216 MB, and 25 MB of scores written)
+// take 57 us, 4.2 TB/s.
+// With many rows by the instructions that unpack codes and form probabilities:
+// 2 x 2048 queries of 32 heads over 6001 and 4501 tokens take 451 us;
+// their products alone would take 247 us at a library's fp16 rate.
 template <int D, int CT, int WT, int WR, bool F32, bool STORE>
 __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void attend_kernel(AttendArgs a, int splits,
                                                              int row_blocks, Ws ws) {
@@ -762,7 +769,8 @@ __device__ __forceinline__ float lse_of(const RowJoin &j) {
 
 // Joins the splits (blocks [0, join)), a wave a row, and adds the rows'
 // probabilities to the weights from the stored scores (the other blocks, 1024
-// tokens each).
+// tokens each).  Bound by reading both: 1024 rows and the weights of 8 heads of
+// 32 sequences of 4224 to 8192 tokens (38 MB and the outputs) take 8.7 us.
 constexpr int kSumTokens = 1024;
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int join, bool f32,
