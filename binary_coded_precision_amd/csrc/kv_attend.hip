@@ -879,58 +879,86 @@ __device__ __forceinline__ float row_lse(const Ws &ws, int splits, int64_t strid
   return m + log2f(l);
 }
 
-// The weights of many rows: 32 tokens a workgroup, whose waves take turns over
-// the row tiles and recompute the scores from the K codes; the sums stay in
-// registers, so no atomics and a fixed order.
-template <int D, bool F32>
+// The weights of many rows: 32 TN tokens a workgroup, whose waves take turns over
+// the row tiles and form the scores again from the K codes; the sums stay in
+// registers, so no atomics and a fixed order.  A row tile's queries and factors
+// cost more to bring in than 32 tokens' scores: they are asked for a tile ahead,
+// and TN is 2, what the registers hold as unpacked codes up to 128 channels, where
+// that leaves two workgroups for each compute unit.  2 x 2048 queries of 32 heads
+// over 6001 and 4501 tokens (128 channels, 8 cached heads): 371 us; 577 without
+// the tile ahead, 788 with TN = 1 as well.  At 4 x 1000 over 1000 (64 channels)
+// 50 us against 72; TN = 4 took 93.
+template <int D, bool F32, int TN>
 __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, Ws ws) {
-  __shared__ float part[4][32];
+  __shared__ float part[4][32 * TN];
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int BH = a.c.B * a.c.H, R = a.n * a.G;
   const int64_t rows = (int64_t)BH * R;
-  const int bh = blockIdx.x % BH, stride = gridDim.x / BH * 32;
+  const int bh = blockIdx.x % BH, stride = gridDim.x / BH * 32 * TN;
   const int b = bh / a.c.H, h = bh % a.c.H;
   const int L = kv_len(a.c, b);
-  for (int t = blockIdx.x / BH * 32; t < L; t += stride) {
-    Tiles<D> T;
-    const Where at = where(a.c, b, h, t, L);
-    load_k(T, a.c, at, lane);
-    load_m(T, a.c, at, lane);
-    float sum[8];
+  for (int t = blockIdx.x / BH * 32 * TN; t < L; t += stride) {
+    Tiles<D> T[TN];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    for (int k = 0; k < TN; ++k) {
+      // tiles past the last token are the first one again, and not written
+      const Where at = where(a.c, b, h, t + 32 * k < L ? t + 32 * k : t, L);
+      load_k(T[k], a.c, at, lane);
+      load_m(T[k], a.c, at, lane);
+    }
+    float sum[TN][8];
+#pragma unroll
+    for (int k = 0; k < TN; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[k][i] = 0.f;
     // the first query that sees token t
     const int first = max(0, t - (L - a.n)) * a.G / 16;
+    // a row tile's queries and factors are asked for while the one before is summed
+    RawQueries<D, 1, F32> raw;
+    float2 ml{};
+    auto ask = [&](int rt) {
+      fetch_queries<D, 1, F32>(raw, a, b, h, rt * 16, R, lane);
+      ml = ws.ml[(int64_t)bh * R + min(rt * 16 + (lane & 15), R - 1)];
+    };
+    if ((first + wave) * 16 < R) ask(first + wave);
     for (int rt = first + wave; rt * 16 < R; rt += 4) {
       Queries<D, 1, F32> Q;
-      RawQueries<D, 1, F32> raw;
-      fetch_queries<D, 1, F32>(raw, a, b, h, rt * 16, R, lane);
       load_queries<D, 1, F32>(Q, raw, a.negate, rt * 16, R, lane);
       const int row = rt * 16 + (lane & 15);
-      const float lse = row < R ? row_lse(ws, splits, rows, (int64_t)bh * R + row) : INFINITY;
       const int last = row < R ? L - a.n + row / a.G : -1;
+      float lse = INFINITY;
+      if (splits > 1)
+        lse = row_lse(ws, splits, rows, (int64_t)bh * R + min(row, R - 1));
+      else if (ml.x != kNegInf)
+        lse = ml.x + log2f(ml.y);
+      if ((rt + 4) * 16 < R) ask(rt + 4);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        float4v S[1];
-        tile_scores<D, 1, F32>(S, T, s, Q);
+      for (int k = 0; k < TN; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = raw_score(S[0][i], Q.sum[0], T.m[s][2 * i]);
-          sum[4 * s + i] += t + 16 * s + 4 * g + i > last
-                                ? 0.f
-                                : __builtin_amdgcn_exp2f(fmaf(x, a.unit, -lse));
+        for (int s = 0; s < 2; ++s) {
+          float4v S[1];
+          tile_scores<D, 1, F32>(S, T[k], s, Q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = raw_score(S[0][i], Q.sum[0], T[k].m[s][2 * i]);
+            sum[k][4 * s + i] += t + 32 * k + 16 * s + 4 * g + i > last
+                                     ? 0.f
+                                     : __builtin_amdgcn_exp2f(fmaf(x, a.unit, -lse));
+          }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < TN; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x = sum[k][i];
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) x += __shfl_xor(x, d);
+        if ((lane & 15) == 0) part[wave][32 * k + 16 * (i >> 2) + 4 * g + (i & 3)] = x;
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int k = 1; k < 16; k <<= 1) sum[i] += __shfl_xor(sum[i], k);
-      if ((lane & 15) == 0) part[wave][16 * (i >> 2) + 4 * g + (i & 3)] = sum[i];
-    }
     __syncthreads();
-    if (threadIdx.x < 32 && t + (int)threadIdx.x < L) {
+    if (threadIdx.x < 32 * TN && t + (int)threadIdx.x < L) {
       const int i = threadIdx.x;
       a.weights[(int64_t)bh * a.c.room() + t + i] +=
           part[0][i] + part[1][i] + (part[2][i] + part[3][i]);
@@ -987,8 +1015,13 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
   }
   if (a.weights != nullptr && !p.scores) {
     // a launch's work items are counted in 32 bits: longer rows take turns
-    const int chunks = (int)std::min<int64_t>((room + 31) / 32, kMaxGroups / BH);
-    weights_kernel<D, F32><<<BH * chunks, 256, 0, s>>>(a, p.splits, ws);
+    constexpr int kTiles = D <= 128 ? 2 : 1;
+    const int wide = (room + 32 * kTiles - 1) / (32 * kTiles), narrow = (room + 31) / 32;
+    if ((int64_t)BH * wide >= 512)
+      weights_kernel<D, F32, kTiles>
+          <<<BH * std::min(wide, kMaxGroups / BH), 256, 0, s>>>(a, p.splits, ws);
+    else
+      weights_kernel<D, F32, 1><<<BH * narrow, 256, 0, s>>>(a, p.splits, ws);
     e = hipGetLastError();
   }
   return e;

@@ -115,6 +115,29 @@ def test_attend(lens, n, Hq, H, D, page, dtype, weights):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("n,Hq,D", [(40, 8, 64), (19, 16, 128), (9, 16, 256)])
+def test_attend_weights_of_many_rows_in_a_large_cache(n, Hq, D, dtype):
+    """Room for far more tokens than there are: the weights' workgroups take several tiles each."""
+    lens, H, page, width = [70, 33, 0, 129], 8, 16, 65
+    say("kv_attend weights", n, Hq, D, dtype)
+    c = make(lens, H, D, page, width, seed=n)
+    dev = device(c)
+    q = np.random.default_rng(2).normal(size=(4, n, Hq, D)).astype(DT[dtype][1])
+    o = torch.empty(q.shape, dtype=DT[dtype][0], device="cuda")
+    w = torch.full((4, H, dev.room), 0.25, device="cuda")
+    bcq.bcq_kv_attend(dev, torch.from_numpy(q).cuda(), o, weights=w)
+    ref, total, b, wb = lb.attend(c, q, np.float32(1 / math.sqrt(D)))
+    err = np.abs(o.cpu().numpy().astype(np.float64) - ref)
+    assert (err <= bound(ref, b, D, max(lens), dtype)).all()
+    got = w.cpu().numpy().astype(np.float64)
+    T = total.shape[2]
+    tol = 4 * D * 2.0**-24 * 2 * wb + (T + n * Hq + 16) * 2.0**-23 * (total + 0.25)
+    assert (np.abs(got[..., :T] - 0.25 - total) <= tol).all()
+    for i, L in enumerate(lens):
+        assert (got[i, :, L:] == 0.25).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("spread", [1e-4, 1e3, None])
 def test_attend_v_scales_of_any_size(spread, dtype):
     """Values all tiny, all large, or from 1e-3 to 1e3 within a row."""
