@@ -417,7 +417,6 @@ constexpr int kStep = 128;
 
 template <int BM, int BT, int WM, int WT>
 struct TileShape {
-  static constexpr int kThreads = WM * WT * 64;
   static constexpr int kRows = BM / WM, kTokens = BT / WT;    // of a wave
   static constexpr int kM = kRows / 32, kT = kTokens / 32;    // its 32x32 tiles
   static constexpr int kLoads = (BM + BT) / 8 / (WM * WT);    // of 1 KB, a wave and stage

@@ -508,7 +508,8 @@ __device__ __forceinline__ void add_values(Sums<D, CT> &A, const Frag (&P)[CT],
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float4v &o = A.o[ct][4 * hh + j];
-            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], part ? P[ct].h : Plo[ct].h, o, 0, 0, 0);
+            const half8 p = part ? P[ct].h : Plo[ct].h;
+            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], p, o, 0, 0, 0);
           }
     }
   }
@@ -562,8 +563,8 @@ __device__ __forceinline__ int by_length(const KvView &c, int rank, int lane) {
 // 2 x 2048 queries of 32 heads over 6001 and 4501 tokens take 451 us;
 // their products alone would take 247 us at a library's fp16 rate.
 template <int D, int CT, int WT, int WR, bool F32, bool STORE>
-__global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void attend_kernel(AttendArgs a, int splits,
-                                                             int row_blocks, Ws ws) {
+__global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void attend_kernel(
+    AttendArgs a, int splits, int row_blocks, Ws ws) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WT, wt = wave % WT;
