@@ -192,7 +192,12 @@ __device__ __forceinline__ void store_sums(int32_t *token, int m, int M, int4v s
 // launch of its own costs several.  One token by 4096 x 4096 (16.8 MB) takes
 // 8.4 us, the launch and the chain from a token's first load to its codes among
 // them; reading the weights alone would take 3.3 us.
-constexpr int kFusedTokens = 16, kFusedElements = 16384;
+//
+// Up to two tokens: each one more costs every workgroup 1.7 us of loads, extremes
+// and codes one after the other, and the two launches of the way below cost 3 (us
+// in a graph, by 4096 x 4096: one token 8.0 against 11.2, two 9.6 against 11.8,
+// three 11.5 each, four 12.8 against 11.8; eight by 4096 x 1024 11.5 against 6.3).
+constexpr int kFusedTokens = 2, kFusedElements = 16384;
 constexpr int kFusedDepth = 8;  // steps in flight
 
 template <typename T>
