@@ -438,12 +438,13 @@ def test_evict(lens, keep, recent, H, D, page, room, kind):
         assert torch.equal(pd[b, :, :m], po[b, :, :m])
 
 
-# evictions of three and four tokens, moves made by the selecting workgroup at every number of
+# evictions of one to four tokens, moves made by the selecting workgroup at every number of
 # channels, more equal weights than are listed
 @pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
 @pytest.mark.parametrize("lens,keep,recent,H,D,page,room", [
     ([68, 67], 64, 10, 2, 64, 16, 80), ([5003], 5000, 9, 1, 64, 64, 5056),
     ([250], 200, 10, 1, 256, 64, 256), ([5056, 5030], 5000, 40, 1, 128, 32, 5056),
+    ([5002, 5001], 5000, 9, 1, 64, 64, 5056), ([33002], 33000, 7, 1, 64, 256, 33024),
     ([5056], 1000, 100, 1, 64, 64, 5056), ([33024], 33020, 7, 1, 64, 256, 33024)])
 def test_evict_by_way(lens, keep, recent, H, D, page, room, kind):
     test_evict(lens, keep, recent, H, D, page, room, kind)
