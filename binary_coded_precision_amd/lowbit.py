@@ -75,12 +75,18 @@ def _raw(t, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that a call on `stream` (None: the current one) may write at once: memory of that
+    stream's, as another's may still be in use there by what was queued before it was freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _workspace(n_bytes: int, device, stream):
-    """A workspace of n_bytes for a call on `stream`; the allocator learns of its use there."""
-    w = torch.empty(max(n_bytes, 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        w.record_stream(stream)
-    return w
+    """A workspace of n_bytes for a call on `stream`."""
+    return _empty(max(n_bytes, 1), torch.uint8, device, stream)
 
 
 def _float(name: str, t) -> int:
