@@ -143,15 +143,15 @@ def bcq_int_quantize(X, codes=None, scales=None, stream=None):
     """Rounds each row of ``X`` [rows][K] (fp16 or fp32, rows 16-byte aligned) to 8 bits.
 
     Returns ``(codes, scales)``: int8 [rows][K] (a view of rows padded to 16 bytes with zeros)
-    and fp32 [rows], allocated unless given."""
+    and fp32 [rows], allocated on ``stream`` unless given."""
     lib = _lib or _bind()
     dt = _float("X", X)
     rows, K = X.shape
     ldx = _rows("X", X, rows, K, K)
     if codes is None:
-        codes = torch.empty((rows, _pad16(K)), dtype=torch.int8, device=X.device)[:, :K]
+        codes = _empty((rows, _pad16(K)), torch.int8, X.device, stream)[:, :K]
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=X.device)
+        scales = _empty(rows, torch.float32, X.device, stream)
     if codes.dtype is not torch.int8 or not codes.is_cuda:
         raise ValueError("codes must be an int8 device tensor")
     if rows == 1:

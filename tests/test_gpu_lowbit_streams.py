@@ -65,3 +65,21 @@ def test_attention_on_two_streams_with_workspaces_of_their_own():
         bcq.bcq_kv_attend(c, q[1], got[1], stream=side)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_the_quantizers_outputs_dropped_before_it_has_run():
+    """What the current stream allocates next is not what another stream is still to write."""
+    say("int_quantize on another stream")
+    x = torch.randn((512, 4096), device="cuda", dtype=torch.float16)
+    big = torch.randn((4096, 4096), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy(big)
+    codes, scales = bcq.bcq_int_quantize(x, stream=side)
+    shape, n = codes.shape, len(scales)
+    del codes, scales
+    mine = torch.full(shape, 3, dtype=torch.int8, device="cuda")
+    ones = torch.ones(n, device="cuda")
+    torch.cuda.synchronize()
+    assert (mine == 3).all() and (ones == 1).all()

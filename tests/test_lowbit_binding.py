@@ -124,3 +124,14 @@ def test_a_workspace_is_memory_of_the_stream_it_is_used_on(machine, name):
     with_workspace()[name](side)
     assert machine.allocated == [(side, 0)]
     assert machine.calls[0][0] == name and machine.calls[0][1][-1] == 7
+
+
+def test_the_quantizers_outputs_are_memory_of_its_stream(machine):
+    """Dropped early, they may be handed out again only to what is queued behind the call."""
+    side = Stream(7)
+    codes, scales = lowbit.bcq_int_quantize(zeros(3, 64), stream=side)
+    assert machine.allocated == [(side, 0), (side, 0)]
+    assert codes.shape == (3, 64) and scales.shape == (3,)
+    machine.allocated.clear()
+    lowbit.bcq_int_quantize(zeros(3, 64))
+    assert machine.allocated == [(None, 0), (None, 0)]
