@@ -89,6 +89,13 @@ def _workspace(n_bytes: int, device, stream):
     return _empty(max(n_bytes, 1), torch.uint8, device, stream)
 
 
+def _space(t):
+    """(address, bytes) of a workspace."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    return t.data_ptr(), t.nbytes
+
+
 def _float(name: str, t) -> int:
     """The dtype code of a device tensor of fp16 or fp32."""
     if not t.is_cuda:
@@ -187,7 +194,7 @@ def bcq_int_gemm(A, a_scales, W, w_scales, Y, bias=None, workspace=None, stream=
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
     r = lib.bcq_int_gemm(A.data_ptr(), _plain("a_scales", a_scales, torch.float32, (T,)), T, lda,
                          W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(), ldy, dt,
-                         workspace.data_ptr(), workspace.nbytes, _raw(W, stream))
+                         *_space(workspace), _raw(W, stream))
     if r:
         _fail("bcq_int_gemm", r)
 
@@ -209,7 +216,7 @@ def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) ->
     if workspace is None:
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
     r = lib.bcq_int_linear(X.data_ptr(), T, ldx, W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(),
-                           ldy, dt, workspace.data_ptr(), workspace.nbytes, _raw(W, stream))
+                           ldy, dt, *_space(workspace), _raw(W, stream))
     if r:
         _fail("bcq_int_linear", r)
 
@@ -343,7 +350,7 @@ def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None
         cache._ref, Q.data_ptr(), n, heads, qs[0], qs[1], qs[2], O.data_ptr(), os[0], os[1],
         os[2], dt, shape[3] ** -0.5 if scale is None else scale,
         0 if weights is None else _plain("weights", weights, torch.float32, cache._slots),
-        workspace.data_ptr(), workspace.nbytes, _raw(Q, stream))
+        *_space(workspace), _raw(Q, stream))
     if r:
         _fail("bcq_kv_attend", r)
 
@@ -372,6 +379,6 @@ def bcq_kv_evict(cache: KVCache, keep: int, recent: int, weights, pos, lens_out=
         else _plain("lens_out", lens_out, i32, (cache.batch,)),
         w if weights_out is None else _plain("weights_out", weights_out, f32, slots),
         p if pos_out is None else _plain("pos_out", pos_out, i32, slots),
-        workspace.data_ptr(), workspace.nbytes, _raw(weights, stream))
+        *_space(workspace), _raw(weights, stream))
     if r:
         _fail("bcq_kv_evict", r)

@@ -135,3 +135,22 @@ def test_the_quantizers_outputs_are_memory_of_its_stream(machine):
     machine.allocated.clear()
     lowbit.bcq_int_quantize(zeros(3, 64))
     assert machine.allocated == [(None, 0), (None, 0)]
+
+
+@pytest.mark.parametrize("bad", ["host", "strided"])
+def test_a_workspace_that_kernels_cannot_write_is_refused(machine, bad):
+    w = torch.zeros(1 << 13, dtype=torch.uint8)
+    if bad == "strided":  # its bytes are fewer than its extent says
+        w = OnDevice(w[:16].expand(512, 16))
+    x, y = zeros(3, 64), zeros(3, 4)
+    a, b = zeros(3, 64, dtype=torch.int8), zeros(4, 64, dtype=torch.int8)
+    s = {n: zeros(n, dtype=torch.float32) for n in (3, 4)}
+    q, c = zeros(1, 1, 1, 64), cache()
+    weights, pos = zeros(1, 1, 32, dtype=torch.float32), zeros(1, 1, 32, dtype=torch.int32)
+    for call in (lambda: lowbit.bcq_int_linear(x, b, s[4], y, workspace=w),
+                 lambda: lowbit.bcq_int_gemm(a, s[3], b, s[4], y, workspace=w),
+                 lambda: lowbit.bcq_kv_attend(c, q, q, workspace=w),
+                 lambda: lowbit.bcq_kv_evict(c, 5, 1, weights, pos, workspace=w)):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
+    assert not machine.calls
