@@ -1,6 +1,9 @@
 """Binding of the low-bit serving operators: the 8-bit integer linear layer and the 4-bit
 key/value cache (append, read, attend, evict).  Names and semantics are those of
 ``include/bcq.h``; the package exports everything here.
+
+The tensors of a call, and its ``stream`` if one is given, belong to one device, which need not be
+the current one.
 """
 
 from __future__ import annotations
@@ -68,11 +71,28 @@ def _pad16(n: int) -> int:
     return (n + 15) // 16 * 16
 
 
-def _raw(t, stream) -> int:
-    """The raw stream a call goes to: the given one, or the current one of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _device(name: str, t, stream) -> int:
+    """The device of a call: t's, which a given stream has to belong to."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    dev = t.get_device()
+    if stream is not None and stream.device_index != dev:
+        raise ValueError("stream must belong to the device of %s" % name)
+    return dev
+
+
+def _call(name: str, dev: int, stream, *args) -> None:
+    """Calls an entry point on `stream` (None: the device's current one).  Launches go to the
+    current device, so that has to be the tensors'."""
+    fn = getattr(_lib, name)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status:
+        _fail(name, status)
 
 
 def _empty(shape, dtype, device, stream):
@@ -89,17 +109,17 @@ def _workspace(n_bytes: int, device, stream):
     return _empty(max(n_bytes, 1), torch.uint8, device, stream)
 
 
-def _space(t):
+def _space(t, dev: int):
     """(address, bytes) of a workspace."""
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous device tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor on the call's device")
     return t.data_ptr(), t.nbytes
 
 
-def _float(name: str, t) -> int:
-    """The dtype code of a device tensor of fp16 or fp32."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % name)
+def _float(name: str, t, dev: int) -> int:
+    """The dtype code of a tensor of fp16 or fp32 on the call's device."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be a device tensor on the call's device" % name)
     d = t.dtype
     if d is torch.float16:
         return 1
@@ -108,11 +128,13 @@ def _float(name: str, t) -> int:
     raise TypeError("%s must be float16 or float32, got %s" % (name, d))
 
 
-def _plain(name: str, t, dtype, shape) -> int:
-    """The address of a contiguous device tensor of this dtype and shape."""
-    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s device tensor of shape %s, got %s of %s" %
-                         (name, dtype, tuple(shape), tuple(t.shape), t.dtype))
+def _plain(name: str, t, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this dtype and shape on the call's device."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
+            not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s device tensor of shape %s on device %d, got "
+                         "%s of %s on %s" % (name, dtype, tuple(shape), dev, tuple(t.shape),
+                                             t.dtype, t.device))
     return t.data_ptr()
 
 
@@ -151,52 +173,51 @@ def bcq_int_quantize(X, codes=None, scales=None, stream=None):
 
     Returns ``(codes, scales)``: int8 [rows][K] (a view of rows padded to 16 bytes with zeros)
     and fp32 [rows], allocated on ``stream`` unless given."""
-    lib = _lib or _bind()
-    dt = _float("X", X)
+    _lib or _bind()
+    dev = _device("X", X, stream)
+    dt = _float("X", X, dev)
     rows, K = X.shape
     ldx = _rows("X", X, rows, K, K)
     if codes is None:
         codes = _empty((rows, _pad16(K)), torch.int8, X.device, stream)[:, :K]
     if scales is None:
         scales = _empty(rows, torch.float32, X.device, stream)
-    if codes.dtype is not torch.int8 or not codes.is_cuda:
-        raise ValueError("codes must be an int8 device tensor")
+    if codes.dtype is not torch.int8 or codes.get_device() != dev:
+        raise ValueError("codes must be an int8 device tensor on X's device")
     if rows == 1:
         ldx = _pad16(ldx)  # a single row has no next one to be aligned with
-    r = lib.bcq_int_quantize(X.data_ptr(), dt, rows, K, ldx, codes.data_ptr(),
-                             _rows("codes", codes, rows, K, _pad16(K)),
-                             _plain("scales", scales, torch.float32, (rows,)), _raw(X, stream))
-    if r:
-        _fail("bcq_int_quantize", r)
+    _call("bcq_int_quantize", dev, stream, X.data_ptr(), dt, rows, K, ldx, codes.data_ptr(),
+          _rows("codes", codes, rows, K, _pad16(K)),
+          _plain("scales", scales, torch.float32, (rows,), dev))
     return codes, scales
 
 
-def _product(W, w_scales, Y, T: int, bias):
-    """Checks what the two products share; (M, K, ldw, ldy, dtype, scales', bias' address)."""
-    if W.dtype is not torch.int8 or not W.is_cuda:
+def _product(W, w_scales, Y, T: int, bias, stream):
+    """Checks what the two products share; (device, M, K, ldw, ldy, dtype, scales', bias'
+    address)."""
+    dev = _device("W", W, stream)
+    if W.dtype is not torch.int8:
         raise ValueError("W must be an int8 device tensor")
     M, K = W.shape
-    return (M, K, _rows("W", W, M, K, _pad16(K)), _rows("Y", Y, T, M, M), _float("Y", Y),
-            _plain("w_scales", w_scales, torch.float32, (M,)),
-            0 if bias is None else _plain("bias", bias, Y.dtype, (M,)))
+    return (dev, M, K, _rows("W", W, M, K, _pad16(K)), _rows("Y", Y, T, M, M),
+            _float("Y", Y, dev), _plain("w_scales", w_scales, torch.float32, (M,), dev),
+            0 if bias is None else _plain("bias", bias, Y.dtype, (M,), dev))
 
 
 def bcq_int_gemm(A, a_scales, W, w_scales, Y, bias=None, workspace=None, stream=None) -> None:
     """``Y[t][m] = (A[t] . W[m]) * (a_scales[t] * w_scales[m]) + bias[m]`` from 8-bit codes as
     :func:`bcq_int_quantize` returns them.  ``workspace`` as in :func:`bcq_int_linear`."""
-    lib = _lib or _bind()
+    _lib or _bind()
     T = A.shape[0]
-    M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias)
-    if A.dtype is not torch.int8 or not A.is_cuda:
-        raise ValueError("A must be an int8 device tensor")
+    dev, M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias, stream)
+    if A.dtype is not torch.int8 or A.get_device() != dev:
+        raise ValueError("A must be an int8 device tensor on W's device")
     lda = _rows("A", A, T, K, _pad16(K))
     if workspace is None:
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
-    r = lib.bcq_int_gemm(A.data_ptr(), _plain("a_scales", a_scales, torch.float32, (T,)), T, lda,
-                         W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(), ldy, dt,
-                         *_space(workspace), _raw(W, stream))
-    if r:
-        _fail("bcq_int_gemm", r)
+    _call("bcq_int_gemm", dev, stream, A.data_ptr(),
+          _plain("a_scales", a_scales, torch.float32, (T,), dev), T, lda, W.data_ptr(), sp, M, K,
+          ldw, bp, Y.data_ptr(), ldy, dt, *_space(workspace, dev))
 
 
 def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) -> None:
@@ -205,20 +226,18 @@ def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) ->
 
     ``workspace=None`` allocates one through torch; :func:`new_int_workspace` keeps that out of
     a hot loop."""
-    lib = _lib or _bind()
+    _lib or _bind()
     T = X.shape[0]
-    M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias)
-    if X.dtype is not Y.dtype or not X.is_cuda:
-        raise ValueError("X and Y must be device tensors of one dtype")
+    dev, M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias, stream)
+    if X.dtype is not Y.dtype or X.get_device() != dev:
+        raise ValueError("X and Y must be device tensors of one dtype on W's device")
     ldx = _rows("X", X, T, K, K)
     if T == 1:
         ldx = _pad16(ldx)  # a single row has no next one to be aligned with
     if workspace is None:
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
-    r = lib.bcq_int_linear(X.data_ptr(), T, ldx, W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(),
-                           ldy, dt, *_space(workspace), _raw(W, stream))
-    if r:
-        _fail("bcq_int_linear", r)
+    _call("bcq_int_linear", dev, stream, X.data_ptr(), T, ldx, W.data_ptr(), sp, M, K, ldw, bp,
+          Y.data_ptr(), ldy, dt, *_space(workspace, dev))
 
 
 # ----------------------------------------------------------------------------- 4-bit cache
@@ -239,12 +258,14 @@ class KVCache:
         P, H, page, half = k_codes.shape
         D = 2 * half
         B, width = page_table.shape
+        dev = self._dev = _device("k_codes", k_codes, None)
         self._st = _KVCache(
-            B, H, D, page, P, width, _plain("k_codes", k_codes, torch.uint8, (P, H, page, half)),
-            _plain("v_codes", v_codes, torch.uint8, (P, H, page // 4, 2 * D)),
-            _plain("scales", scales, torch.float16, (P, H, page, 4)),
-            _plain("page_table", page_table, torch.int32, (B, width)),
-            _plain("lens", lens, torch.int32, (B,)))
+            B, H, D, page, P, width,
+            _plain("k_codes", k_codes, torch.uint8, (P, H, page, half), dev),
+            _plain("v_codes", v_codes, torch.uint8, (P, H, page // 4, 2 * D), dev),
+            _plain("scales", scales, torch.float16, (P, H, page, 4), dev),
+            _plain("page_table", page_table, torch.int32, (B, width), dev),
+            _plain("lens", lens, torch.int32, (B,), dev))
         self._ref = ctypes.byref(self._st)
         self.k_codes, self.v_codes, self.scales = k_codes, v_codes, scales
         self.page_table, self.lens = page_table, lens
@@ -275,17 +296,18 @@ class KVCache:
         return self._ref
 
 
-def _pair(K, V, cache: KVCache):
+def _pair(K, V, cache: KVCache, stream):
     """(n, dtype, strides of K, of V) of vectors [batch][n][heads][D] with contiguous channels."""
+    _device("cache", cache.k_codes, stream)
     shape = K.shape
     if len(shape) != 4 or shape[0] != cache.batch or shape[2] != cache.heads or \
             shape[3] != cache.head_dim or V.shape != shape:
         raise ValueError("K and V must be [%d][n][%d][%d], got %s and %s" %
                          (cache.batch, cache.heads, cache.head_dim, tuple(shape),
                           tuple(V.shape)))
-    dt = _float("K", K)
-    if V.dtype is not K.dtype or not V.is_cuda:
-        raise ValueError("K and V must be device tensors of one dtype")
+    dt = _float("K", K, cache._dev)
+    if V.dtype is not K.dtype or V.get_device() != cache._dev:
+        raise ValueError("K and V must be device tensors of one dtype on the cache's device")
     ks, vs = K.stride(), V.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("K and V must have contiguous channels")
@@ -297,24 +319,21 @@ def bcq_kv_append(cache: KVCache, K, V, positions=None, weights=None, pos=None,
     """Quantizes ``K`` and ``V`` [batch][n][heads][D] into the last n slots of every sequence;
     ``cache.lens`` must count them already.  ``weights`` and ``pos`` [batch][heads][room] get 0
     and the token's position (``positions`` int32 [batch][n], or its slot)."""
-    n, dt, ks, vs = _pair(K, V, cache)
-    r = _lib.bcq_kv_append(
-        cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2], V.data_ptr(), vs[0], vs[1], vs[2], dt,
-        0 if positions is None else _plain("positions", positions, torch.int32,
-                                           (cache.batch, n)),
-        0 if weights is None else _plain("weights", weights, torch.float32, cache._slots),
-        0 if pos is None else _plain("pos", pos, torch.int32, cache._slots), _raw(K, stream))
-    if r:
-        _fail("bcq_kv_append", r)
+    n, dt, ks, vs = _pair(K, V, cache, stream)
+    dev, slots = cache._dev, cache._slots
+    _call("bcq_kv_append", dev, stream, cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2],
+          V.data_ptr(), vs[0], vs[1], vs[2], dt,
+          0 if positions is None else _plain("positions", positions, torch.int32,
+                                             (cache.batch, n), dev),
+          0 if weights is None else _plain("weights", weights, torch.float32, slots, dev),
+          0 if pos is None else _plain("pos", pos, torch.int32, slots, dev))
 
 
 def bcq_kv_read(cache: KVCache, K, V, stream=None) -> None:
     """Writes the values of the last n cached tokens to ``K`` and ``V`` [batch][n][heads][D]."""
-    n, dt, ks, vs = _pair(K, V, cache)
-    r = _lib.bcq_kv_read(cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2], V.data_ptr(), vs[0],
-                         vs[1], vs[2], dt, _raw(K, stream))
-    if r:
-        _fail("bcq_kv_read", r)
+    n, dt, ks, vs = _pair(K, V, cache, stream)
+    _call("bcq_kv_read", cache._dev, stream, cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2],
+          V.data_ptr(), vs[0], vs[1], vs[2], dt)
 
 
 def bcq_kv_workspace_bytes(cache: KVCache, n: int, q_heads: int, with_weights: bool) -> int:
@@ -333,11 +352,12 @@ def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None
     """Causal attention of ``Q`` [batch][n][q_heads][D], the queries of the last n cached tokens,
     over the cache into ``O`` (same shape); ``scale`` defaults to 1/sqrt(D).  ``weights``
     [batch][heads][room] float32 accumulates each cached token's probabilities."""
-    dt = _float("Q", Q)
+    dev = _device("cache", cache.k_codes, stream)
+    dt = _float("Q", Q, dev)
     shape = Q.shape
     if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim or \
-            O.shape != shape or O.dtype is not Q.dtype or not O.is_cuda:
-        raise ValueError("Q and O must be [%d][n][q_heads][%d] of one dtype" %
+            O.shape != shape or O.dtype is not Q.dtype or O.get_device() != dev:
+        raise ValueError("Q and O must be [%d][n][q_heads][%d] of one dtype on the cache's device" %
                          (cache.batch, cache.head_dim))
     n, heads = shape[1], shape[2]
     qs, os = Q.stride(), O.stride()
@@ -346,13 +366,10 @@ def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None
     if workspace is None:
         workspace = _workspace(bcq_kv_workspace_bytes(cache, n, heads, weights is not None),
                                Q.device, stream)
-    r = _lib.bcq_kv_attend(
-        cache._ref, Q.data_ptr(), n, heads, qs[0], qs[1], qs[2], O.data_ptr(), os[0], os[1],
-        os[2], dt, shape[3] ** -0.5 if scale is None else scale,
-        0 if weights is None else _plain("weights", weights, torch.float32, cache._slots),
-        *_space(workspace), _raw(Q, stream))
-    if r:
-        _fail("bcq_kv_attend", r)
+    _call("bcq_kv_attend", dev, stream, cache._ref, Q.data_ptr(), n, heads, qs[0], qs[1], qs[2],
+          O.data_ptr(), os[0], os[1], os[2], dt, shape[3] ** -0.5 if scale is None else scale,
+          0 if weights is None else _plain("weights", weights, torch.float32, cache._slots, dev),
+          *_space(workspace, dev))
 
 
 def bcq_kv_evict_workspace_bytes(cache: KVCache, keep: int) -> int:
@@ -370,15 +387,13 @@ def bcq_kv_evict(cache: KVCache, keep: int, recent: int, weights, pos, lens_out=
     the largest ``weights``.  In place unless ``lens_out``, ``weights_out``, ``pos_out`` are
     given (the codes always are: see ``include/bcq.h``)."""
     slots, f32, i32 = cache._slots, torch.float32, torch.int32
-    w, p = _plain("weights", weights, f32, slots), _plain("pos", pos, i32, slots)
+    dev = _device("cache", cache.k_codes, stream)
+    w, p = _plain("weights", weights, f32, slots, dev), _plain("pos", pos, i32, slots, dev)
     if workspace is None:
         workspace = _workspace(bcq_kv_evict_workspace_bytes(cache, keep), weights.device, stream)
-    r = _lib.bcq_kv_evict(
-        cache._ref, keep, recent, w, p,
-        cache.lens.data_ptr() if lens_out is None
-        else _plain("lens_out", lens_out, i32, (cache.batch,)),
-        w if weights_out is None else _plain("weights_out", weights_out, f32, slots),
-        p if pos_out is None else _plain("pos_out", pos_out, i32, slots),
-        *_space(workspace), _raw(weights, stream))
-    if r:
-        _fail("bcq_kv_evict", r)
+    _call("bcq_kv_evict", dev, stream, cache._ref, keep, recent, w, p,
+          cache.lens.data_ptr() if lens_out is None
+          else _plain("lens_out", lens_out, i32, (cache.batch,), dev),
+          w if weights_out is None else _plain("weights_out", weights_out, f32, slots, dev),
+          p if pos_out is None else _plain("pos_out", pos_out, i32, slots, dev),
+          *_space(workspace, dev))

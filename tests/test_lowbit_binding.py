@@ -154,3 +154,87 @@ def test_a_workspace_that_kernels_cannot_write_is_refused(machine, bad):
         with pytest.raises(ValueError, match="workspace"):
             call()
     assert not machine.calls
+
+
+# ----------------------------------------------------------------------------- devices
+
+
+def entries(index):
+    """Every call of the binding on tensors of one device, as functions of a stream."""
+    k, c = zeros(1, 1, 1, 64, index=index), cache(index)
+    return {
+        "bcq_int_quantize": lambda t: lowbit.bcq_int_quantize(zeros(3, 64, index=index), stream=t),
+        "bcq_kv_append": lambda t: lowbit.bcq_kv_append(c, k, k, stream=t),
+        "bcq_kv_read": lambda t: lowbit.bcq_kv_read(c, k, k, stream=t),
+        **with_workspace(index),
+    }
+
+
+ENTRIES = WITH_WORKSPACE + ("bcq_int_quantize", "bcq_kv_append", "bcq_kv_read")
+
+
+@pytest.mark.parametrize("index", [0, 1])
+@pytest.mark.parametrize("name", ENTRIES)
+def test_a_call_runs_with_its_tensors_device_current(machine, name, index):
+    """A launch goes to the current device, whose streams alone it may name."""
+    entries(index)[name](None)
+    (called, args, device), = machine.calls
+    assert (called, args[-1], device) == (name, 100 + index, index)
+    assert machine.device == 0 and all(d == index for _, d in machine.allocated)
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_a_stream_of_another_device_is_refused(machine, name):
+    with pytest.raises(ValueError, match="stream"):
+        entries(0)[name](Stream(7, 1))
+    assert not machine.calls and not machine.allocated
+
+
+def test_tensors_of_two_devices_are_refused(machine):
+    f32, i32, i8, u8 = torch.float32, torch.int32, torch.int8, torch.uint8
+    here, c = 0, cache(0)
+    # each call with its tensors, one of which at a time is on the other device
+    calls = [
+        (lowbit.bcq_int_quantize, dict(X=(3, 64)), {},
+         dict(codes=((3, 64), i8), scales=((3,), f32))),
+        (lowbit.bcq_int_gemm, {}, {},
+         dict(A=((3, 64), i8), a_scales=((3,), f32), W=((4, 64), i8), w_scales=((4,), f32),
+              Y=((3, 4), f32), bias=((4,), f32), workspace=((4096,), u8))),
+        (lowbit.bcq_int_linear, {}, {},
+         dict(X=((3, 64), f32), W=((4, 64), i8), w_scales=((4,), f32), Y=((3, 4), f32),
+              bias=((4,), f32), workspace=((4096,), u8))),
+        (lowbit.bcq_kv_append, {}, dict(cache=c),
+         dict(K=((1, 1, 1, 64), f32), V=((1, 1, 1, 64), f32), positions=((1, 1), i32),
+              weights=((1, 1, 32), f32), pos=((1, 1, 32), i32))),
+        (lowbit.bcq_kv_read, {}, dict(cache=c),
+         dict(K=((1, 1, 1, 64), f32), V=((1, 1, 1, 64), f32))),
+        (lowbit.bcq_kv_attend, {}, dict(cache=c),
+         dict(Q=((1, 1, 1, 64), f32), O=((1, 1, 1, 64), f32), weights=((1, 1, 32), f32),
+              workspace=((4096,), u8))),
+        (lowbit.bcq_kv_evict, {}, dict(cache=c, keep=5, recent=1),
+         dict(weights=((1, 1, 32), f32), pos=((1, 1, 32), i32), lens_out=((1,), i32),
+              weights_out=((1, 1, 32), f32), pos_out=((1, 1, 32), i32),
+              workspace=((4096,), u8))),
+    ]
+    for fn, plain, more, tensors in calls:
+        def arguments(away):
+            got = {n: zeros(*shape) for n, shape in plain.items()}
+            for n, (shape, dtype) in tensors.items():
+                got[n] = zeros(*shape, dtype=dtype, index=1 if n == away else here)
+            return dict(got, **more)
+
+        fn(**arguments(None))
+        machine.calls.clear()
+        for away in tensors:
+            with pytest.raises(ValueError, match="device"):
+                fn(**arguments(away))
+            assert not machine.calls, (fn.__name__, away)
+
+
+def test_a_cache_lies_on_one_device(machine):
+    shapes = [((2, 1, 16, 32), torch.uint8), ((2, 1, 4, 128), torch.uint8),
+              ((2, 1, 16, 4), torch.float16), ((1, 2), torch.int32), ((1,), torch.int32)]
+    for away in range(5):
+        with pytest.raises(ValueError, match="device"):
+            lowbit.KVCache(*(zeros(*shape, dtype=dtype, index=int(i == away))
+                             for i, (shape, dtype) in enumerate(shapes)))
