@@ -1,0 +1,58 @@
+"""Attention over the 4-bit cache on the GPU, held as a whole to what test_lowbit_accuracy says, in
+every way that a call can go."""
+
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import binary_coded_precision_amd as bcq  # noqa: E402
+from test_gpu_kv import device  # noqa: E402
+from test_lowbit_accuracy import definition, filled, outputs_hold, weights_hold  # noqa: E402
+
+DT = {"f16": (torch.float16, np.float16), "f32": (torch.float32, np.float32)}
+
+
+def say(*a):
+    print("[gpu-case]", *a, file=sys.stderr, flush=True)
+
+
+def check(c, q, scale, weights=True):
+    """A call's outputs, and its weights, against the definition."""
+    dev = device(c)
+    x = torch.from_numpy(q).cuda()
+    o = torch.empty_like(x)
+    w = torch.zeros((q.shape[0], c.H, dev.room), device="cuda") if weights else None
+    bcq.bcq_kv_attend(dev, x, o, scale=scale, weights=w)
+    ref, total = definition(c, q, float(np.float32(scale)))
+    assert outputs_hold(o.cpu().numpy(), ref)
+    if weights:
+        got = w.cpu().numpy()
+        assert weights_hold(got[..., :total.shape[2]], total)
+        assert not got[..., total.shape[2]:].any()
+
+
+# lens, n, heads, cached heads, D, page, pages of a sequence
+WAYS = [
+    ([120], 1, 8, 2, 128, 16, 8), ([700], 1, 8, 2, 128, 64, 11),  # up to 16 rows; split
+    ([700, 450], 2, 8, 2, 64, 64, 11), ([500], 1, 4, 1, 256, 64, 8),
+    ([110, 60], 5, 16, 4, 64, 16, 7), ([600], 5, 16, 4, 128, 32, 19),  # up to 32
+    ([250], 40, 4, 2, 128, 16, 16), ([200], 70, 4, 2, 64, 16, 13),  # more
+    ([200], 40, 4, 2, 256, 16, 13), ([1100], 40, 4, 2, 128, 128, 9),  # more, split
+    ([600], 17, 2, 2, 256, 32, 19),
+    ([300, 90, 0, 201], 50, 4, 2, 128, 64, 64),  # weights of 64 tokens a workgroup
+    ([300, 90, 0, 201], 70, 2, 2, 64, 64, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("lens,n,Hq,H,D,page,width", WAYS)
+def test_every_way(lens, n, Hq, H, D, page, width, dtype):
+    say("kv_attend accuracy", lens, n, Hq, H, D, page, dtype)
+    c = filled(lens, H, D, page, width, seed=n + D)
+    q = np.random.default_rng(3).normal(size=(len(lens), n, Hq, D)).astype(DT[dtype][1])
+    check(c, q, D ** -0.5)
+    check(c, q, D ** -0.5, weights=False)
