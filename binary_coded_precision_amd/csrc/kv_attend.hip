@@ -10,9 +10,9 @@
 //
 // so both products run on the codes themselves, which fp16 holds exactly, and
 // each token's four factors enter in fp32 afterwards.  A code c of K sits in an
-// operand as the fp16 with bit pattern c, the subnormal c * 2^-24 (the matrix
-// cores keep subnormal inputs), which takes one AND for two codes; codes masked
-// four bits up are 16c * 2^-24, and the queries of those channels carry 1/16.
+// operand as the fp16 with bit pattern 16c, the subnormal c * 2^-20 (the matrix
+// cores keep subnormal inputs), which takes a shift and an AND for two codes, and
+// the queries of fp16 calls are the other operand as they are.
 // Codes of V are centred: an average over many tokens is small against its
 // terms, and what the terms' roundings leave would otherwise be multiplied by
 // the 7.5 that the codes have in common, which the matrix cores' sums, cut off
@@ -61,7 +61,7 @@ constexpr float kNegInf = -INFINITY;
 // in fp16, and what fp32 calls keep of its rounding is above fp16's smallest.
 constexpr float kSlack = 6.f, kLift = 9.f;
 constexpr float kRaise = 15.f + kLift;  // 15: the exponent's bias in the V scale's bits
-constexpr float kCodeScale = 16777216.f;  // 2^24: a code's subnormal back to the code
+constexpr float kCodeScale = 1048576.f;  // 2^20: a code's subnormal back to the code
 
 struct Ws {
   float2 *ml;     // [splits][BH][R]: reference and sum of a row's exponentials
@@ -147,18 +147,20 @@ __device__ __forceinline__ half2v pair_of(uint32_t w) {
 }
 
 // Left operand of S^T for word w of a tile: channels 8w..8w+7 of the lane's
-// quarter in the order 0 4 1 5 2 6 3 7.  fp16 calls take the odd ones 16-fold,
-// as their bits lie.  fp32 calls shift all of them there: the matrix cores keep
-// fewer bits of a product with a smaller subnormal (measured: 1e-6 of a sum of
-// 32 products with c * 2^-24, 2e-8 with 16c * 2^-24).
-template <int D, bool F32>
+// quarter in the order 0 4 1 5 2 6 3 7.  All four bits up: with half of them as
+// the subnormals c * 2^-24, which saves two of these shifts (448 us instead of 456
+// at 2 x 2048 queries over 6001 tokens), their queries would have to carry 1/16,
+// which fp16 does not hold of queries below 2^-10, and the matrix cores keep
+// fewer bits of a product with a smaller subnormal (measured: 1e-6 of a sum of 32
+// products with c * 2^-24, 2e-8 with c * 2^-20).
+template <int D>
 __device__ __forceinline__ half8 k_frag(const Tiles<D> &t, int s, int w) {
-  const uint32_t x = t.k[s][w], x8 = x >> 8;
+  const uint32_t x = t.k[s][w];
   Frag f;
-  f.w[0] = F32 ? (x << 4) & 0x00f000f0u : x & 0x000f000fu;
+  f.w[0] = (x << 4) & 0x00f000f0u;
   f.w[1] = x & 0x00f000f0u;
-  f.w[2] = F32 ? (x >> 4) & 0x00f000f0u : x8 & 0x000f000fu;
-  f.w[3] = x8 & 0x00f000f0u;
+  f.w[2] = (x >> 4) & 0x00f000f0u;
+  f.w[3] = (x >> 8) & 0x00f000f0u;
   return f.h;
 }
 
@@ -173,15 +175,13 @@ __device__ __forceinline__ half2v centred(uint32_t w) {
 }
 constexpr float kCentreScale = 512.f;
 
-// Right operand of S^T: a query row's channels in k_frag's order, the odd ones
-// times `odd`.
-__device__ __forceinline__ half8 q_order(const float (&x)[8], float odd) {
+// Right operand of S^T: a query row's channels in k_frag's order.
+__device__ __forceinline__ half8 q_order(const float (&x)[8]) {
   half8 f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float by = (e & 1) ? odd : 1.f;
-    f[2 * e] = (_Float16)(x[e] * by);
-    f[2 * e + 1] = (_Float16)(x[e + 4] * by);
+    f[2 * e] = (_Float16)x[e];
+    f[2 * e + 1] = (_Float16)x[e + 4];
   }
   return f;
 }
@@ -201,7 +201,7 @@ template <int D, int CT, bool F32>
 struct Queries {
   half8 hi[CT][D / 32];
   half8 lo[F32 ? CT : 1][F32 ? D / 32 : 1];
-  float sum[CT];  // of the row, in the codes' unit 2^-24
+  float sum[CT];  // of the row, in the codes' unit 2^-20
   float row_scale[F32 ? CT : 1];
 };
 
@@ -277,7 +277,7 @@ __device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q,
       top = group_max(top);
       // the largest to 2^10..2^11: what the first fp16 leaves stays a normal one
       const int e2 = (top > 0.f && top < INFINITY) ? ilogbf(top) - 10 : 0;
-      Q.row_scale[ct] = ldexpf(1.f, e2 - 4);  // and k_frag's 16
+      Q.row_scale[ct] = ldexpf(1.f, e2);
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         float y[8], rest[8];
@@ -286,17 +286,17 @@ __device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q,
           y[e] = ldexpf(x[w][e], -e2);
           rest[e] = y[e] - (float)(_Float16)y[e];
         }
-        Q.hi[ct][w] = q_order(y, 1.f);
-        Q.lo[ct][w] = q_order(rest, 1.f);
+        Q.hi[ct][w] = q_order(y);
+        Q.lo[ct][w] = q_order(rest);
       }
     } else {
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) Q.hi[ct][w] = q_order(x[w], 0.0625f);
+      for (int w = 0; w < D / 32; ++w) Q.hi[ct][w] = q_order(x[w]);
     }
   }
 }
 
-// q . c (times 2^-24) of one 16-token tile for the lane's column and 4 tokens.
+// q . c (times 2^-20) of one 16-token tile for the lane's column and 4 tokens.
 template <int D, int CT, bool F32>
 __device__ __forceinline__ void tile_scores(float4v (&S)[CT], const Tiles<D> &t, int s,
                                             const Queries<D, CT, F32> &Q) {
@@ -309,7 +309,7 @@ __device__ __forceinline__ void tile_scores(float4v (&S)[CT], const Tiles<D> &t,
   }
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {
-    const half8 kf = k_frag<D, F32>(t, s, w);
+    const half8 kf = k_frag<D>(t, s, w);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       if constexpr (F32) {
@@ -333,7 +333,7 @@ struct Sums {
   float m[CT], l[CT], z[CT];
 };
 
-// A score before the softmax's scale, in the unit 2^-24: ks * (q . c) + kz * sum(q).
+// A score before the softmax's scale, in the unit 2^-20: ks * (q . c) + kz * sum(q).
 __device__ __forceinline__ float raw_score(float qc, float sum, uint32_t m) {
   const half2v f = pair_of(m);
   return fmaf(qc, (float)f[0], sum * (float)f[1]);

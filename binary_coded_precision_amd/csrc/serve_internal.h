@@ -74,7 +74,7 @@ struct AttendArgs {
   int n, G;          // queries of a sequence; query heads of a cached head
   bool q_wide;       // 8 channels of q can be read at once
   bool negate;       // the softmax's scale is negative
-  float unit;        // its size times log2(e), for scores in the unit 2^-24
+  float unit;        // its size times log2(e), for scores in the unit 2^-20
   float *weights;    // [B][H][room] or null
   void *ws;
 };

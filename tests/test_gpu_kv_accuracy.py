@@ -56,3 +56,29 @@ def test_every_way(lens, n, Hq, H, D, page, width, dtype):
     q = np.random.default_rng(3).normal(size=(len(lens), n, Hq, D)).astype(DT[dtype][1])
     check(c, q, D ** -0.5)
     check(c, q, D ** -0.5, weights=False)
+
+
+# lens, n, heads, cached heads, D, page, pages of a sequence: few rows, 32, more
+FEW = [([300], 1, 8, 2, 128, 64, 5), ([200], 7, 4, 1, 64, 16, 13), ([200], 40, 4, 2, 256, 16, 13)]
+
+
+@pytest.mark.parametrize("exponent", [-10, -13, -16])
+@pytest.mark.parametrize("lens,n,Hq,H,D,page,width", FEW)
+def test_small_queries(lens, n, Hq, H, D, page, width, exponent):
+    """fp16 queries near and below that type's smallest normal number, with a scale that makes up
+    for it."""
+    say("kv_attend small queries", lens, n, D, exponent)
+    c = filled(lens, H, D, page, width, seed=D)
+    q = np.random.default_rng(4).normal(size=(1, n, Hq, D)) * 2.0**exponent
+    check(c, q.astype(np.float16), D ** -0.5 * 2.0**-exponent)
+
+
+@pytest.mark.parametrize("lens,n,Hq,H,D,page,width", FEW)
+def test_queries_of_unlike_size(lens, n, Hq, H, D, page, width):
+    """Rows of a tile from 1e-5 to 6e4, each with loud and quiet channels."""
+    say("kv_attend unlike queries", lens, n, D)
+    c = filled(lens, H, D, page, width, seed=D, k_mean=0.1)
+    rng = np.random.default_rng(5)
+    rows = 2.0 ** rng.integers(-16, 13, (1, n, Hq, 1))
+    q = rng.normal(size=(1, n, Hq, D)) * rows * 2.0 ** rng.integers(-4, 1, D)
+    check(c, np.clip(q, -6e4, 6e4).astype(np.float16), 1e-3)
