@@ -42,6 +42,8 @@
 // one load; K needs one load of D/8 bytes a lane for 16 tokens.  No shared
 // memory is used in the loop and no barrier: the waves of a workgroup either
 // take turns over the tokens (few rows) or hold different rows.
+#include <float.h>
+
 #include <algorithm>
 
 #include "serve_internal.h"
@@ -61,7 +63,8 @@ constexpr float kNegInf = -INFINITY;
 // in fp16, and what fp32 calls keep of its rounding is above fp16's smallest.
 constexpr float kSlack = 6.f, kLift = 9.f;
 constexpr float kRaise = 15.f + kLift;  // 15: the exponent's bias in the V scale's bits
-constexpr float kCodeScale = 1048576.f;  // 2^20: a code's subnormal back to the code
+constexpr int kCodeLog = 20;
+constexpr float kCodeScale = 1 << kCodeLog;  // a code's subnormal back to the code
 
 struct Ws {
   float2 *ml;     // [splits][BH][R]: reference and sum of a row's exponentials
@@ -196,13 +199,13 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 // A lane's queries: its column's row of each of CT tiles, channels of its
-// quarter.  F32 holds each as two fp16 after dividing the row by `row_scale`.
+// quarter.  F32 holds each as two fp16 after taking a power of two out of the row.
 template <int D, int CT, bool F32>
 struct Queries {
   half8 hi[CT][D / 32];
   half8 lo[F32 ? CT : 1][F32 ? D / 32 : 1];
-  float sum[CT];  // of the row, in the codes' unit 2^-20
-  float row_scale[F32 ? CT : 1];
+  float sum[CT];              // of the row, in the scores' unit
+  float unit[F32 ? CT : 1];  // of a product with the codes, in the scores'
 };
 
 // The queries as they lie in memory: their loads can be under way long before
@@ -247,7 +250,7 @@ __device__ __forceinline__ void fetch_queries(RawQueries<D, CT, F32> &raw, const
 // Rows past R become zeros: a tile's spare columns.
 template <int D, int CT, bool F32>
 __device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q,
-                                             const RawQueries<D, CT, F32> &raw, bool negate,
+                                             const RawQueries<D, CT, F32> &raw, float unit,
                                              int row0, int R, int lane) {
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
@@ -263,40 +266,47 @@ __device__ __forceinline__ void load_queries(Queries<D, CT, F32> &Q,
           x[w][e] = (float)raw.h[ct][w][e];
         if (row >= R) x[w][e] = 0.f;
       }
-    float sum = 0.f, top = 0.f;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[w][e] = negate ? -x[w][e] : x[w][e];
-        sum += x[w][e];
-        top = fmaxf(top, fabsf(x[w][e]));
-      }
-    Q.sum[ct] = group_sum(sum) * (1.f / kCodeScale);
+    float sum = 0.f;
     if constexpr (F32) {
+      float top = 0.f;
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[w][e]));
       top = group_max(top);
       // the largest to 2^10..2^11: what the first fp16 leaves stays a normal one
       const int e2 = (top > 0.f && top < INFINITY) ? ilogbf(top) - 10 : 0;
-      Q.row_scale[ct] = ldexpf(1.f, e2);
+      // scores are finite up to here, and rows of this size have nothing but their
+      // largest left long before
+      constexpr float kMost = 0x1p100f;
+      Q.unit[ct] = fminf(fmaxf(ldexpf(unit, e2 + kCodeLog), -kMost), kMost);
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         float y[8], rest[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           y[e] = ldexpf(x[w][e], -e2);
+          sum += y[e];
           rest[e] = y[e] - (float)(_Float16)y[e];
         }
         Q.hi[ct][w] = q_order(y);
         Q.lo[ct][w] = q_order(rest);
       }
+      Q.sum[ct] = group_sum(sum) * (Q.unit[ct] * (1.f / kCodeScale));
     } else {
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) Q.hi[ct][w] = q_order(x[w]);
+      for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += x[w][e];
+        Q.hi[ct][w] = q_order(x[w]);
+      }
+      Q.sum[ct] = group_sum(sum) * unit;
     }
   }
 }
 
-// q . c (times 2^-20) of one 16-token tile for the lane's column and 4 tokens.
+// q . c of one 16-token tile for the lane's column and 4 tokens: times 2^-20, in
+// fp32 calls times the scores' unit.
 template <int D, int CT, bool F32>
 __device__ __forceinline__ void tile_scores(float4v (&S)[CT], const Tiles<D> &t, int s,
                                             const Queries<D, CT, F32> &Q) {
@@ -322,7 +332,7 @@ __device__ __forceinline__ void tile_scores(float4v (&S)[CT], const Tiles<D> &t,
   }
   if constexpr (F32) {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) S[ct] = (S[ct] + low[ct]) * Q.row_scale[ct];
+    for (int ct = 0; ct < CT; ++ct) S[ct] = (S[ct] + low[ct]) * Q.unit[ct];
   }
 }
 
@@ -333,15 +343,19 @@ struct Sums {
   float m[CT], l[CT], z[CT];
 };
 
-// A score before the softmax's scale, in the unit 2^-20: ks * (q . c) + kz * sum(q).
-__device__ __forceinline__ float raw_score(float qc, float sum, uint32_t m) {
+// A score in log2 units, rounded as such: ks * (q . c) + kz * sum(q).  What goes
+// into an exponential is then a difference of two such numbers, which is exact
+// where it matters; scale * score - reference in one multiply-add would leave
+// the rounding of a large reference in it.
+template <bool F32>
+__device__ __forceinline__ float score(float qc, float sum, uint32_t m, float code_unit) {
   const half2v f = pair_of(m);
-  return fmaf(qc, (float)f[0], sum * (float)f[1]);
+  return fmaf(qc, F32 ? (float)f[0] : (float)f[0] * code_unit, sum * (float)f[1]);
 }
 
 template <int D, int CT, bool F32>
-__device__ __forceinline__ void raw_scores(float4v (&S)[2][CT], const Tiles<D> &T,
-                                           const Queries<D, CT, F32> &Q) {
+__device__ __forceinline__ void scores(float4v (&S)[2][CT], const Tiles<D> &T,
+                                       const Queries<D, CT, F32> &Q, float code_unit) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     tile_scores<D, CT, F32>(S[s], T, s, Q);
@@ -349,7 +363,7 @@ __device__ __forceinline__ void raw_scores(float4v (&S)[2][CT], const Tiles<D> &
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
-        S[s][ct][i] = raw_score(S[s][ct][i], Q.sum[ct], T.m[s][2 * i]);
+        S[s][ct][i] = score<F32>(S[s][ct][i], Q.sum[ct], T.m[s][2 * i], code_unit);
   }
 }
 
@@ -400,8 +414,7 @@ __device__ __forceinline__ half2v cut(float a, float b) {
 // Plo.
 template <int D, int CT>
 __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Frag (&Plo)[CT],
-                                              const float4v (&S)[2][CT], const Tiles<D> &T,
-                                              float unit) {
+                                              const float4v (&S)[2][CT], const Tiles<D> &T) {
   // The tile's largest score and largest V scale together bound its terms; only
   // where that asks for it are the terms themselves looked at.
   ushort2v scales = pair16(T.m[0][1]);
@@ -416,11 +429,10 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Fra
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) high[ct] = fmaxf(high[ct], S[s][ct][i]);
     }
-  const float lv_most = rough_log2((uint32_t)scales[0]);
+  const float room = kRaise + kSlack - rough_log2((uint32_t)scales[0]);
   bool raise = false;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
-    raise |= fmaf(high[ct], unit, lv_most) > A.m[ct] + (kRaise + kSlack);
+  for (int ct = 0; ct < CT; ++ct) raise |= high[ct] - A.m[ct] > room;
   if (__any(raise)) {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
@@ -429,10 +441,17 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Fra
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          top = fmaxf(top, fmaf(S[s][ct][i], unit, rough_log2(T.m[s][2 * i + 1] & 0xffffu)));
+          top = fmaxf(top, S[s][ct][i] + rough_log2(T.m[s][2 * i + 1] & 0xffffu));
       // each row by its own scores, so that no row depends on its neighbours
       const float z = group_max(top);
-      const float m = z > A.m[ct] + (kRaise + kSlack) ? z - kRaise : A.m[ct];
+      float m = z > A.m[ct] + (kRaise + kSlack) ? z - kRaise : A.m[ct];
+      // Scores so large that such sums are rounded to units and more: the largest
+      // itself is the reference.  Terms are then at most the V scales.
+      const bool vast = fabsf(z) >= 0x1p22f && fabsf(z) < INFINITY;
+      if (__any(vast)) {
+        const float most = group_max(high[ct]);
+        m = vast ? fmaxf(A.m[ct], most) : m;
+      }
       const float f = m == A.m[ct] ? 1.f : exp2f(A.m[ct] - m);
       A.m[ct] = m;
       A.l[ct] *= f;
@@ -463,7 +482,7 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Fra
         float pv[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(S[s][ct][i + j], unit, -m[ct]));
+          const float p = __builtin_amdgcn_exp2f(S[s][ct][i + j] - m[ct]);
           A.l[ct] += p;
           A.z[ct] = fmaf(p, mid[j], A.z[ct]);
           pv[j] = p * (float)f[j][0];
@@ -606,7 +625,7 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
   }
 
   Queries<D, CT, F32> Q;
-  load_queries<D, CT, F32>(Q, raw, a.negate, row0, R, lane);
+  load_queries<D, CT, F32>(Q, raw, a.unit, row0, R, lane);
   Sums<D, CT> A;
   int last[CT];
   float *sc[CT];
@@ -631,7 +650,7 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
     const Where w = ahead;
     ahead = place_of(next + WT);
     float4v S[2][CT];
-    raw_scores<D, CT, F32>(S, T, Q);
+    scores<D, CT, F32>(S, T, Q, a.code_unit);
     load_k(T, a.c, w, lane);
     if (tile >= free_end) mask_scores<D, CT>(S, T, tile * 32 + 4 * g, last);
     if constexpr (STORE) {
@@ -640,11 +659,10 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
           if (sc[ct] != nullptr && tile * 32 + 16 * s < L)
-            *reinterpret_cast<float4v *>(sc[ct] + tile * 32 + 16 * s + 4 * g) =
-                S[s][ct] * a.unit;
+            *reinterpret_cast<float4v *>(sc[ct] + tile * 32 + 16 * s + 4 * g) = S[s][ct];
     }
     Frag P[CT], Plo[CT];
-    softmax_tiles<D, CT>(A, P, Plo, S, T, a.unit);
+    softmax_tiles<D, CT>(A, P, Plo, S, T);
     load_m(T, a.c, w, lane);
     add_values<D, CT, F32>(A, P, Plo, T);
     load_v(T, a.c, w, lane);
@@ -762,10 +780,11 @@ __device__ __forceinline__ RowJoin join_row(const Ws &ws, int splits, int64_t st
   for (int d = 1; d < 64; d <<= 1) j.l += __shfl_xor(j.l, d);
   return j;
 }
-// log2 of a row's sum of exponentials; +inf for a row that sees nothing, so
-// that its probabilities come out as zero.
-__device__ __forceinline__ float lse_of(const RowJoin &j) {
-  return j.m == kNegInf ? INFINITY : j.m + log2f(j.l);
+// What a row's probabilities are made of: 2^(score - m) * inv, all zero for a row
+// that sees nothing.  One number, m + log2(sum), would be rounded to a unit and
+// more where scores are large.
+__device__ __forceinline__ float2 normal_of(float m, float l) {
+  return m == kNegInf ? make_float2(INFINITY, 0.f) : make_float2(m, 1.f / l);
 }
 
 // Joins the splits (blocks [0, join)), a wave a row, and adds the rows'
@@ -815,7 +834,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
       store_out(a, at + c * 64 + lane, j.l == 0.f ? 0.f : o[c] / j.l, f32);
     return;
   }
-  __shared__ float lse[32];
+  __shared__ float2 normal[32];
   const int blk = blockIdx.x - join, bh = blk % BH;
   const int t = blk / BH * kSumTokens + threadIdx.x * 4;
   const int L = kv_len(a.c, bh / a.c.H);
@@ -837,8 +856,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
   float4v was = {0.f, 0.f, 0.f, 0.f};
   if (wide) was = *w;
   for (int r = wave; r < R; r += 4) {
-    const float e = lse_of(join_row(ws, splits, rows, (int64_t)bh * R + r, lane));
-    if (lane == 0) lse[r] = e;
+    const RowJoin j = join_row(ws, splits, rows, (int64_t)bh * R + r, lane);
+    if (lane == 0) normal[r] = normal_of(j.m, j.l);
   }
   __syncthreads();
   if (t >= L) return;
@@ -851,10 +870,12 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
       const int r = min(r0 + k, R - 1);
       // nothing is stored in tiles past the last token that a row sees
       const int seen = r0 + k < R ? L - a.n + r / a.G : -1;
-      const float e = lse[r];
+      const float2 e = normal[r];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sum[i] += t + i > seen ? 0.f : __builtin_amdgcn_exp2f(s[k][i] - e);
+      for (int i = 0; i < 4; ++i) {
+        const float with = fmaf(__builtin_amdgcn_exp2f(s[k][i] - e.x), e.y, sum[i]);
+        sum[i] = t + i > seen ? sum[i] : with;
+      }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) s[k] = next[k];
@@ -868,16 +889,16 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
 }
 
 // The same of one row in every lane, for the few splits that calls with many rows have.
-__device__ __forceinline__ float row_lse(const Ws &ws, int splits, int64_t stride, int64_t row) {
+__device__ __forceinline__ float2 row_normal(const Ws &ws, int splits, int64_t stride,
+                                             int64_t row) {
   float m = kNegInf;
   for (int s = 0; s < splits; ++s) m = fmaxf(m, ws.ml[s * stride + row].x);
-  if (m == kNegInf) return INFINITY;
   float l = 0.f;
-  for (int s = 0; s < splits; ++s) {
+  for (int s = 0; s < splits && m != kNegInf; ++s) {
     const float2 x = ws.ml[s * stride + row];
     l += x.y * exp2f(x.x - m);
   }
-  return m + log2f(l);
+  return normal_of(m, l);
 }
 
 // The weights of many rows: 32 TN tokens a workgroup, whose waves take turns over
@@ -925,14 +946,12 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
     if ((first + wave) * 16 < R) ask(first + wave);
     for (int rt = first + wave; rt * 16 < R; rt += 4) {
       Queries<D, 1, F32> Q;
-      load_queries<D, 1, F32>(Q, raw, a.negate, rt * 16, R, lane);
+      load_queries<D, 1, F32>(Q, raw, a.unit, rt * 16, R, lane);
       const int row = rt * 16 + (lane & 15);
       const int last = row < R ? L - a.n + row / a.G : -1;
-      float lse = INFINITY;
-      if (splits > 1)
-        lse = row_lse(ws, splits, rows, (int64_t)bh * R + min(row, R - 1));
-      else if (ml.x != kNegInf)
-        lse = ml.x + log2f(ml.y);
+      const float2 normal =
+          splits > 1 ? row_normal(ws, splits, rows, (int64_t)bh * R + min(row, R - 1))
+                     : normal_of(ml.x, ml.y);
       if ((rt + 4) * 16 < R) ask(rt + 4);
 #pragma unroll
       for (int k = 0; k < TN; ++k)
@@ -942,10 +961,10 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
           tile_scores<D, 1, F32>(S, T[k], s, Q);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x = raw_score(S[0][i], Q.sum[0], T[k].m[s][2 * i]);
-            sum[k][4 * s + i] += t + 32 * k + 16 * s + 4 * g + i > last
-                                     ? 0.f
-                                     : __builtin_amdgcn_exp2f(fmaf(x, a.unit, -lse));
+            const float x = score<F32>(S[0][i], Q.sum[0], T[k].m[s][2 * i], a.code_unit);
+            float &to = sum[k][4 * s + i];
+            const float with = fmaf(__builtin_amdgcn_exp2f(x - normal.x), normal.y, to);
+            to = t + 32 * k + 16 * s + 4 * g + i > last ? to : with;
           }
         }
     }
@@ -1065,11 +1084,13 @@ AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool w
 
 hipError_t launch_kv_attend(const AttendArgs &call, float scale, int D, bcq_dtype dt,
                             hipStream_t s) {
-  // The scores' unit is kept positive, so that -inf stays a hidden token's score
-  // whatever the scale: a negative one turns the queries, a zero becomes tiny.
+  // fp16 calls: up to 2^80 the scores of any queries and factors are finite, and a
+  // scale that large already leaves nothing of any but the largest, whose
+  // distance to the next is at least 2^-48 before it.  fp32 calls: see load_queries.
   AttendArgs a = call;
-  a.negate = scale < 0.f;
-  a.unit = fmaxf(fabsf(scale) * 1.44269504088896340736f * kCodeScale, 1e-30f);
+  if (dt == BCQ_F16) scale = fminf(fmaxf(scale, -0x1p80f), 0x1p80f);
+  a.unit = fminf(fmaxf(scale * 1.44269504088896340736f, -FLT_MAX), FLT_MAX);
+  a.code_unit = dt == BCQ_F16 ? a.unit * kCodeScale : 0.f;
   if (dt == BCQ_F32)
     return D == 64    ? launch_dim<64, true>(a, s)
            : D == 128 ? launch_dim<128, true>(a, s)

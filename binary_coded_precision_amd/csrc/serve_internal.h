@@ -73,12 +73,12 @@ struct AttendArgs {
   KvStrides qs, os;
   int n, G;          // queries of a sequence; query heads of a cached head
   bool q_wide;       // 8 channels of q can be read at once
-  bool negate;       // the softmax's scale is negative
-  float unit;        // its size times log2(e), for scores in the unit 2^-20
+  float unit;        // the softmax's scale times log2(e)
+  float code_unit;   // that times 2^20, in fp16 calls
   float *weights;    // [B][H][room] or null
   void *ws;
 };
-// negate and unit of `call` are filled in from the softmax's scale.
+// unit and code_unit of `call` are filled in from the softmax's scale.
 hipError_t launch_kv_attend(const AttendArgs &call, float scale, int D, bcq_dtype dt,
                             hipStream_t s);
 

@@ -82,3 +82,19 @@ def test_queries_of_unlike_size(lens, n, Hq, H, D, page, width):
     rows = 2.0 ** rng.integers(-16, 13, (1, n, Hq, 1))
     q = rng.normal(size=(1, n, Hq, D)) * rows * 2.0 ** rng.integers(-4, 1, D)
     check(c, np.clip(q, -6e4, 6e4).astype(np.float16), 1e-3)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, 3e7, -1e9, 1e31, -3e33, 3.4e38])
+@pytest.mark.parametrize("lens,n,Hq,H,D,page,width", FEW)
+def test_scales_up_to_the_largest(lens, n, Hq, H, D, page, width, scale, dtype):
+    """Scores of any size: all weight on a row's largest, wherever it lies, shared among equals."""
+    say("kv_attend scale", lens, n, D, scale, dtype)
+    c = filled(lens, H, D, page, width, seed=1)
+    k = np.random.default_rng(7).normal(size=D) * 4
+    for t in (2, 3, lens[0] // 2, lens[0] - n):  # the same key, with unlike values
+        for h in range(H):
+            c.put(0, h, t, k, np.linspace(-1, 1 + t, D))
+    q = np.random.default_rng(6).normal(size=(1, n, Hq, D))
+    q[0, :, ::2] = k * np.sign(scale)  # half of the heads look for it
+    check(c, q.astype(DT[dtype][1]), scale)
