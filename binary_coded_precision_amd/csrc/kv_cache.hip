@@ -4,7 +4,9 @@
 // A vector of D channels (one token's K or V of one cached head) is
 // zero + scale * code: zero = fp16(min), scale = fp16((max - min) * (1/15)),
 // code = rint((x - zero) / scale) held to 0..15, each step rounded to fp32 (the
-// constant too), so the codes are a function of the inputs alone.
+// constant too), so the codes are a function of the inputs alone.  Where either
+// factor is not finite the scale becomes NaN: an infinite zero beside a finite
+// scale would be read as an infinity, and as a score of -inf hide the token.
 #include <type_traits>
 
 #include "serve_internal.h"
@@ -117,8 +119,11 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k
   }
   float step = (hi - lo) * (1.f / 15.f);
   asm volatile("" : "+v"(step));  // rounded to fp32 first: one instruction could do both at once
-  const _Float16 zh = (_Float16)lo, sh = (_Float16)step;
-  const float zero = (float)zh, scale = (float)sh;
+  const _Float16 zh = (_Float16)lo, near_step = (_Float16)step;
+  const float zero = (float)zh;
+  const bool good = (float)near_step < INFINITY && fabsf(zero) < INFINITY;
+  const _Float16 sh = good ? near_step : (_Float16)NAN;
+  const float scale = (float)sh;
   uint32_t word = 0;
   // the quotient's neighbour y * (1 / scale) is less than 1e-5 off it and rounds
   // to the same integer unless it lies that close to a half

@@ -466,8 +466,10 @@ size_t bcq_int_workspace_bytes(int32_t T, int32_t M, int32_t K);
  * own, as an asymmetric group of head_dim channels:
  *     zero = fp16(min), scale = fp16((max - min) * (1/15)),
  *     code = rint((x - zero) / scale), held to 0..15   (0 where scale is 0)
- * evaluated in fp32 (the constant too).  A vector holding NaN, or values past fp16's range, gets
- * a scale or zero that is not finite, and what reads it NaN.
+ * evaluated in fp32 (the constant too).  A vector whose scale or zero is not
+ * finite so (it holds NaN or an infinity, or its smallest value or a fifteenth
+ * of its range is past fp16's) gets a scale of NaN and codes 0, and what reads
+ * it NaN.
  *
  * k_codes: [num_pages][heads][page_tokens][head_dim/2] bytes, channel 2i in the
  *   low half of byte i, channel 2i + 1 in the high half.

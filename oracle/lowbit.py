@@ -40,6 +40,7 @@ def quantize_vectors(x):
         lo, hi = x.min(axis=-1), x.max(axis=-1)
         scale = ((hi - lo) * np.float32(1 / 15)).astype(np.float16)
         zero = lo.astype(np.float16)
+        scale = np.where(np.isfinite(scale) & np.isfinite(zero), scale, np.float16(np.nan))
         s = scale.astype(np.float32)[..., None]
         q = np.where(s > 0, (x - zero.astype(np.float32)[..., None]) / np.where(s > 0, s, 1), 0)
         q = np.nan_to_num(np.rint(q), nan=0, posinf=15, neginf=0)

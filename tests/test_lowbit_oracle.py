@@ -86,3 +86,10 @@ def test_eviction_by_hand():
     assert lb.kept_slots(7, 5, 0, w, pos).tolist() == [0, 1, 2, 3, 4]  # ties: the lower slots
     assert lb.evict(3, 4, 1, w, pos).tolist() == [0, 1, 2]
     assert lb.kept_slots(3, 2, 0, np.array([np.nan, -np.inf, 0], np.float32), pos).tolist() == [1, 2]
+
+
+def test_vectors_past_the_range_have_no_scale():
+    x = np.array([[-7e4, -6.9e4], [7e4, 7e4], [1, np.inf], [-np.inf, 1], [np.nan, 1],
+                  [-6e4, 1e6], [0, 9e5]], np.float32)
+    c, s, _ = lb.quantize_vectors(x)
+    assert np.isnan(s[:6]).all() and not c[:6].any() and np.isfinite(s[6]) and c[6, 1] == 15
