@@ -372,11 +372,12 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
 }
 
 // Scores of the tokens past each row's last to -inf.  Factors of V that are not
-// finite would reach hidden rows as 0 * NaN: they become 0, and the score of a
-// row that does see them NaN, which makes its output NaN all the same.
+// finite would reach hidden rows as 0 * NaN: they become 0, and what a row that
+// does see them has summed of the zeros NaN, which its output is made with; its
+// probabilities do not depend on V.
 template <int D, int CT>
-__device__ __forceinline__ void mask_scores(float4v (&S)[2][CT], Tiles<D> &T, int t,
-                                            const int (&last)[CT]) {
+__device__ __forceinline__ void mask_scores(float4v (&S)[2][CT], Tiles<D> &T, Sums<D, CT> &A,
+                                            int t, const int (&last)[CT]) {
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -387,8 +388,9 @@ __device__ __forceinline__ void mask_scores(float4v (&S)[2][CT], Tiles<D> &T, in
       T.m[s][2 * i + 1] = bad ? 0u : T.m[s][2 * i + 1];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        const float x = bad ? NAN : S[s][ct][i];
-        S[s][ct][i] = t + 16 * s + i > last[ct] ? kNegInf : x;
+        const bool hidden = t + 16 * s + i > last[ct];
+        S[s][ct][i] = hidden ? kNegInf : S[s][ct][i];
+        A.z[ct] = bad && !hidden ? NAN : A.z[ct];
       }
     }
 }
@@ -546,9 +548,10 @@ __device__ __forceinline__ int64_t out_at(const AttendArgs &a, int b, int h, int
 }
 
 // Waves a SIMD that the registers are held to: with few rows the loads' latency
-// is what counts, and 4 waves (128 registers) hide more of it than 3.
+// is what counts, and 4 waves (128 registers) hide more of it than 3.  The others
+// need 113 to 256 registers, two waves at least.
 constexpr int least_waves(int D, int CT, int WT, bool f32) {
-  return WT == 4 && CT == 1 && D <= 128 && !f32 ? 4 : 1;
+  return WT == 4 && CT == 1 && D <= 128 && !f32 ? 4 : 2;
 }
 
 // The sequence of a given rank by length, the longest first (by index past 64
@@ -652,7 +655,7 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
     float4v S[2][CT];
     scores<D, CT, F32>(S, T, Q, a.code_unit);
     load_k(T, a.c, w, lane);
-    if (tile >= free_end) mask_scores<D, CT>(S, T, tile * 32 + 4 * g, last);
+    if (tile >= free_end) mask_scores<D, CT>(S, T, A, tile * 32 + 4 * g, last);
     if constexpr (STORE) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
