@@ -486,8 +486,9 @@ size_t bcq_int_workspace_bytes(int32_t T, int32_t M, int32_t K);
  *   0 .. max_pages * page_tokens).
  * k_codes, v_codes and scales 16-byte aligned, the others 4.  head_dim 64, 128
  * or 256, page_tokens a power of two from 16 to 256 (otherwise
- * BCQ_ERR_UNSUPPORTED); batch * heads below 2^22, max_pages * page_tokens up to
- * BCQ_KV_MAX_TOKENS and the product of the four up to 2^33.  The memory is the
+ * BCQ_ERR_UNSUPPORTED); batch up to 2^16, heads up to 2^12, batch * heads below
+ * 2^22, max_pages * page_tokens up to BCQ_KV_MAX_TOKENS and the product of the
+ * four up to 2^33.  The memory is the
  * caller's; the tables may change between calls, so calls may be captured in a
  * graph.
  *
@@ -517,7 +518,8 @@ typedef struct {
  * weights, pos: [batch][heads][max_pages * page_tokens], or NULL: for each slot
  *   written, weights becomes 0 and pos the token's position, positions[b][i]
  *   (or the slot where positions is NULL), as bcq_kv_evict reads them.
- * batch * heads * n * head_dim stays below 2^33.  n = 0 does nothing.
+ * n is at most BCQ_KV_MAX_TOKENS, batch * heads * (n + 6) * head_dim below
+ * 2^33 - 512.  n = 0 does nothing.
  * Validation and stream behaviour as in bcq_gemv.
  */
 bcq_status bcq_kv_append(const bcq_kv_cache *cache, int32_t n, const void *K, int64_t k_batch,
@@ -551,7 +553,8 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
  * Products run on the matrix cores with the codes as they are; softmax and
  * sums are in fp32.  Each token's probability times its V scale is held in 22
  * bits relative to the largest of its row; fp32 calls hold the queries in 22
- * bits too.  batch * n * q_heads is at most 2^29.
+ * bits too.  n is at most BCQ_KV_MAX_TOKENS, q_heads at most 2^16, n * q_heads at
+ * most 2^28 and batch * n * q_heads at most 2^29.
  * workspace: bcq_kv_workspace_bytes(cache, n, q_heads, weights != NULL) bytes,
  *   16-byte aligned, of no account before and after; calls that may run at the
  *   same time need separate ones.  NULL when that is 0.
