@@ -762,6 +762,11 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
 }
 
 constexpr int kMaxSplits = 64;  // one a lane where they are joined
+// Tokens whose terms a wave sums in one go: what the matrix cores cut off at each
+// addition grows with them.  Values that are all alike, the worst for it, come out
+// 1.74e-4 of their norm off fp16 (1.72e-4 is its rounding) over 2^17 tokens and
+// 4.5e-4 over 2^20.
+constexpr int64_t kMostTokens = 1 << 17;
 
 // Splits of one row over the lanes of a wave: each split's factor against the
 // row's largest reference (0 for lanes past them), the sum of exponentials, and
@@ -1064,13 +1069,14 @@ AttendPlan attend_plan(int B, int H, int D, int room, int n, int q_heads, bool w
   p.row_blocks = (int)((R + block - 1) / block);
   const int64_t units = BH * p.row_blocks;
   // Enough workgroups for 256 compute units, none with less than one step of
-  // 32 tokens a wave.
+  // 32 tokens a wave, and no wave with more than kMostTokens unless there are more
+  // rows than one launch can join.
   const int64_t want = p.wt == 4 ? 1024 : 512, least = p.wt == 4 ? 128 : 256;
-  int64_t splits = (want + units - 1) / units;
   const int64_t most = (room + least - 1) / least;
-  splits = splits > most ? most : splits;
-  splits = splits > kMaxSplits ? kMaxSplits : splits;
-  p.splits = (int)(splits < 1 ? 1 : splits);
+  const int64_t few = (room + kMostTokens * p.wt - 1) / (kMostTokens * p.wt);
+  int64_t splits = std::max(std::min((want + units - 1) / units, most), few);
+  splits = std::min<int64_t>({splits, kMaxSplits, kMaxGroups / units});
+  p.splits = BH * R > 4 * (int64_t)kMaxGroups ? 1 : (int)splits;
   p.scores = weights && p.wt != 1;
   const size_t rows = (size_t)(BH * R);
   size_t at = 0;

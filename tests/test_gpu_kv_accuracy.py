@@ -98,3 +98,24 @@ def test_scales_up_to_the_largest(lens, n, Hq, H, D, page, width, scale, dtype):
     q = np.random.default_rng(6).normal(size=(1, n, Hq, D))
     q[0, :, ::2] = k * np.sign(scale)  # half of the heads look for it
     check(c, q.astype(DT[dtype][1]), scale)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_a_million_tokens_in_one_pass(dtype):
+    """Values all alike, whose sums grow all the way, for as many rows as leave one workgroup a
+    whole sequence: the output is the value."""
+    L, n, H, G, D = 1 << 20, 2048 if dtype == "f16" else 512, 8, 4, 128
+    say("kv_attend of a million tokens", n, dtype)
+    c = bcq.KVCache.new(1, L, H, D, page_tokens=256)
+    c.lens.fill_(L)
+    k = torch.randn((1, L, 1, D), device="cuda", dtype=torch.float16) * 0.5
+    v = torch.randn((1, 1, 1, D), device="cuda")
+    bcq.bcq_kv_append(c, k.expand(1, L, H, D), v.half().expand(1, L, H, D))
+    value = torch.empty((1, 1, H, D), device="cuda")
+    bcq.bcq_kv_read(c, torch.empty_like(value), value)
+    q = torch.randn((1, n, H * G, D), device="cuda").to(DT[dtype][0])
+    o = torch.empty_like(q)
+    bcq.bcq_kv_attend(c, q, o)
+    ref = value[0, 0, 0].cpu().numpy().astype(np.float64)
+    got = o[0, ::67, ::3].reshape(-1, D).cpu().numpy()
+    assert outputs_hold(got, np.broadcast_to(ref, got.shape))
