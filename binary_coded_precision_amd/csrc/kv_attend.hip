@@ -67,7 +67,8 @@ constexpr int kCodeLog = 20;
 constexpr float kCodeScale = 1 << kCodeLog;  // a code's subnormal back to the code
 
 struct Ws {
-  float2 *ml;     // [splits][BH][R]: reference and sum of a row's exponentials
+  float2 *ml;     // [splits][BH][R]: reference and sum of a row's exponentials; joined,
+                  // [BH][R], for the weights of many rows
   float *o;       // [splits][BH][R][D]: outputs before the division
   float *scores;  // [BH][R][room], log2 units, -inf where masked
 };
@@ -764,9 +765,9 @@ __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void att
 constexpr int kMaxSplits = 64;  // one a lane where they are joined
 // Tokens whose terms a wave sums in one go: what the matrix cores cut off at each
 // addition grows with them.  Values that are all alike, the worst for it, come out
-// 1.74e-4 of their norm off fp16 (1.72e-4 is its rounding) over 2^17 tokens and
-// 4.5e-4 over 2^20.
-constexpr int64_t kMostTokens = 1 << 17;
+// 1.00 times as far off as fp16's rounding takes them over 2^16 tokens, up to
+// 1.26 times over 2^17 and 2.6 over 2^20.
+constexpr int64_t kMostTokens = 1 << 16;
 
 // Splits of one row over the lanes of a wave: each split's factor against the
 // row's largest reference (0 for lanes past them), the sum of exponentials, and
@@ -840,6 +841,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       store_out(a, at + c * 64 + lane, j.l == 0.f ? 0.f : o[c] / j.l, f32);
+    // where no block of this launch reads it, for the weights formed afterwards
+    if (lane == 0 && ws.scores == nullptr) ws.ml[row] = make_float2(j.m, j.l);
     return;
   }
   __shared__ float2 normal[32];
@@ -896,19 +899,6 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
   }
 }
 
-// The same of one row in every lane, for the few splits that calls with many rows have.
-__device__ __forceinline__ float2 row_normal(const Ws &ws, int splits, int64_t stride,
-                                             int64_t row) {
-  float m = kNegInf;
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, ws.ml[s * stride + row].x);
-  float l = 0.f;
-  for (int s = 0; s < splits && m != kNegInf; ++s) {
-    const float2 x = ws.ml[s * stride + row];
-    l += x.y * exp2f(x.x - m);
-  }
-  return normal_of(m, l);
-}
-
 // The weights of many rows: 32 TN tokens a workgroup, whose waves take turns over
 // the row tiles and form the scores again from the K codes; the sums stay in
 // registers, so no atomics and a fixed order.  A row tile's queries and factors
@@ -919,12 +909,11 @@ __device__ __forceinline__ float2 row_normal(const Ws &ws, int splits, int64_t s
 // the tile ahead, 788 with TN = 1 as well.  At 4 x 1000 over 1000 (64 channels)
 // 50 us against 72; TN = 4 took 93.
 template <int D, bool F32, int TN>
-__global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, Ws ws) {
+__global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, Ws ws) {
   __shared__ float part[4][32 * TN];
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int BH = a.c.B * a.c.H, R = a.n * a.G;
-  const int64_t rows = (int64_t)BH * R;
   const int bh = blockIdx.x % BH, stride = gridDim.x / BH * 32 * TN;
   const int b = bh / a.c.H, h = bh % a.c.H;
   const int L = kv_len(a.c, b);
@@ -957,9 +946,7 @@ __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, int splits, 
       load_queries<D, 1, F32>(Q, raw, a.unit, rt * 16, R, lane);
       const int row = rt * 16 + (lane & 15);
       const int last = row < R ? L - a.n + row / a.G : -1;
-      const float2 normal =
-          splits > 1 ? row_normal(ws, splits, rows, (int64_t)bh * R + min(row, R - 1))
-                     : normal_of(ml.x, ml.y);
+      const float2 normal = normal_of(ml.x, ml.y);
       if ((rt + 4) * 16 < R) ask(rt + 4);
 #pragma unroll
       for (int k = 0; k < TN; ++k)
@@ -1047,9 +1034,9 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s) {
     const int wide = (room + 32 * kTiles - 1) / (32 * kTiles), narrow = (room + 31) / 32;
     if ((int64_t)BH * wide >= 512)
       weights_kernel<D, F32, kTiles>
-          <<<BH * std::min(wide, kMaxGroups / BH), 256, 0, s>>>(a, p.splits, ws);
+          <<<BH * std::min(wide, kMaxGroups / BH), 256, 0, s>>>(a, ws);
     else
-      weights_kernel<D, F32, 1><<<BH * narrow, 256, 0, s>>>(a, p.splits, ws);
+      weights_kernel<D, F32, 1><<<BH * narrow, 256, 0, s>>>(a, ws);
     e = hipGetLastError();
   }
   return e;

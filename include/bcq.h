@@ -553,9 +553,10 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
  * Products run on the matrix cores with the codes as they are; softmax and
  * sums are in fp32.  Each token's probability times its V scale is held in 22
  * bits relative to the largest of its row; fp32 calls hold the queries in 22
- * bits too.  fp16 calls leave the sums of up to 2^17 tokens to the matrix cores,
- * which cut off about 1e-7 of a sum at each addition of 32 terms.  n is at most BCQ_KV_MAX_TOKENS, q_heads at most 2^16, n * q_heads at
- * most 2^28 and batch * n * q_heads at most 2^29.
+ * bits too.  fp16 calls leave the sums of up to 2^16 tokens to the matrix cores,
+ * which cut off about 1e-7 of a sum at each addition of 32 terms.
+ * n is at most BCQ_KV_MAX_TOKENS, q_heads at most 2^16, n * q_heads at most 2^28
+ * and batch * n * q_heads at most 2^29.
  * workspace: bcq_kv_workspace_bytes(cache, n, q_heads, weights != NULL) bytes,
  *   16-byte aligned, of no account before and after; calls that may run at the
  *   same time need separate ones.  NULL when that is 0.

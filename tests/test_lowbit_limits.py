@@ -46,7 +46,7 @@ def test_queries(lib, n, q_heads, batch, want):
 
 
 def test_long_sequences_are_shared_out(lib):
-    """No wave sums more than 2^17 tokens in one go, whatever the number of rows, up to what a
+    """No wave sums more than 2^16 tokens in one go, whatever the number of rows, up to what a
     launch can join; the workspace holds the parts."""
     def size(room, n, heads=1, q_heads=16, batch=1):
         c = cache(batch=batch, heads=heads, max_pages=room // 64)
@@ -54,12 +54,12 @@ def test_long_sequences_are_shared_out(lib):
 
     part = 8 + 128 * 4  # of a row: a reference, a sum, outputs
     for n in (1 << 13, 1 << 20):  # enough workgroups without
-        assert size(1 << 17, n) == 0
-        for room, splits in ((1 << 18, 2), (3 << 17, 3), (1 << 24, 64)):
+        assert size(1 << 16, n) == 0
+        for room, splits in ((1 << 17, 2), (3 << 16, 3), (1 << 22, 64), (1 << 24, 64)):
             assert splits * n * 16 * part <= size(room, n) < splits * n * 16 * part + 512
     # a decode step's four waves share a workgroup's tokens
-    assert size(1 << 19, 1, heads=1 << 10, q_heads=1 << 10, batch=16) == 0
-    got = size(1 << 20, 1, heads=1 << 10, q_heads=1 << 10, batch=8)
+    assert size(1 << 18, 1, heads=1 << 10, q_heads=1 << 10, batch=16) == 0
+    got = size(1 << 19, 1, heads=1 << 10, q_heads=1 << 10, batch=8)
     assert 2 * (1 << 13) * part <= got < 2 * (1 << 13) * part + 512
     # more rows than a launch joins
     assert size(1 << 18, 1 << 24) == 0
