@@ -53,6 +53,8 @@ class AttentionBlock:
     def prompt(self, x):
         """x [batch][n][hidden] of an empty cache -> the block's output of the same shape."""
         n = x.shape[1]
+        if n > self.cache.room:
+            raise ValueError("a prompt of %d tokens, room for %d" % (n, self.cache.room))
         x = x.reshape(-1, self.hidden)
         qkv = x.new_empty((len(x), self.codes[0][0].shape[0]))
         bcq.bcq_int_linear(x, *self.codes[0], qkv)
