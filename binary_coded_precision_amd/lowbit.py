@@ -71,28 +71,26 @@ def _pad16(n: int) -> int:
     return (n + 15) // 16 * 16
 
 
-def _device(name: str, t, stream) -> int:
-    """The device of a call: t's, which a given stream has to belong to."""
+def _device(name: str, t) -> int:
+    """The device of a call, that of its tensor t."""
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    dev = t.get_device()
-    if stream is not None and stream.device_index != dev:
-        raise ValueError("stream must belong to the device of %s" % name)
-    return dev
+    return t.get_device()
 
 
-def _call(name: str, dev: int, stream, *args) -> None:
-    """Calls an entry point on `stream` (None: the device's current one).  Launches go to the
-    current device, so that has to be the tensors'."""
-    fn = getattr(_lib, name)
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status:
-        _fail(name, status)
+def _raw(dev: int, stream) -> int:
+    """The raw stream a call goes to: the given one, or the current one of its device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError("stream must belong to device %d, as the call's tensors do" % dev)
+    return stream.cuda_stream
+
+
+def _there(dev: int, call, *args):
+    """A call made again with its tensors' device current: launches go to that one."""
+    with torch.cuda.device(dev):
+        return call(*args)
 
 
 def _empty(shape, dtype, device, stream):
@@ -173,8 +171,11 @@ def bcq_int_quantize(X, codes=None, scales=None, stream=None):
 
     Returns ``(codes, scales)``: int8 [rows][K] (a view of rows padded to 16 bytes with zeros)
     and fp32 [rows], allocated on ``stream`` unless given."""
-    _lib or _bind()
-    dev = _device("X", X, stream)
+    lib = _lib or _bind()
+    dev = _device("X", X)
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_int_quantize, X, codes, scales, stream)
+    raw = _raw(dev, stream)
     dt = _float("X", X, dev)
     rows, K = X.shape
     ldx = _rows("X", X, rows, K, K)
@@ -186,38 +187,44 @@ def bcq_int_quantize(X, codes=None, scales=None, stream=None):
         raise ValueError("codes must be an int8 device tensor on X's device")
     if rows == 1:
         ldx = _pad16(ldx)  # a single row has no next one to be aligned with
-    _call("bcq_int_quantize", dev, stream, X.data_ptr(), dt, rows, K, ldx, codes.data_ptr(),
-          _rows("codes", codes, rows, K, _pad16(K)),
-          _plain("scales", scales, torch.float32, (rows,), dev))
+    r = lib.bcq_int_quantize(X.data_ptr(), dt, rows, K, ldx, codes.data_ptr(),
+                             _rows("codes", codes, rows, K, _pad16(K)),
+                             _plain("scales", scales, torch.float32, (rows,), dev), raw)
+    if r:
+        _fail("bcq_int_quantize", r)
     return codes, scales
 
 
-def _product(W, w_scales, Y, T: int, bias, stream):
-    """Checks what the two products share; (device, M, K, ldw, ldy, dtype, scales', bias'
-    address)."""
-    dev = _device("W", W, stream)
+def _product(W, w_scales, Y, T: int, bias, dev: int):
+    """Checks what the two products share; (M, K, ldw, ldy, dtype, scales', bias' address)."""
     if W.dtype is not torch.int8:
         raise ValueError("W must be an int8 device tensor")
     M, K = W.shape
-    return (dev, M, K, _rows("W", W, M, K, _pad16(K)), _rows("Y", Y, T, M, M),
-            _float("Y", Y, dev), _plain("w_scales", w_scales, torch.float32, (M,), dev),
+    return (M, K, _rows("W", W, M, K, _pad16(K)), _rows("Y", Y, T, M, M), _float("Y", Y, dev),
+            _plain("w_scales", w_scales, torch.float32, (M,), dev),
             0 if bias is None else _plain("bias", bias, Y.dtype, (M,), dev))
 
 
 def bcq_int_gemm(A, a_scales, W, w_scales, Y, bias=None, workspace=None, stream=None) -> None:
     """``Y[t][m] = (A[t] . W[m]) * (a_scales[t] * w_scales[m]) + bias[m]`` from 8-bit codes as
     :func:`bcq_int_quantize` returns them.  ``workspace`` as in :func:`bcq_int_linear`."""
-    _lib or _bind()
+    lib = _lib or _bind()
+    dev = _device("W", W)
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_int_gemm, A, a_scales, W, w_scales, Y, bias, workspace, stream)
+    raw = _raw(dev, stream)
     T = A.shape[0]
-    dev, M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias, stream)
+    M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias, dev)
     if A.dtype is not torch.int8 or A.get_device() != dev:
         raise ValueError("A must be an int8 device tensor on W's device")
     lda = _rows("A", A, T, K, _pad16(K))
     if workspace is None:
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
-    _call("bcq_int_gemm", dev, stream, A.data_ptr(),
-          _plain("a_scales", a_scales, torch.float32, (T,), dev), T, lda, W.data_ptr(), sp, M, K,
-          ldw, bp, Y.data_ptr(), ldy, dt, *_space(workspace, dev))
+    r = lib.bcq_int_gemm(A.data_ptr(), _plain("a_scales", a_scales, torch.float32, (T,), dev), T,
+                         lda, W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(), ldy, dt,
+                         *_space(workspace, dev), raw)
+    if r:
+        _fail("bcq_int_gemm", r)
 
 
 def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) -> None:
@@ -226,9 +233,13 @@ def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) ->
 
     ``workspace=None`` allocates one through torch; :func:`new_int_workspace` keeps that out of
     a hot loop."""
-    _lib or _bind()
+    lib = _lib or _bind()
+    dev = _device("W", W)
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_int_linear, X, W, w_scales, Y, bias, workspace, stream)
+    raw = _raw(dev, stream)
     T = X.shape[0]
-    dev, M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias, stream)
+    M, K, ldw, ldy, dt, sp, bp = _product(W, w_scales, Y, T, bias, dev)
     if X.dtype is not Y.dtype or X.get_device() != dev:
         raise ValueError("X and Y must be device tensors of one dtype on W's device")
     ldx = _rows("X", X, T, K, K)
@@ -236,8 +247,10 @@ def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) ->
         ldx = _pad16(ldx)  # a single row has no next one to be aligned with
     if workspace is None:
         workspace = _workspace(bcq_int_workspace_bytes(T, M, K), W.device, stream)
-    _call("bcq_int_linear", dev, stream, X.data_ptr(), T, ldx, W.data_ptr(), sp, M, K, ldw, bp,
-          Y.data_ptr(), ldy, dt, *_space(workspace, dev))
+    r = lib.bcq_int_linear(X.data_ptr(), T, ldx, W.data_ptr(), sp, M, K, ldw, bp, Y.data_ptr(),
+                           ldy, dt, *_space(workspace, dev), raw)
+    if r:
+        _fail("bcq_int_linear", r)
 
 
 # ----------------------------------------------------------------------------- 4-bit cache
@@ -258,7 +271,7 @@ class KVCache:
         P, H, page, half = k_codes.shape
         D = 2 * half
         B, width = page_table.shape
-        dev = self._dev = _device("k_codes", k_codes, None)
+        dev = self._dev = _device("k_codes", k_codes)
         self._st = _KVCache(
             B, H, D, page, P, width,
             _plain("k_codes", k_codes, torch.uint8, (P, H, page, half), dev),
@@ -296,9 +309,8 @@ class KVCache:
         return self._ref
 
 
-def _pair(K, V, cache: KVCache, stream):
+def _pair(K, V, cache: KVCache):
     """(n, dtype, strides of K, of V) of vectors [batch][n][heads][D] with contiguous channels."""
-    _device("cache", cache.k_codes, stream)
     shape = K.shape
     if len(shape) != 4 or shape[0] != cache.batch or shape[2] != cache.heads or \
             shape[3] != cache.head_dim or V.shape != shape:
@@ -319,21 +331,30 @@ def bcq_kv_append(cache: KVCache, K, V, positions=None, weights=None, pos=None,
     """Quantizes ``K`` and ``V`` [batch][n][heads][D] into the last n slots of every sequence;
     ``cache.lens`` must count them already.  ``weights`` and ``pos`` [batch][heads][room] get 0
     and the token's position (``positions`` int32 [batch][n], or its slot)."""
-    n, dt, ks, vs = _pair(K, V, cache, stream)
     dev, slots = cache._dev, cache._slots
-    _call("bcq_kv_append", dev, stream, cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2],
-          V.data_ptr(), vs[0], vs[1], vs[2], dt,
-          0 if positions is None else _plain("positions", positions, torch.int32,
-                                             (cache.batch, n), dev),
-          0 if weights is None else _plain("weights", weights, torch.float32, slots, dev),
-          0 if pos is None else _plain("pos", pos, torch.int32, slots, dev))
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_append, cache, K, V, positions, weights, pos, stream)
+    n, dt, ks, vs = _pair(K, V, cache)
+    r = _lib.bcq_kv_append(
+        cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2], V.data_ptr(), vs[0], vs[1], vs[2], dt,
+        0 if positions is None else _plain("positions", positions, torch.int32,
+                                           (cache.batch, n), dev),
+        0 if weights is None else _plain("weights", weights, torch.float32, slots, dev),
+        0 if pos is None else _plain("pos", pos, torch.int32, slots, dev), _raw(dev, stream))
+    if r:
+        _fail("bcq_kv_append", r)
 
 
 def bcq_kv_read(cache: KVCache, K, V, stream=None) -> None:
     """Writes the values of the last n cached tokens to ``K`` and ``V`` [batch][n][heads][D]."""
-    n, dt, ks, vs = _pair(K, V, cache, stream)
-    _call("bcq_kv_read", cache._dev, stream, cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2],
-          V.data_ptr(), vs[0], vs[1], vs[2], dt)
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_read, cache, K, V, stream)
+    n, dt, ks, vs = _pair(K, V, cache)
+    r = _lib.bcq_kv_read(cache._ref, n, K.data_ptr(), ks[0], ks[1], ks[2], V.data_ptr(), vs[0],
+                         vs[1], vs[2], dt, _raw(dev, stream))
+    if r:
+        _fail("bcq_kv_read", r)
 
 
 def bcq_kv_workspace_bytes(cache: KVCache, n: int, q_heads: int, with_weights: bool) -> int:
@@ -352,7 +373,10 @@ def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None
     """Causal attention of ``Q`` [batch][n][q_heads][D], the queries of the last n cached tokens,
     over the cache into ``O`` (same shape); ``scale`` defaults to 1/sqrt(D).  ``weights``
     [batch][heads][room] float32 accumulates each cached token's probabilities."""
-    dev = _device("cache", cache.k_codes, stream)
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_attend, cache, Q, O, scale, weights, workspace, stream)
+    raw = _raw(dev, stream)
     dt = _float("Q", Q, dev)
     shape = Q.shape
     if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim or \
@@ -366,10 +390,13 @@ def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None
     if workspace is None:
         workspace = _workspace(bcq_kv_workspace_bytes(cache, n, heads, weights is not None),
                                Q.device, stream)
-    _call("bcq_kv_attend", dev, stream, cache._ref, Q.data_ptr(), n, heads, qs[0], qs[1], qs[2],
-          O.data_ptr(), os[0], os[1], os[2], dt, shape[3] ** -0.5 if scale is None else scale,
-          0 if weights is None else _plain("weights", weights, torch.float32, cache._slots, dev),
-          *_space(workspace, dev))
+    r = _lib.bcq_kv_attend(
+        cache._ref, Q.data_ptr(), n, heads, qs[0], qs[1], qs[2], O.data_ptr(), os[0], os[1],
+        os[2], dt, shape[3] ** -0.5 if scale is None else scale,
+        0 if weights is None else _plain("weights", weights, torch.float32, cache._slots, dev),
+        *_space(workspace, dev), raw)
+    if r:
+        _fail("bcq_kv_attend", r)
 
 
 def bcq_kv_evict_workspace_bytes(cache: KVCache, keep: int) -> int:
@@ -387,13 +414,20 @@ def bcq_kv_evict(cache: KVCache, keep: int, recent: int, weights, pos, lens_out=
     the largest ``weights``.  In place unless ``lens_out``, ``weights_out``, ``pos_out`` are
     given (the codes always are: see ``include/bcq.h``)."""
     slots, f32, i32 = cache._slots, torch.float32, torch.int32
-    dev = _device("cache", cache.k_codes, stream)
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_evict, cache, keep, recent, weights, pos, lens_out, weights_out,
+                      pos_out, workspace, stream)
+    raw = _raw(dev, stream)
     w, p = _plain("weights", weights, f32, slots, dev), _plain("pos", pos, i32, slots, dev)
     if workspace is None:
         workspace = _workspace(bcq_kv_evict_workspace_bytes(cache, keep), weights.device, stream)
-    _call("bcq_kv_evict", dev, stream, cache._ref, keep, recent, w, p,
-          cache.lens.data_ptr() if lens_out is None
-          else _plain("lens_out", lens_out, i32, (cache.batch,), dev),
-          w if weights_out is None else _plain("weights_out", weights_out, f32, slots, dev),
-          p if pos_out is None else _plain("pos_out", pos_out, i32, slots, dev),
-          *_space(workspace, dev))
+    r = _lib.bcq_kv_evict(
+        cache._ref, keep, recent, w, p,
+        cache.lens.data_ptr() if lens_out is None
+        else _plain("lens_out", lens_out, i32, (cache.batch,), dev),
+        w if weights_out is None else _plain("weights_out", weights_out, f32, slots, dev),
+        p if pos_out is None else _plain("pos_out", pos_out, i32, slots, dev),
+        *_space(workspace, dev), raw)
+    if r:
+        _fail("bcq_kv_evict", r)
