@@ -84,8 +84,8 @@ __device__ __forceinline__ float row_scale(float top) {
 // One workgroup a row.  Rows of up to 2048 N elements are held in registers
 // between the two passes, longer ones (N = 0) read again from the caches.  Bound
 // by memory and, at a row a workgroup, by the two passes' latency: 4096 rows of
-// 4096 fp16 take 16.3 us (50 MB, 3.1 TB/s); a wave a row, four rows a workgroup,
-// took 20.6 us.
+// 4096 fp16 take 16.7 us (50 MB, 3.0 TB/s), in fp32 25.6 us (84 MB, 3.3 TB/s); a
+// wave a row, four rows a workgroup, took 20.6 us in fp16.
 template <typename T, int N>
 __global__ __launch_bounds__(256) void quantize_kernel(const T *X, int K, int ldx, int8_t *codes,
                                                        int ldc, float *scales) {
@@ -190,8 +190,8 @@ __device__ __forceinline__ void store_sums(int32_t *token, int m, int M, int4v s
 // before the tokens are quantized.  Every workgroup quantizes the tokens for
 // itself: T * K is at most kFusedElements, a fraction of a microsecond, where a
 // launch of its own costs several.  One token by 4096 x 4096 (16.8 MB) takes
-// 8.4 us, the launch and the chain from a token's first load to its codes among
-// them; reading the weights alone would take 3.3 us.
+// 8.3 us, the chain from a token's first load to its codes among them; reading the
+// weights alone would take 3.3 us.
 //
 // Up to two tokens: each one more costs every workgroup 1.7 us of loads, extremes
 // and codes one after the other, and the two launches of the way below cost 3 (us
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256) void fused_kernel(IntProduct p, const T *X, in
 // directly, so that a compute unit's two or three workgroups have 30 KB of W and
 // more in flight; a step waits for its own loads only (loads return in order),
 // and loads past the end of K come from 16 bytes of zeros, which keeps the count
-// the same.  37 tokens by 14336 x 4096 (58.7 MB) take 14.2 us, 4.1 TB/s.
+// the same.  37 tokens by 14336 x 4096 (58.7 MB) take 15.0 us, 3.9 TB/s.
 constexpr int kRing = 5;
 
 template <typename T, int BT, bool SPLIT>
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(256) void few_kernel(IntProduct p, int tiles_m, int
 // registers by then, so it runs while the next step's first are read and the
 // stage just finished is asked for again, a whole step ahead of its use.
 //
-// 4096 tokens by 14336 x 4096: the 768 whole tiles of 256 take 253 us, 1.63
+// 4096 tokens by 14336 x 4096: the 768 whole tiles of 256 take 232 us, 1.78
 // POP/s; at K = 14336 they reach 2.1 POP/s, the rate of a library's largest
 // product, so what a shorter K loses is the start and the 128 KB of outputs at
 // the end of each tile, which nothing overlaps (one workgroup fills a compute
@@ -632,7 +632,7 @@ __global__ __launch_bounds__(256) void join_kernel(IntProduct p, int slices,
 // Where the tiles of 256 fill the compute units a few times and at most half of
 // them once more, those last tiles go in halves (256 x 128, 0.88 of the rate) to
 // all of them, in a launch of their own: 4096 tokens by 14336 x 4096, 896 tiles,
-// take 293 us so and 309 in whole tiles.
+// take 252 us so and 269 in whole tiles (without the quantizer, one set of inputs).
 constexpr int kFewTokens = 64;
 constexpr int kUnits = 256;
 struct TilePlan {

@@ -22,8 +22,8 @@
 // relative to the row's largest (below), and for fp32 calls the queries are too
 // (after a power of two for each row).  One fp16 for p_t * vs_t would add an error
 // as large as an fp16 output's own rounding: 3.0e-4 to 3.4e-4 of the output's norm
-// in all, against 2.1e-4 (and 2048 queries over 6001 and 4501 tokens would take
-// 396 us, not 451).  As the matrix cores cut off
+// in all, against 2.1e-4 (and 2 x 2048 queries over 6001 and 4501 tokens would
+// take 400 us, not 460).  As the matrix cores cut off
 // what they add to a running sum, 1e-7 of it each time and always downwards
 // (measured), fp32 calls start every product at zero and sum in ordinary fp32.
 //
@@ -152,8 +152,8 @@ __device__ __forceinline__ half2v pair_of(uint32_t w) {
 
 // Left operand of S^T for word w of a tile: channels 8w..8w+7 of the lane's
 // quarter in the order 0 4 1 5 2 6 3 7.  All four bits up: with half of them as
-// the subnormals c * 2^-24, which saves two of these shifts (448 us instead of 456
-// at 2 x 2048 queries over 6001 tokens), their queries would have to carry 1/16,
+// the subnormals c * 2^-24, which saves two of these shifts (448 against 456 us
+// at 2 x 2048 queries over 6001 and 4501 tokens), their queries would have to carry 1/16,
 // which fp16 does not hold of queries below 2^-10, and the matrix cores keep
 // fewer bits of a product with a smaller subnormal (measured: 1e-6 of a sum of 32
 // products with c * 2^-24, 2e-8 with c * 2^-20).
@@ -581,9 +581,9 @@ __device__ __forceinline__ int by_length(const KvView &c, int rank, int lane) {
 //
 // With few rows it is bound by the cache's bytes: 32 sequences of 4224 to 8192
 // tokens, 8 cached heads of 128 channels (216 MB, and 25 MB of scores written)
-// take 57 us, 4.2 TB/s.
+// take 58 us, 4.2 TB/s.
 // With many rows by the instructions that unpack codes and form probabilities:
-// 2 x 2048 queries of 32 heads over 6001 and 4501 tokens take 451 us;
+// 2 x 2048 queries of 32 heads over 6001 and 4501 tokens take 460 us;
 // their products alone would take 247 us at a library's fp16 rate.
 template <int D, int CT, int WT, int WR, bool F32, bool STORE>
 __global__ __launch_bounds__(64 * WT * WR, least_waves(D, CT, WT, F32)) void attend_kernel(
@@ -799,7 +799,7 @@ __device__ __forceinline__ float2 normal_of(float m, float l) {
 // Joins the splits (blocks [0, join)), a wave a row, and adds the rows'
 // probabilities to the weights from the stored scores (the other blocks, 1024
 // tokens each).  Bound by reading both: 1024 rows and the weights of 8 heads of
-// 32 sequences of 4224 to 8192 tokens (38 MB and the outputs) take 8.7 us.
+// 32 sequences of 4224 to 8192 tokens (38 MB and the outputs) take 9.1 us.
 constexpr int kSumTokens = 1024;
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int join, bool f32,
@@ -905,9 +905,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, int splits, int
 // cost more to bring in than 32 tokens' scores: they are asked for a tile ahead,
 // and TN is 2, what the registers hold as unpacked codes up to 128 channels, where
 // that leaves two workgroups for each compute unit.  2 x 2048 queries of 32 heads
-// over 6001 and 4501 tokens (128 channels, 8 cached heads): 371 us; 577 without
-// the tile ahead, 788 with TN = 1 as well.  At 4 x 1000 over 1000 (64 channels)
-// 50 us against 72; TN = 4 took 93.
+// over 6001 and 4501 tokens (128 channels, 8 cached heads): 413 us; 462 without
+// the tile ahead, 589 with TN = 1.  At 4 x 1000 over 1000 (64 channels) 27 us, 28
+// with TN = 1 or 4.
 template <int D, bool F32, int TN>
 __global__ __launch_bounds__(256) void weights_kernel(AttendArgs a, Ws ws) {
   __shared__ float part[4][32 * TN];

@@ -91,10 +91,9 @@ __host__ __forceinline__ uint32_t vectors_of(const KvView &c, int n) {
 }
 
 // Bound by the bytes of the vectors read; every lane converts what it loads,
-// the extremes meet in D/4 lanes and no shared memory is needed.  4099 and
-// 3075 tokens of 8 heads of 64 channels in fp32, slices of one projection (29 MB
-// read, 4.6 MB written): 16.9 us, 2.0 TB/s; four vectors a group of lanes took
-// 20.4 us.
+// the extremes meet in D/4 lanes and no shared memory is needed.  2 x 4099 tokens
+// of 8 heads of 64 channels in fp32, slices of one projection (33.6 MB read, 4.6
+// MB written): 17.0 us, 2.2 TB/s; four vectors a group of lanes took 20.4 us.
 template <int D, typename T, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k, KvStrides ks,
                                                      const T *v, KvStrides vs,
@@ -251,7 +250,11 @@ constexpr int kRank = 256;   // slots left that are ranked against each other
 // costs 5 (rows of 2049: one 8.7 us against 12.2, two 11.4 against 11.5, four 15.7
 // against 11.3; rows of 30001: two 18.5 against 19.7, four 25.4 against 21.5).
 constexpr int kFew = 2;
-constexpr int kInPlace = 64;  // moves that the selecting workgroup makes itself
+// Moves that the selecting workgroup makes itself, by the most there can be (rows
+// of up to 2048 + that many, 32 and 256 rows, in a graph): with 64 10 and 11.6 us
+// against 11.4 and 14.0 for a launch of their own, with 128 12.1 and 14.5 against 11.6
+// and 16.8, with 256 15.4 and 20.3 against 12.0 and 21.2.
+constexpr int kInPlace = 64;
 
 struct EvictArgs {
   KvView c;
@@ -347,7 +350,7 @@ __device__ __forceinline__ T *nth(B *base, uint32_t i) {
 // One compute unit's vector ALUs bound it (an operation on each of 32768 slots
 // takes 0.2 us), hence few operations a slot and pass: slots past L have a rank
 // below all others instead of a test, and blocks without a match are left after
-// one ballot.  32 rows of 20480 to 32768 slots, 4096 kept: 24 us, then 21 us of moves.
+// one ballot.  32 rows of 32768 slots, 4096 kept: 24 us, then 21 us of moves.
 //
 // D > 0: there are at most kInPlace moves, made here; lens_out is then not lens.
 template <int Q, bool ONCE, int D>

@@ -546,7 +546,8 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
  * that sees nothing gets zeros.  What a query does not see has no influence,
  * whatever its scales hold.
  * Q, O: strides as in bcq_kv_append, q_heads heads (a multiple of heads), dtype
- *   BCQ_F16 or BCQ_F32.  scale: finite; 1/sqrt(head_dim) is usual.
+ *   BCQ_F16 or BCQ_F32; O does not overlap Q, which is read again after O is
+ *   written where weights are.  scale: finite; 1/sqrt(head_dim) is usual.
  * weights: NULL, or [batch][heads][max_pages * page_tokens] fp32, to whose slots
  *   the probabilities are added, summed over the queries and over the query
  *   heads of a cached head, in a fixed order.
