@@ -148,6 +148,18 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream=None):
+    """A tensor that a call on ``stream`` (None: the current one) may write at once: memory of
+    that stream's, as another's may still be in use there by what was queued before it was
+    freed."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dtype_code(t) -> int:
     import torch
 
@@ -282,7 +294,7 @@ def bcq_lowrank_correct(u_signs, v_signs, alpha, x, y, z=None, stream=None) -> N
     if not (x.dtype == y.dtype == alpha.dtype):
         raise ValueError("alpha, x and y must share one dtype")
     if z is None:
-        z = torch.empty(R, dtype=torch.float32, device=y.device)
+        z = _empty(R, torch.float32, y.device, stream)
     _need_vec("u_signs", u_signs, M * ((R + 31) // 32))
     _need_vec("v_signs", v_signs, R * (K // 32))
     _need_vec("z", z, R)
@@ -302,7 +314,7 @@ def bcq_gemv_lowrank(store: "Store", p: int, x, u_signs, v_signs, lr_alpha, y, z
 
     R, M, K = lr_alpha.numel(), store.M, store.K
     if z is None:
-        z = torch.empty(R, dtype=torch.float32, device=y.device)
+        z = _empty(R, torch.float32, y.device, stream)
     _need_vec("x", x, K)
     _need_vec("y", y, M)
     _need_vec("u_signs", u_signs, M * ((R + 31) // 32))
@@ -344,10 +356,10 @@ def bcq_quantize(W, P: int, p_low: int = 2, iters: int = 20, out_dtype=None, str
     if K % BCQ_GROUP or not (1 <= p_low <= P <= BCQ_MAX_PLANES):
         raise ValueError("K must be a multiple of 128 and 1 <= p_low <= P <= 4")
     G = K // BCQ_GROUP
-    signs = torch.empty((P, M, K // 32), dtype=torch.int32, device=W.device)
+    signs = _empty((P, M, K // 32), torch.int32, W.device, stream)
     n_alpha = sum(p for p in range(p_low, P + 1)) * M * G
-    abuf = torch.empty(n_alpha, dtype=out_dtype, device=W.device)
-    zbuf = torch.empty((P - p_low + 1, M, G), dtype=out_dtype, device=W.device)
+    abuf = _empty(n_alpha, out_dtype, W.device, stream)
+    zbuf = _empty((P - p_low + 1, M, G), out_dtype, W.device, stream)
     _check("bcq_quantize",
            load().bcq_quantize(_ptr(W), _dtype_code(W), M, K, W.stride(0), P, p_low, iters,
                                _ptr(signs), _ptr(abuf), _ptr(zbuf), codes[out_dtype],
@@ -364,17 +376,17 @@ def bcq_workspace_bytes(store: "Store", b: int) -> int:
     return int(load().bcq_workspace_bytes(store.ref(), b))
 
 
-def new_workspace(store: "Store", b: int):
+def new_workspace(store: "Store", b: int, stream=None):
     """A device workspace of ``bcq_workspace_bytes(store, b)`` bytes for
-    ``bcq_gemm_skinny`` or ``bcq_gemv_mixed_p`` at batch b, or None when the
-    call needs none.  Its
+    ``bcq_gemm_skinny`` or ``bcq_gemv_mixed_p`` at batch b on ``stream`` (None:
+    the current one), or None when the call needs none.  Its
     contents need no initialisation; calls that may overlap need separate ones."""
     import torch
 
     n = bcq_workspace_bytes(store, b)
     if n == 0:
         return None
-    return torch.empty((n + 3) // 4, dtype=torch.int32, device=store.bits.device)
+    return _empty((n + 3) // 4, torch.int32, store.bits.device, stream)
 
 
 def bcq_gemm_skinny(store: "Store", p: int, X, Y, workspace=None, stream=None) -> None:
@@ -387,7 +399,7 @@ def bcq_gemm_skinny(store: "Store", p: int, X, Y, workspace=None, stream=None) -
     _need_mat("Y", Y, b, store.M)
     _check_store_tensors(store, [p])
     if workspace is None:
-        workspace = new_workspace(store, b)
+        workspace = new_workspace(store, b, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("bcq_gemm_skinny",
            load().bcq_gemm_skinny(store.ref(), p, _ptr(X), b, X.stride(0), _dtype_code(X),
@@ -420,7 +432,7 @@ def bcq_gemv_mixed_p(store: "Store", p_host: Sequence[int], X, Y, workspace=None
     _check_store_tensors(store, p_host)
     ps = (ctypes.c_int32 * b)(*[int(v) for v in p_host])
     if workspace is None:
-        workspace = new_workspace(store, b)
+        workspace = new_workspace(store, b, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("bcq_gemv_mixed_p",
            load().bcq_gemv_mixed_p(store.ref(), ps, _ptr(X), b, X.stride(0), _dtype_code(X),
@@ -472,8 +484,7 @@ class Store:
 
         P, M, W = signs.shape
         K = W * 32
-        packed = torch.empty(bcq_packed_bytes(P, M, K) // 4, dtype=torch.int32,
-                             device=signs.device)
+        packed = _empty(bcq_packed_bytes(P, M, K) // 4, torch.int32, signs.device, stream)
         bcq_pack_planes(signs, P, M, K, packed, stream)
         return cls(M, K, P, packed, alpha, zero)
 
