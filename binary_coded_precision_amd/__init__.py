@@ -23,7 +23,7 @@ from . import lowbit
 from .lowbit import (BCQ_KV_MAX_TOKENS, KVCache, bcq_int_gemm, bcq_int_linear, bcq_int_quantize,
                      bcq_int_workspace_bytes, bcq_kv_append, bcq_kv_attend, bcq_kv_evict,
                      bcq_kv_evict_workspace_bytes, bcq_kv_read, bcq_kv_workspace_bytes,
-                     new_int_workspace, new_kv_evict_workspace, new_kv_workspace)
+                     bcq_rms_norm, new_int_workspace, new_kv_evict_workspace, new_kv_workspace)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbcq.so")

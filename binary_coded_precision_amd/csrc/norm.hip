@@ -1,0 +1,188 @@
+// norm.hip -- residual addition, root-mean-square norm and rounding to 8 bits of
+// each token's row (bcq_rms_norm).
+//
+//   h = round(x + residual)                      to the call's type
+//   y = (h * inv) * gamma,  inv = 1 / sqrt(mean(h^2) + eps)
+//   scale = max|y| * (1/127),  code = rint(y / scale)
+//
+// The squares are summed in fp64: they stay in range for every fp32 row, and
+// inv, rounded once to fp32, does not depend on the order of the sum but for a
+// sum within 1e-15 of a rounding's border.  The two products and the quotient
+// are single operations in fp32, so that codes are a function of h and inv.
+#include "row_codes.h"
+#include "serve_internal.h"
+
+namespace bcq {
+namespace {
+
+template <typename T>
+__device__ __forceinline__ void store_row8(T *row, const float (&x)[8], int k, int K) {
+  if (k + 8 <= K) {
+    if constexpr (sizeof(T) == 2) {
+      typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+      half8 h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = (_Float16)x[e];
+      *reinterpret_cast<half8 *>(row + k) = h;
+    } else {
+      reinterpret_cast<float4 *>(row + k)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4 *>(row + k)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < K) row[k + e] = (T)x[e];
+  }
+}
+
+// Sum and maximum over a workgroup's threads.  `red` is not in use by what was
+// called before with another one.
+template <int THREADS>
+__device__ __forceinline__ double sum_all(double x, double *red) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+  if constexpr (THREADS == 64) return x;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) x += red[w];
+  return x;
+}
+template <int THREADS>
+__device__ __forceinline__ float max_all(float x, float *red) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x = nan_max(x, __shfl_xor(x, d));
+  if constexpr (THREADS == 64) return x;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) x = nan_max(x, red[w]);
+  return x;
+}
+
+// h of 8 elements from where they are found: the sum, rounded to T.
+template <typename T>
+__device__ __forceinline__ void load_h(float (&h)[8], const T *x, const T *r, int k, int K) {
+  load_row8(h, x, k, K);
+  if (r != nullptr) {
+    float b[8];
+    load_row8(b, r, k, K);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = (float)(T)(h[e] + b[e]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_row8(float (&y)[8], const float (&h)[8], float inv,
+                                           const T *gamma, int k, int K) {
+  float g[8];
+  load_row8(g, gamma, k, K);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = (h[e] * inv) * g[e];
+}
+
+// One workgroup a row.  Rows of up to 8 N THREADS elements are held in registers;
+// longer ones (N = 0) are read again from the caches for each of three passes.
+template <typename T, int N, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
+  __shared__ double red_sum[THREADS / 64];
+  __shared__ float red_max[THREADS / 64];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, K = a.K;
+  const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+  const T *r = a.residual == nullptr ? nullptr
+                                     : static_cast<const T *>(a.residual) + row * a.ldr;
+  const T *gamma = static_cast<const T *>(a.gamma);
+  T *h_out = a.h == nullptr ? nullptr : static_cast<T *>(a.h) + row * a.ldh;
+  T *y_out = a.y == nullptr ? nullptr : static_cast<T *>(a.y) + row * a.ldy;
+  int8_t *codes = a.codes == nullptr ? nullptr : a.codes + row * a.ldc;
+  constexpr int STEP = THREADS * 8;
+  const int end = codes == nullptr ? K : (K + 15) / 16 * 16;  // codes' zeros behind K
+
+  float v[N > 0 ? N : 1][8];
+  double sum = 0.;
+  if constexpr (N > 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) load_h<T>(v[n], x, r, n * STEP + tid * 8, K);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fma((double)v[n][e], (double)v[n][e], sum);
+    if (h_out != nullptr)
+#pragma unroll
+      for (int n = 0; n < N; ++n) store_row8<T>(h_out, v[n], n * STEP + tid * 8, K);
+  } else {
+    for (int k = tid * 8; k < K; k += STEP) {
+      load_h<T>(v[0], x, r, k, K);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fma((double)v[0][e], (double)v[0][e], sum);
+      if (h_out != nullptr) store_row8<T>(h_out, v[0], k, K);
+    }
+    // x or the residual may be what h has just replaced; a thread reads what it wrote
+    if (h_out != nullptr) x = h_out, r = nullptr;
+  }
+  sum = sum_all<THREADS>(sum, red_sum);
+  const float inv = (float)(1. / sqrt(sum / K + a.eps));
+  if (y_out == nullptr && codes == nullptr) return;
+
+  float top = 0.f;
+  if constexpr (N > 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int k = n * STEP + tid * 8;
+      scale_row8<T>(v[n], v[n], inv, gamma, k, K);
+      if (y_out != nullptr) store_row8<T>(y_out, v[n], k, K);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = nan_max(top, k + e < K ? fabsf(v[n][e]) : 0.f);
+    }
+  } else {
+    for (int k = tid * 8; k < K; k += STEP) {
+      load_h<T>(v[0], x, r, k, K);
+      scale_row8<T>(v[0], v[0], inv, gamma, k, K);
+      if (y_out != nullptr) store_row8<T>(y_out, v[0], k, K);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = nan_max(top, k + e < K ? fabsf(v[0][e]) : 0.f);
+    }
+  }
+  if (codes == nullptr) return;
+  const float s = row_scale(max_all<THREADS>(top, red_max));
+  if (tid == 0) a.scales[row] = s;
+  if constexpr (N > 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int k = n * STEP + tid * 8;
+      if (k < end) *reinterpret_cast<uint2 *>(codes + k) = codes8(v[n], s);
+    }
+  } else {
+    for (int k = tid * 8; k < end; k += STEP) {
+      load_h<T>(v[0], x, r, k, K);
+      scale_row8<T>(v[0], v[0], inv, gamma, k, K);
+      *reinterpret_cast<uint2 *>(codes + k) = codes8(v[0], s);
+    }
+  }
+}
+
+template <typename T>
+hipError_t norm_type(const NormArgs &a, int T_, hipStream_t s) {
+  if (a.K <= 2048)
+    norm_kernel<T, 1, 256><<<T_, 256, 0, s>>>(a);
+  else if (a.K <= 4096)
+    norm_kernel<T, 2, 256><<<T_, 256, 0, s>>>(a);
+  else if (a.K <= 8192)
+    norm_kernel<T, 4, 256><<<T_, 256, 0, s>>>(a);
+  else if (a.K <= 16384)
+    norm_kernel<T, 2, 1024><<<T_, 1024, 0, s>>>(a);
+  else
+    norm_kernel<T, 0, 1024><<<T_, 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs &a, int T, bcq_dtype dt, hipStream_t s) {
+  return dt == BCQ_F16 ? norm_type<_Float16>(a, T, s) : norm_type<float>(a, T, s);
+}
+
+}  // namespace bcq

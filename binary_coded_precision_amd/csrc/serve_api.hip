@@ -1,6 +1,7 @@
 // serve_api.hip -- the C entry points of the low-bit serving operators:
 // argument validation on the host, then the launches.  As in bcq_api.hip every
 // check runs before any HIP call.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -177,6 +178,33 @@ bcq_status bcq_int_linear(const void *X, int32_t T, int32_t ldx, const int8_t *W
   if (e != hipSuccess) return BCQ_ERR_HIP;
   return hip_status(
       bcq::launch_int_gemm(p, dtype, reinterpret_cast<int32_t *>(ws + w.partial), stream));
+}
+
+bcq_status bcq_rms_norm(const void *X, int32_t ldx, const void *residual, int32_t ldr,
+                        const void *gamma, double eps, int32_t T, int32_t K, bcq_dtype dtype,
+                        void *H, int32_t ldh, void *Y, int32_t ldy, int8_t *codes, int32_t ldc,
+                        float *scales, hipStream_t stream) {
+  if (!dtype_valid(dtype) || T < 0 || T > kMaxRows || K < 1 || K > kMaxIntK)
+    return BCQ_ERR_INVALID_ARG;
+  if (!(eps >= FLT_MIN && eps <= FLT_MAX)) return BCQ_ERR_INVALID_ARG;
+  if (T == 0) return BCQ_OK;
+  if (H == nullptr && Y == nullptr && codes == nullptr) return BCQ_ERR_INVALID_ARG;
+  if ((codes == nullptr) != (scales == nullptr)) return BCQ_ERR_INVALID_ARG;
+  if (X == nullptr || gamma == nullptr || ldx < K) return BCQ_ERR_INVALID_ARG;
+  if (residual != nullptr && ldr < K) return BCQ_ERR_INVALID_ARG;
+  if ((H != nullptr && ldh < K) || (Y != nullptr && ldy < K) ||
+      (codes != nullptr && ldc < bcq::pad16(K)))
+    return BCQ_ERR_INVALID_ARG;
+  const size_t es = dtype_size(dtype);
+  const auto rows_aligned = [&](const void *p, int32_t ld) {
+    return p == nullptr || (aligned(p, 16) && (size_t)ld * es % 16 == 0);
+  };
+  if (!rows_aligned(X, ldx) || !rows_aligned(residual, ldr) || !rows_aligned(H, ldh) ||
+      !rows_aligned(Y, ldy) || !aligned(gamma, 16) || !aligned(codes, 16) ||
+      (codes != nullptr && ldc % 16 != 0) || !aligned(scales, 4))
+    return BCQ_ERR_ALIGNMENT;
+  const bcq::NormArgs a{X, residual, gamma, H, Y, codes, scales, ldx, ldr, ldh, ldy, ldc, K, eps};
+  return hip_status(bcq::launch_rms_norm(a, T, dtype, stream));
 }
 
 bcq_status bcq_kv_append(const bcq_kv_cache *cache, int32_t n, const void *K, int64_t k_batch,

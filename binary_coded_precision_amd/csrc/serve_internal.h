@@ -1,5 +1,6 @@
 // serve_internal.h -- declarations shared by the low-bit serving operators
-// (8-bit integer products and the 4-bit key/value cache).  Not part of the ABI.
+// (8-bit integer products, the norm before them, and the 4-bit key/value cache).
+// Not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -31,6 +32,19 @@ hipError_t launch_int_gemm(const IntProduct &p, bcq_dtype dt, int32_t *partial, 
 bool int_fused_ok(int T, int K);
 hipError_t launch_int_fused(const IntProduct &p, const void *X, int ldx, bcq_dtype dt,
                             hipStream_t s);
+
+// ---- norm (norm.hip) ----
+
+struct NormArgs {
+  const void *x, *residual, *gamma;  // residual may be null
+  void *h, *y;                       // may be null; h may be x or residual
+  int8_t *codes;                     // may be null, then scales is too
+  float *scales;
+  int64_t ldx, ldr, ldh, ldy, ldc;
+  int K;
+  double eps;
+};
+hipError_t launch_rms_norm(const NormArgs &a, int T, bcq_dtype dt, hipStream_t s);
 
 // ---- 4-bit key/value cache ----
 

@@ -1,5 +1,5 @@
-"""Binding of the low-bit serving operators: the 8-bit integer linear layer and the 4-bit
-key/value cache (append, read, attend, evict).  Names and semantics are those of
+"""Binding of the low-bit serving operators: the 8-bit integer linear layer, the norm before it
+and the 4-bit key/value cache (append, read, attend, evict).  Names and semantics are those of
 ``include/bcq.h``; the package exports everything here.
 
 The tensors of a call, and its ``stream`` if one is given, belong to one device, which need not be
@@ -32,6 +32,8 @@ SIGNATURES = {
     "bcq_int_linear": (_int, [_vp, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _int,
                               _vp, _sz, _vp]),
     "bcq_int_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "bcq_rms_norm": (_int, [_vp, _i32, _vp, _i32, _vp, ctypes.c_double, _i32, _i32, _int, _vp,
+                            _i32, _vp, _i32, _vp, _i32, _vp, _vp]),
     "bcq_kv_append": (_int, [_kc, _i32, _vp, *_strides, _vp, *_strides, _int, _vp, _vp, _vp,
                              _vp]),
     "bcq_kv_read": (_int, [_kc, _i32, _vp, *_strides, _vp, *_strides, _int, _vp]),
@@ -251,6 +253,46 @@ def bcq_int_linear(X, W, w_scales, Y, bias=None, workspace=None, stream=None) ->
                            ldy, dt, *_space(workspace, dev), raw)
     if r:
         _fail("bcq_int_linear", r)
+
+
+# ----------------------------------------------------------------------------- norm
+
+
+def bcq_rms_norm(X, gamma, eps, residual=None, H=None, Y=None, codes=None, scales=None,
+                 stream=None) -> None:
+    """``h = X + residual`` into ``H``, its root-mean-square norm times ``gamma`` [K] into ``Y``,
+    and that rounded to 8 bits into ``codes`` (int8 [T][K], rows padded to 16 bytes) and
+    ``scales`` (float32 [T]), as :func:`bcq_int_gemm` reads them; what is None is left out.
+    All rows are [T][K] of ``X``'s dtype, 16-byte aligned; ``H`` may be ``X`` or ``residual``."""
+    lib = _lib or _bind()
+    dev = _device("X", X)
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_rms_norm, X, gamma, eps, residual, H, Y, codes, scales, stream)
+    raw = _raw(dev, stream)
+    dt = _float("X", X, dev)
+    T, K = X.shape
+
+    def rows(name, t):
+        if t is None:
+            return 0, 0
+        if t.dtype is not X.dtype or t.get_device() != dev:
+            raise ValueError("%s must be a device tensor of X's dtype on its device" % name)
+        ld = _rows(name, t, T, K, K)
+        # a single row has no next one to be aligned with
+        return t.data_ptr(), _pad16(ld) if T == 1 else ld
+
+    cp = ldc = sp = 0
+    if codes is not None:
+        if codes.dtype is not torch.int8 or codes.get_device() != dev:
+            raise ValueError("codes must be an int8 device tensor on X's device")
+        cp, ldc = codes.data_ptr(), _rows("codes", codes, T, K, _pad16(K))
+    if scales is not None:
+        sp = _plain("scales", scales, torch.float32, (T,), dev)
+    r = lib.bcq_rms_norm(*rows("X", X), *rows("residual", residual),
+                         _plain("gamma", gamma, X.dtype, (K,), dev), eps, T, K, dt,
+                         *rows("H", H), *rows("Y", Y), cp, ldc, sp, raw)
+    if r:
+        _fail("bcq_rms_norm", r)
 
 
 # ----------------------------------------------------------------------------- 4-bit cache

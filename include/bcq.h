@@ -459,6 +459,33 @@ bcq_status bcq_int_linear(const void *X, int32_t T, int32_t ldx, const int8_t *W
 size_t bcq_int_workspace_bytes(int32_t T, int32_t M, int32_t K);
 
 /*
+ * The norm before a product, with the residual's addition before it and the
+ * rounding to 8 bits behind it; row by row of X [T][ldx]:
+ *     h = X + residual                                     rounded to dtype
+ *     y = (h * inv) * gamma,  inv = 1 / sqrt(sum_k h^2 / K + eps)
+ *     scales = max_k |y| * (1/127),  codes = rint(y / scales)
+ * with the squares summed in fp64, inv rounded once to fp32 and every other step
+ * one operation in fp32 (the constant too); a row of zeros has codes and scale
+ * 0, a row whose h or y holds an infinity or NaN has codes 0 and scale NaN.
+ * residual: [T][ldr], or NULL for none (h = X).  gamma: [K].
+ * H: [T][ldh], gets h; NULL where it is not needed.  It may be X or residual, with
+ *   the same leading dimension; otherwise it overlaps neither.
+ * Y: [T][ldy], gets y rounded to dtype, as the planes' products read it, or NULL.
+ * codes: [T][ldc], scales: [T], as bcq_int_quantize writes them and bcq_int_gemm
+ *   reads them (ldc a multiple of 16, at least K rounded up to one, zeros from K up
+ *   to that multiple), or both NULL.  One of H, Y and codes at least is given.
+ * X, residual, gamma, H and Y are of dtype (BCQ_F16 or BCQ_F32), 16-byte aligned
+ *   with ld*size a multiple of 16 bytes and ld >= K; codes are 16-byte aligned.
+ *   Nothing past K is read, or written but for those zeros.
+ * eps: from FLT_MIN to FLT_MAX.  1 <= K <= 131071, T < 2^24; T = 0 does nothing.
+ * Validation and stream behaviour as in bcq_gemv.
+ */
+bcq_status bcq_rms_norm(const void *X, int32_t ldx, const void *residual, int32_t ldr,
+                        const void *gamma, double eps, int32_t T, int32_t K, bcq_dtype dtype,
+                        void *H, int32_t ldh, void *Y, int32_t ldy, int8_t *codes, int32_t ldc,
+                        float *scales, hipStream_t stream);
+
+/*
  * A key/value cache held in 4 bits, in pages.
  *
  * Each vector (one token's key or value of one cached head, head_dim channels)

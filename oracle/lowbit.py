@@ -165,3 +165,19 @@ def evict(length, keep, recent, weights, pos):
     fill = [t for t in kept.tolist() if t >= m]
     src[holes] = fill
     return src
+
+
+# ------------------------------------------------------------------------------ norm
+
+
+def rms_norm(x, residual, gamma, eps):
+    """(h, y, codes, scale) of rows x [T][K] of float16 or float32: h in the rows' type, y in
+    float64 from h, the codes and scales from single operations in float32 as the format says."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        h = x if residual is None else \
+            (x.astype(np.float32) + residual.astype(np.float32)).astype(x.dtype)
+        h64 = h.astype(np.float64)
+        inv = 1 / np.sqrt((h64 * h64).mean(axis=1, keepdims=True) + eps)
+        y = h64 * inv * gamma.astype(np.float64)
+        y32 = h.astype(np.float32) * inv.astype(np.float32) * gamma.astype(np.float32)
+    return (h, y) + quantize_rows(y32)
