@@ -18,7 +18,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbcq.so")
 SOURCES = ["bcq_api.hip", "pack.hip", "gemv_lut.hip", "gemm_mfma.hip", "lowrank.hip", "dequant.hip",
            "quantize.hip", "serve_api.hip", "int_gemm.hip", "norm.hip", "kv_cache.hip",
-           "kv_attend.hip"]
+           "kv_reserve.hip", "kv_attend.hip"]
 # Per-file flags: the quantizers' codes are functions of exactly rounded values
 # (fp64 in the planes', fp32 in the key/value cache's), so no multiply-add there
 # is fused into one rounding; so are the norm's (fp32).

@@ -1,5 +1,5 @@
 // kv_cache.hip -- what fills, reads back and shrinks the 4-bit key/value cache
-// (bcq_kv_append, bcq_kv_read, bcq_kv_evict).
+// (bcq_kv_append, bcq_kv_read, the same by slots, bcq_kv_evict).
 //
 // A vector of D channels (one token's K or V of one cached head) is
 // zero + scale * code: zero = fp16(min), scale = fp16((max - min) * (1/15)),
@@ -90,29 +90,20 @@ __host__ __forceinline__ uint32_t vectors_of(const KvView &c, int n) {
   return (uint32_t)c.B * c.H * 2 * (n == 1 ? 1 : quads_of(n) * 4);
 }
 
-// Bound by the bytes of the vectors read; every lane converts what it loads,
-// the extremes meet in D/4 lanes and no shared memory is needed.  2 x 4099 tokens
-// of 8 heads of 64 channels in fp32, slices of one projection (33.6 MB read, 4.6
-// MB written): 17.0 us, 2.2 TB/s; four vectors a group of lanes took 20.4 us.
+// A vector's 4 channels of this lane as codes (bits 4e of `word`) and the vector's
+// scale and zero, the same in all its D/4 lanes.
+struct Coded {
+  uint32_t word;
+  _Float16 scale, zero;
+};
 template <int D, typename T, bool VEC>
-__global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k, KvStrides ks,
-                                                     const T *v, KvStrides vs,
-                                                     const int32_t *positions, float *weights,
-                                                     int32_t *pos, uint32_t vecs) {
-  constexpr int L = D / 4;
-  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int i = threadIdx.x % L;
-  if (vec >= vecs) return;  // whole groups of L lanes leave together
-  const Place p = place(c, n, vec);
-  if (!p.in) return;
-  const KvStrides st = p.v ? vs : ks;
-  const T *src = (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4;
+__device__ __forceinline__ Coded code_vector(const T *src) {
   float x[4];
   load4<T, VEC>(x, src);
   float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
   float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
 #pragma unroll
-  for (int d = 1; d < L; d <<= 1) {
+  for (int d = 1; d < D / 4; d <<= 1) {
     lo = nan_min(lo, __shfl_xor(lo, d));
     hi = nan_max(hi, __shfl_xor(hi, d));
   }
@@ -142,25 +133,70 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     word |= (scale > 0.f ? (uint32_t)fminf(fmaxf(q[e], 0.f), 15.f) : 0u) << (4 * e);
-  if (p.slot < 0) return;
-  const int64_t token = kv_token(c, p.b, p.h, p.slot);
-  if (token < 0) return;
-  *reinterpret_cast<uint16_t *>(p.v ? c.v + v_byte<D>(token, i) : c.k + k_byte<D>(token, i)) =
-      (uint16_t)word;
+  return {word, sh, zh};
+}
+// Stored as K or V of cached token `token` (lane i of the vector's).
+template <int D>
+__device__ __forceinline__ void put_vector(const KvView &c, const Coded &x, int64_t token, bool v,
+                                           int i) {
+  *reinterpret_cast<uint16_t *>(v ? c.v + v_byte<D>(token, i) : c.k + k_byte<D>(token, i)) =
+      (uint16_t)x.word;
   if (i == 0) {
     union {
       _Float16 h[2];
       uint32_t u;
     } m;
-    m.h[0] = sh;
-    m.h[1] = zh;
-    *reinterpret_cast<uint32_t *>(c.scales + token * 4 + (p.v ? 2 : 0)) = m.u;
-    if (!p.v) {
-      const int64_t at = ((int64_t)p.b * c.H + p.h) * c.room() + p.slot;
-      if (weights != nullptr) weights[at] = 0.f;
-      if (pos != nullptr)
-        pos[at] = positions != nullptr ? positions[(int64_t)p.b * n + p.i] : p.slot;
-    }
+    m.h[0] = x.scale;
+    m.h[1] = x.zero;
+    *reinterpret_cast<uint32_t *>(c.scales + token * 4 + (v ? 2 : 0)) = m.u;
+  }
+}
+// The values of cached token `token`, zeros where it is negative.
+template <int D, typename T, bool VEC>
+__device__ __forceinline__ void get_vector(const KvView &c, T *dst, int64_t token, bool v, int i) {
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (token >= 0) {
+    const uint32_t word = *reinterpret_cast<const uint16_t *>(v ? c.v + v_byte<D>(token, i)
+                                                                : c.k + k_byte<D>(token, i));
+    union {
+      uint32_t u;
+      _Float16 h[2];
+    } m;
+    m.u = *reinterpret_cast<const uint32_t *>(c.scales + token * 4 + (v ? 2 : 0));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[e] = (float)m.h[1] + (float)m.h[0] * (float)((word >> (4 * e)) & 15u);
+  }
+  store4<T, VEC>(dst, x);
+}
+
+// Bound by the bytes of the vectors read; every lane converts what it loads,
+// the extremes meet in D/4 lanes and no shared memory is needed.  2 x 4099 tokens
+// of 8 heads of 64 channels in fp32, slices of one projection (33.6 MB read, 4.6
+// MB written): 17.0 us, 2.2 TB/s; four vectors a group of lanes took 20.4 us.
+template <int D, typename T, bool VEC>
+__global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k, KvStrides ks,
+                                                     const T *v, KvStrides vs,
+                                                     const int32_t *positions, float *weights,
+                                                     int32_t *pos, uint32_t vecs) {
+  constexpr int L = D / 4;
+  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int i = threadIdx.x % L;
+  if (vec >= vecs) return;  // whole groups of L lanes leave together
+  const Place p = place(c, n, vec);
+  if (!p.in) return;
+  const KvStrides st = p.v ? vs : ks;
+  const Coded x = code_vector<D, T, VEC>((p.v ? v : k) + p.b * st.batch + p.i * st.token +
+                                         p.h * st.head + i * 4);
+  if (p.slot < 0) return;
+  const int64_t token = kv_token(c, p.b, p.h, p.slot);
+  if (token < 0) return;
+  put_vector<D>(c, x, token, p.v, i);
+  if (i == 0 && !p.v) {
+    const int64_t at = ((int64_t)p.b * c.H + p.h) * c.room() + p.slot;
+    if (weights != nullptr) weights[at] = 0.f;
+    if (pos != nullptr)
+      pos[at] = positions != nullptr ? positions[(int64_t)p.b * n + p.i] : p.slot;
   }
 }
 
@@ -174,22 +210,66 @@ __global__ __launch_bounds__(256) void read_kernel(KvView c, int n, T *k, KvStri
   const Place p = place(c, n, vec);
   if (!p.in) return;
   const KvStrides st = p.v ? vs : ks;
-  T *dst = (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4;
   const int64_t token = p.slot < 0 ? -1 : kv_token(c, p.b, p.h, p.slot);
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
-  if (token >= 0) {
-    const uint32_t word = *reinterpret_cast<const uint16_t *>(
-        p.v ? c.v + v_byte<D>(token, i) : c.k + k_byte<D>(token, i));
-    union {
-      uint32_t u;
-      _Float16 h[2];
-    } m;
-    m.u = *reinterpret_cast<const uint32_t *>(c.scales + token * 4 + (p.v ? 2 : 0));
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      x[e] = (float)m.h[1] + (float)m.h[0] * (float)((word >> (4 * e)) & 15u);
-  }
-  store4<T, VEC>(dst, x);
+  get_vector<D, T, VEC>(c, (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4,
+                        token, p.v, i);
+}
+
+// Packed tokens, each with its slot among all the pages.  Four tokens that follow
+// each other are neighbours, K before V, then heads, so that what they write of a
+// block of V mostly comes from one wave.
+struct PackedPlace {
+  int64_t t, slot;
+  int h;
+  bool v;
+};
+__device__ __forceinline__ PackedPlace packed_place(const KvView &c, const int64_t *slots, int T,
+                                                    uint32_t vec) {
+  PackedPlace p;
+  p.v = vec >> 2 & 1;
+  const uint32_t quad = (vec >> 3) / (uint32_t)c.H;
+  p.h = (int)((vec >> 3) - quad * (uint32_t)c.H);
+  p.t = (int64_t)quad * 4 + (vec & 3);
+  p.slot = p.t < T ? slots[p.t] : -1;
+  return p;
+}
+// Index of a slot's token within all the pages of cached head h, as kv_token, or -1
+// for a slot that no page has.
+__device__ __forceinline__ int64_t slot_token(const KvView &c, int64_t slot, int h) {
+  const int64_t page = slot >> c.page_log;
+  if ((uint64_t)page >= (uint64_t)c.num_pages) return -1;
+  return ((page * c.H + h) << c.page_log) + (slot & ((1 << c.page_log) - 1));
+}
+
+template <int D, typename T, bool VEC>
+__global__ __launch_bounds__(256) void append_slots_kernel(KvView c, int n, const int64_t *slots,
+                                                           const T *k, KvStrides ks, const T *v,
+                                                           KvStrides vs, uint32_t vecs) {
+  constexpr int L = D / 4;
+  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int i = threadIdx.x % L;
+  if (vec >= vecs) return;
+  const PackedPlace p = packed_place(c, slots, n, vec);
+  const int64_t token = slot_token(c, p.slot, p.h);
+  if (token < 0) return;  // whole groups of L lanes leave together
+  const KvStrides st = p.v ? vs : ks;
+  put_vector<D>(c, code_vector<D, T, VEC>((p.v ? v : k) + p.t * st.token + p.h * st.head + i * 4),
+                token, p.v, i);
+}
+
+template <int D, typename T, bool VEC>
+__global__ __launch_bounds__(256) void read_slots_kernel(KvView c, int n, const int64_t *slots,
+                                                         T *k, KvStrides ks, T *v, KvStrides vs,
+                                                         uint32_t vecs) {
+  constexpr int L = D / 4;
+  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int i = threadIdx.x % L;
+  if (vec >= vecs) return;
+  const PackedPlace p = packed_place(c, slots, n, vec);
+  if (p.t >= n) return;
+  const KvStrides st = p.v ? vs : ks;
+  get_vector<D, T, VEC>(c, (p.v ? v : k) + p.t * st.token + p.h * st.head + i * 4,
+                        slot_token(c, p.slot, p.h), p.v, i);
 }
 
 bool vec_ok(const void *p, KvStrides s, size_t size) {
@@ -222,6 +302,40 @@ hipError_t read_dim(const KvView &c, int n, void *k, KvStrides ks, void *v, KvSt
   else
     read_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, (T *)k, ks, (T *)v, vs, vecs);
   return hipGetLastError();
+}
+
+template <int D, typename T, typename K>
+hipError_t slots_dim(const KvView &c, int n, const int64_t *slots, K *k, KvStrides ks, K *v,
+                     KvStrides vs, hipStream_t s) {
+  const uint32_t vecs = (uint32_t)c.H * 8 * (((uint32_t)n + 3) / 4), per = 256 / (D / 4);
+  const uint32_t grid = (vecs + per - 1) / per;
+  const bool vec = vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T));
+  if constexpr (std::is_const<K>::value) {
+    if (vec)
+      append_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (const T *)k, ks,
+                                                           (const T *)v, vs, vecs);
+    else
+      append_slots_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, slots, (const T *)k, ks,
+                                                            (const T *)v, vs, vecs);
+  } else {
+    if (vec)
+      read_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs, vecs);
+    else
+      read_slots_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs,
+                                                          vecs);
+  }
+  return hipGetLastError();
+}
+template <typename K>
+hipError_t launch_slots(const KvView &c, int D, int n, const int64_t *slots, K *k, KvStrides ks,
+                        K *v, KvStrides vs, bcq_dtype dt, hipStream_t s) {
+  if (dt == BCQ_F16)
+    return D == 64    ? slots_dim<64, _Float16>(c, n, slots, k, ks, v, vs, s)
+           : D == 128 ? slots_dim<128, _Float16>(c, n, slots, k, ks, v, vs, s)
+                      : slots_dim<256, _Float16>(c, n, slots, k, ks, v, vs, s);
+  return D == 64    ? slots_dim<64, float>(c, n, slots, k, ks, v, vs, s)
+         : D == 128 ? slots_dim<128, float>(c, n, slots, k, ks, v, vs, s)
+                    : slots_dim<256, float>(c, n, slots, k, ks, v, vs, s);
 }
 
 // ---- eviction
@@ -841,6 +955,17 @@ hipError_t launch_kv_read(const KvView &c, int D, int n, void *k, KvStrides ks, 
   if (D == 128) BCQ_DIM(128);
   BCQ_DIM(256);
 #undef BCQ_DIM
+}
+
+hipError_t launch_kv_append_slots(const KvView &c, int D, int n, const int64_t *slots,
+                                  const void *k, KvStrides ks, const void *v, KvStrides vs,
+                                  bcq_dtype dt, hipStream_t s) {
+  return launch_slots(c, D, n, slots, k, ks, v, vs, dt, s);
+}
+hipError_t launch_kv_read_slots(const KvView &c, int D, int n, const int64_t *slots, void *k,
+                                KvStrides ks, void *v, KvStrides vs, bcq_dtype dt,
+                                hipStream_t s) {
+  return launch_slots(c, D, n, slots, k, ks, v, vs, dt, s);
 }
 
 size_t evict_workspace_bytes(int B, int H, int room, int keep) {

@@ -109,6 +109,20 @@ bcq_status check_vectors(const bcq_kv_cache *c, int32_t n, const void *k, const 
   return BCQ_OK;
 }
 
+// K and V of T packed tokens.
+bcq_status check_packed(const bcq_kv_cache *c, int32_t T, const int64_t *slots, const void *k,
+                        const void *v, bcq_dtype dtype) {
+  BCQ_TRY(check_cache(c));
+  if (!dtype_valid(dtype) || T < 0 || T > BCQ_KV_MAX_TOKENS) return BCQ_ERR_INVALID_ARG;
+  // a work item takes four channels of K or V, of up to three tokens more than T
+  if ((int64_t)c->heads * ((int64_t)T + 3) * c->head_dim >= ((int64_t)1 << 33) - 512)
+    return BCQ_ERR_INVALID_ARG;
+  if (T > 0 && (slots == nullptr || k == nullptr || v == nullptr)) return BCQ_ERR_INVALID_ARG;
+  if (!aligned(slots, 8) || !aligned(k, dtype_size(dtype)) || !aligned(v, dtype_size(dtype)))
+    return BCQ_ERR_ALIGNMENT;
+  return BCQ_OK;
+}
+
 bcq_status check_attend(const bcq_kv_cache *c, int32_t n, int32_t q_heads) {
   BCQ_TRY(check_cache(c));
   if (n < 0 || n > BCQ_KV_MAX_TOKENS) return BCQ_ERR_INVALID_ARG;
@@ -229,6 +243,64 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
   return hip_status(bcq::launch_kv_read(view(cache), cache->head_dim, n, K,
                                         {k_batch, k_token, k_head}, V,
                                         {v_batch, v_token, v_head}, dtype, stream));
+}
+
+bcq_status bcq_kv_append_slots(const bcq_kv_cache *cache, int32_t T, const int64_t *slots,
+                               const void *K, int64_t k_token, int64_t k_head, const void *V,
+                               int64_t v_token, int64_t v_head, bcq_dtype dtype,
+                               hipStream_t stream) {
+  BCQ_TRY(check_packed(cache, T, slots, K, V, dtype));
+  if (T == 0) return BCQ_OK;
+  return hip_status(bcq::launch_kv_append_slots(view(cache), cache->head_dim, T, slots, K,
+                                                {0, k_token, k_head}, V, {0, v_token, v_head},
+                                                dtype, stream));
+}
+
+bcq_status bcq_kv_read_slots(const bcq_kv_cache *cache, int32_t T, const int64_t *slots, void *K,
+                             int64_t k_token, int64_t k_head, void *V, int64_t v_token,
+                             int64_t v_head, bcq_dtype dtype, hipStream_t stream) {
+  BCQ_TRY(check_packed(cache, T, slots, K, V, dtype));
+  if (T == 0) return BCQ_OK;
+  return hip_status(bcq::launch_kv_read_slots(view(cache), cache->head_dim, T, slots, K,
+                                              {0, k_token, k_head}, V, {0, v_token, v_head},
+                                              dtype, stream));
+}
+
+size_t bcq_kv_reserve_workspace_bytes(const bcq_kv_cache *cache) {
+  if (check_cache(cache) != BCQ_OK) return 0;
+  return bcq::reserve_workspace_bytes(cache->batch, cache->max_pages);
+}
+
+bcq_status bcq_kv_reserve(const bcq_kv_cache *cache, const int32_t *new_tokens,
+                          const int32_t *release, int32_t shared_pages,
+                          const int32_t *free_pages, const int32_t *free_count, int32_t T,
+                          int32_t *lens_out, int32_t *page_table_out, int32_t *free_pages_out,
+                          int32_t *free_count_out, int32_t *starts, int64_t *slots,
+                          int32_t *positions, void *workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  BCQ_TRY(check_cache(cache));
+  if (T < 0 || T > BCQ_KV_MAX_TOKENS || shared_pages < 0 || shared_pages > cache->max_pages)
+    return BCQ_ERR_INVALID_ARG;
+  if (new_tokens == nullptr || free_pages == nullptr || free_count == nullptr ||
+      lens_out == nullptr || page_table_out == nullptr || free_pages_out == nullptr ||
+      free_count_out == nullptr || starts == nullptr ||
+      (T > 0 && (slots == nullptr || positions == nullptr)))
+    return BCQ_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)new_tokens, (const void *)release, (const void *)free_pages,
+                        (const void *)free_count, (const void *)lens_out,
+                        (const void *)page_table_out, (const void *)free_pages_out,
+                        (const void *)free_count_out, (const void *)starts,
+                        (const void *)positions})
+    if (!aligned(p, 4)) return BCQ_ERR_ALIGNMENT;
+  if (!aligned(slots, 8)) return BCQ_ERR_ALIGNMENT;
+  if (workspace == nullptr || workspace_bytes < bcq_kv_reserve_workspace_bytes(cache))
+    return BCQ_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16)) return BCQ_ERR_ALIGNMENT;
+  const bcq::ReserveCall r{new_tokens,     release,        free_pages, free_count,
+                           lens_out,       page_table_out, free_pages_out,
+                           free_count_out, starts,         positions,  slots,
+                           shared_pages,   T};
+  return hip_status(bcq::launch_kv_reserve(view(cache), r, workspace, stream));
 }
 
 size_t bcq_kv_workspace_bytes(const bcq_kv_cache *cache, int32_t n, int32_t q_heads,

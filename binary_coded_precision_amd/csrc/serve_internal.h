@@ -68,6 +68,24 @@ hipError_t launch_kv_append(const KvView &c, int D, int n, const void *k, KvStri
 hipError_t launch_kv_read(const KvView &c, int D, int n, void *k, KvStrides ks, void *v,
                           KvStrides vs, bcq_dtype dt, hipStream_t s);
 
+// The same for n packed tokens, each in a slot (a place among all the pages'
+// tokens); those in no page's are not there.
+hipError_t launch_kv_append_slots(const KvView &c, int D, int n, const int64_t *slots,
+                                  const void *k, KvStrides ks, const void *v, KvStrides vs,
+                                  bcq_dtype dt, hipStream_t s);
+hipError_t launch_kv_read_slots(const KvView &c, int D, int n, const int64_t *slots, void *k,
+                                KvStrides ks, void *v, KvStrides vs, bcq_dtype dt, hipStream_t s);
+
+// Pages given and taken back (kv_reserve.hip); see bcq_kv_reserve.
+struct ReserveCall {
+  const int32_t *new_tokens, *release, *free_pages, *free_count;
+  int32_t *lens_out, *table_out, *free_out, *count_out, *starts, *positions;
+  int64_t *slots;
+  int shared_pages, T;
+};
+size_t reserve_workspace_bytes(int B, int max_pages);
+hipError_t launch_kv_reserve(const KvView &c, const ReserveCall &r, void *ws, hipStream_t s);
+
 // How a call of the attention is laid out; host arithmetic on shapes only, so
 // that the workspace's size and the launch agree.
 struct AttendPlan {

@@ -1,5 +1,5 @@
 """Binding of the low-bit serving operators: the 8-bit integer linear layer, the norm before it
-and the 4-bit key/value cache (append, read, attend, evict).  Names and semantics are those of
+and the 4-bit key/value cache (reserve, append, read, attend, evict).  Names and semantics are those of
 ``include/bcq.h``; the package exports everything here.
 
 The tensors of a call, and its ``stream`` if one is given, belong to one device, which need not be
@@ -37,6 +37,11 @@ SIGNATURES = {
     "bcq_kv_append": (_int, [_kc, _i32, _vp, *_strides, _vp, *_strides, _int, _vp, _vp, _vp,
                              _vp]),
     "bcq_kv_read": (_int, [_kc, _i32, _vp, *_strides, _vp, *_strides, _int, _vp]),
+    "bcq_kv_reserve": (_int, [_kc, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _vp, _vp, _sz, _vp]),
+    "bcq_kv_reserve_workspace_bytes": (_sz, [_kc]),
+    "bcq_kv_append_slots": (_int, [_kc, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp]),
+    "bcq_kv_read_slots": (_int, [_kc, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp]),
     "bcq_kv_attend": (_int, [_kc, _vp, _i32, _i32, *_strides, _vp, *_strides, _int,
                              ctypes.c_float, _vp, _vp, _sz, _vp]),
     "bcq_kv_workspace_bytes": (_sz, [_kc, _i32, _i32, _i32]),
@@ -325,7 +330,7 @@ class KVCache:
         self.k_codes, self.v_codes, self.scales = k_codes, v_codes, scales
         self.page_table, self.lens = page_table, lens
         self.batch, self.heads, self.head_dim, self.page_tokens = B, H, D, page
-        self.room = width * page
+        self.room, self.num_pages = width * page, P
         self._slots = (B, H, self.room)  # of weights and positions
 
     @classmethod
@@ -341,6 +346,23 @@ class KVCache:
                    z((P, heads, page_tokens, 4), torch.float16),
                    torch.arange(P, dtype=torch.int32, device=device).view(batch, width),
                    z((batch,), torch.int32))
+
+    @classmethod
+    def pool(cls, batch: int, tokens: int, pages: int, heads: int, head_dim: int,
+             page_tokens: int = 64, device="cuda"):
+        """``(cache, free_pages, free_count)`` for :func:`bcq_kv_reserve`: `pages` pages, all of
+        them free, and empty tables with room for `tokens` tokens of each of `batch` sequences."""
+        _lib or _bind()
+        z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)  # noqa: E731
+        cache = cls(z((pages, heads, page_tokens, head_dim // 2), torch.uint8),
+                    z((pages, heads, page_tokens // 4, 2 * head_dim), torch.uint8),
+                    z((pages, heads, page_tokens, 4), torch.float16),
+                    torch.full((batch, -(-tokens // page_tokens)), -1, dtype=torch.int32,
+                               device=device),
+                    z((batch,), torch.int32))
+        # the lowest on top
+        return (cache, torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device),
+                torch.full((1,), pages, dtype=torch.int32, device=device))
 
     def tracking(self):
         """Zeroed ``(weights, pos)`` for this cache, as append, attend and evict take them."""
@@ -397,6 +419,95 @@ def bcq_kv_read(cache: KVCache, K, V, stream=None) -> None:
                          vs[1], vs[2], dt, _raw(dev, stream))
     if r:
         _fail("bcq_kv_read", r)
+
+
+def bcq_kv_reserve_workspace_bytes(cache: KVCache) -> int:
+    return int(_lib.bcq_kv_reserve_workspace_bytes(cache._ref))
+
+
+def new_kv_reserve_workspace(cache: KVCache):
+    """A device workspace for :func:`bcq_kv_reserve`; calls that may overlap need separate ones."""
+    return _workspace(bcq_kv_reserve_workspace_bytes(cache), cache.lens.device, None)
+
+
+def bcq_kv_reserve(cache: KVCache, new_tokens, free_pages, free_count, starts, slots, positions,
+                   release=None, shared_pages: int = 0, lens_out=None, page_table_out=None,
+                   free_pages_out=None, free_count_out=None, workspace=None, stream=None) -> None:
+    """Takes back the pages of the sequences that ended (``release`` int32 [batch], or None) and
+    gives pages for ``new_tokens`` int32 [batch] from the stack ``free_pages`` int32 [pages] of
+    ``free_count`` int32 [1].  Writes ``starts`` int32 [batch + 1] and, for T packed tokens,
+    ``slots`` int64 [T] and ``positions`` int32 [T]; the cache's lengths and table and the stack
+    in place unless the ``_out`` arrays are given (see ``include/bcq.h``)."""
+    dev, i32 = cache._dev, torch.int32
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_reserve, cache, new_tokens, free_pages, free_count, starts,
+                      slots, positions, release, shared_pages, lens_out, page_table_out,
+                      free_pages_out, free_count_out, workspace, stream)
+    raw, B, T = _raw(dev, stream), (cache.batch,), slots.shape
+    stack = (cache.num_pages,)
+    free = _plain("free_pages", free_pages, i32, stack, dev)
+    count = _plain("free_count", free_count, i32, (1,), dev)
+    if len(T) != 1:
+        raise ValueError("slots must be [T], got %s" % (tuple(T),))
+    if workspace is None:
+        workspace = _workspace(bcq_kv_reserve_workspace_bytes(cache), cache.lens.device, stream)
+    r = _lib.bcq_kv_reserve(
+        cache._ref, _plain("new_tokens", new_tokens, i32, B, dev),
+        0 if release is None else _plain("release", release, i32, B, dev), shared_pages, free,
+        count, T[0],
+        cache._st.lens if lens_out is None else _plain("lens_out", lens_out, i32, B, dev),
+        cache._st.page_table if page_table_out is None
+        else _plain("page_table_out", page_table_out, i32, cache.page_table.shape, dev),
+        free if free_pages_out is None
+        else _plain("free_pages_out", free_pages_out, i32, stack, dev),
+        count if free_count_out is None
+        else _plain("free_count_out", free_count_out, i32, (1,), dev),
+        _plain("starts", starts, i32, (cache.batch + 1,), dev),
+        _plain("slots", slots, torch.int64, T, dev), _plain("positions", positions, i32, T, dev),
+        *_space(workspace, dev), raw)
+    if r:
+        _fail("bcq_kv_reserve", r)
+
+
+def _packed(K, V, slots, cache: KVCache):
+    """(T, dtype, strides of K, of V) of packed vectors [T][heads][D] with contiguous channels."""
+    shape = K.shape
+    if len(shape) != 3 or shape[1] != cache.heads or shape[2] != cache.head_dim or \
+            V.shape != shape:
+        raise ValueError("K and V must be [T][%d][%d], got %s and %s" %
+                         (cache.heads, cache.head_dim, tuple(shape), tuple(V.shape)))
+    dt = _float("K", K, cache._dev)
+    if V.dtype is not K.dtype or V.get_device() != cache._dev:
+        raise ValueError("K and V must be device tensors of one dtype on the cache's device")
+    ks, vs = K.stride(), V.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError("K and V must have contiguous channels")
+    return shape[0], dt, ks, vs, _plain("slots", slots, torch.int64, shape[:1], cache._dev)
+
+
+def bcq_kv_append_slots(cache: KVCache, K, V, slots, stream=None) -> None:
+    """Quantizes packed ``K`` and ``V`` [T][heads][D] into the slots ``slots`` int64 [T], as
+    :func:`bcq_kv_reserve` writes them."""
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_append_slots, cache, K, V, slots, stream)
+    T, dt, ks, vs, sp = _packed(K, V, slots, cache)
+    r = _lib.bcq_kv_append_slots(cache._ref, T, sp, K.data_ptr(), ks[0], ks[1], V.data_ptr(),
+                                 vs[0], vs[1], dt, _raw(dev, stream))
+    if r:
+        _fail("bcq_kv_append_slots", r)
+
+
+def bcq_kv_read_slots(cache: KVCache, K, V, slots, stream=None) -> None:
+    """Writes the values cached in ``slots`` int64 [T] to ``K`` and ``V`` [T][heads][D]."""
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_read_slots, cache, K, V, slots, stream)
+    T, dt, ks, vs, sp = _packed(K, V, slots, cache)
+    r = _lib.bcq_kv_read_slots(cache._ref, T, sp, K.data_ptr(), ks[0], ks[1], V.data_ptr(), vs[0],
+                               vs[1], dt, _raw(dev, stream))
+    if r:
+        _fail("bcq_kv_read_slots", r)
 
 
 def bcq_kv_workspace_bytes(cache: KVCache, n: int, q_heads: int, with_weights: bool) -> int:

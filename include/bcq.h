@@ -565,6 +565,67 @@ bcq_status bcq_kv_read(const bcq_kv_cache *cache, int32_t n, void *K, int64_t k_
                        int64_t v_token, int64_t v_head, bcq_dtype dtype, hipStream_t stream);
 
 /*
+ * Pages for the new tokens of a step whose sequences bring unlike numbers of them, and
+ * where each of those tokens lies: packed, those of sequence 0 first.  A cache used
+ * so has its pages from a stack of free ones and any number of sequences beside
+ * shared pages: the first shared_pages entries of every sequence's table name the
+ * same pages (a common prefix), which the caller has filled and which are neither
+ * given nor taken back; every sequence counts shared_pages * page_tokens tokens from
+ * the start on (shorter lengths are taken as that).
+ *
+ * One step, on the device, in the sequences' order:
+ *  1. A sequence with release[b] != 0 (release NULL: none) has ended.  Its pages past
+ *     the shared ones go on top of the stack in its table's order, and its length
+ *     becomes that of the shared pages.
+ *  2. Sequence b asks for new_tokens[b] tokens (0 and less: none) and, where its last
+ *     page has no room for them, pages.  It is refused where they pass its table
+ *     (max_pages), and gets nothing.  What the others ask for is summed up: it is
+ *     granted, all of it, where the tokens asked for up to and with it are at most T
+ *     and it needs no page or the pages asked for up to and with it are there.
+ *  3. Its i-th new page is the one below those given before it, from the top.
+ *
+ * lens_out [batch], page_table_out [batch][max_pages], free_pages_out [num_pages],
+ *   free_count_out [1]: the state afterwards, each the array read (cache->lens,
+ *   cache->page_table, free_pages, free_count) for an update in place, or one that
+ *   does not overlap it.  Entries of a table past a sequence's pages and of the stack
+ *   from the new count on are not written; in place only the new entries are.
+ * starts [batch + 1]: packed tokens before each sequence's, and of all: a request that
+ *   was refused has none.  slots [T]: each token's slot, page * page_tokens + its place
+ *   in the page, and positions [T]: its place in the sequence; -1 for both from
+ *   starts[batch] on.
+ * free_count is clamped to 0 .. num_pages.  Entries that name no page are given and
+ *   taken like others, and never followed.  0 <= T <= BCQ_KV_MAX_TOKENS.
+ * workspace: bcq_kv_reserve_workspace_bytes(cache) bytes, 16-byte aligned, of no
+ *   account before and after; calls that may run at the same time need separate ones.
+ * Validation and stream behaviour as in bcq_gemv.
+ */
+bcq_status bcq_kv_reserve(const bcq_kv_cache *cache, const int32_t *new_tokens,
+                          const int32_t *release, int32_t shared_pages,
+                          const int32_t *free_pages, const int32_t *free_count, int32_t T,
+                          int32_t *lens_out, int32_t *page_table_out, int32_t *free_pages_out,
+                          int32_t *free_count_out, int32_t *starts, int64_t *slots,
+                          int32_t *positions, void *workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* Device workspace of bcq_kv_reserve, 0 for an invalid cache. */
+size_t bcq_kv_reserve_workspace_bytes(const bcq_kv_cache *cache);
+
+/*
+ * bcq_kv_append and bcq_kv_read for T packed tokens, token t in slot slots[t] (as
+ * bcq_kv_reserve writes them; of a call's tokens no two in one).  A slot that lies in
+ * no page is never followed: nothing is written there, and zeros are read.
+ * K, V: element (t, h, d) at t*_token + h*_head + d.  The table and lengths of the
+ * cache are not read.  heads * (T + 3) * head_dim below 2^33 - 512; T = 0 does nothing.
+ */
+bcq_status bcq_kv_append_slots(const bcq_kv_cache *cache, int32_t T, const int64_t *slots,
+                               const void *K, int64_t k_token, int64_t k_head, const void *V,
+                               int64_t v_token, int64_t v_head, bcq_dtype dtype,
+                               hipStream_t stream);
+bcq_status bcq_kv_read_slots(const bcq_kv_cache *cache, int32_t T, const int64_t *slots, void *K,
+                             int64_t k_token, int64_t k_head, void *V, int64_t v_token,
+                             int64_t v_head, bcq_dtype dtype, hipStream_t stream);
+
+/*
  * Attention of the last n tokens' queries over the cache, causal: query i of
  * sequence b sees slots 0 .. lens[b] - n + i.
  *     O[b][i][g] = sum_t softmax_t(scale * Q[b][i][g] . k_t) v_t

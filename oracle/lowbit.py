@@ -181,3 +181,44 @@ def rms_norm(x, residual, gamma, eps):
         y = h64 * inv * gamma.astype(np.float64)
         y32 = h.astype(np.float32) * inv.astype(np.float32) * gamma.astype(np.float32)
     return (h, y) + quantize_rows(y32)
+
+
+# ------------------------------------------------------------------------------ pages
+
+
+def reserve(lens, table, free, count, new, release, shared, page, T):
+    """One step of giving and taking pages, sequence by sequence: (lens, table, free, count,
+    starts, slots, positions) afterwards, arrays changed only where the step writes them."""
+    lens, table = [int(n) for n in lens], np.array(table)
+    stack = [int(p) for p in free[:count]]
+    B, width = table.shape
+    pages = lambda n: max(-(-n // page), shared)  # noqa: E731
+    lens = [max(min(max(n, 0), width * page), shared * page) for n in lens]
+    for b in range(B):
+        if release is not None and release[b]:
+            stack += [int(p) for p in table[b, shared:pages(lens[b])]]
+            lens[b] = shared * page
+    stack = stack[:len(free)]
+    starts, slots, positions = [0], [], []
+    asked_pages = asked_tokens = 0
+    top = len(stack)
+    for b in range(B):
+        want = max(int(new[b]), 0)
+        need = pages(lens[b] + want) - pages(lens[b])
+        if lens[b] + want > width * page:
+            want = need = 0
+        asked_pages += need
+        asked_tokens += want
+        if asked_tokens <= T and (need == 0 or asked_pages <= top):
+            for i in range(need):
+                table[b, pages(lens[b]) + i] = stack.pop()
+            for t in range(lens[b], lens[b] + want):
+                slots.append(int(table[b, t // page]) * page + t % page)
+                positions.append(t)
+            lens[b] += want
+        starts.append(len(slots))
+    free = np.array(free)
+    free[:len(stack)] = stack
+    rest = [-1] * (T - len(slots))
+    return (np.array(lens, np.int32), table, free, len(stack), np.array(starts, np.int32),
+            np.array(slots + rest, np.int64), np.array(positions + rest, np.int32))
