@@ -20,12 +20,14 @@ from typing import Dict, Optional, Sequence
 import numpy as np
 
 from . import lowbit
-from .lowbit import (BCQ_KV_MAX_TOKENS, KVCache, bcq_int_gemm, bcq_int_linear, bcq_int_quantize,
-                     bcq_int_workspace_bytes, bcq_kv_append, bcq_kv_append_slots, bcq_kv_attend,
-                     bcq_kv_evict, bcq_kv_evict_workspace_bytes, bcq_kv_read, bcq_kv_read_slots,
-                     bcq_kv_reserve, bcq_kv_reserve_workspace_bytes, bcq_kv_workspace_bytes,
-                     bcq_rms_norm, new_int_workspace, new_kv_evict_workspace,
-                     new_kv_reserve_workspace, new_kv_workspace)
+from .lowbit import (BCQ_KV_MAX_TOKENS, BCQ_KV_PACKED_MAX_BATCH, KVCache, bcq_int_gemm,
+                     bcq_int_linear, bcq_int_quantize, bcq_int_workspace_bytes, bcq_kv_append,
+                     bcq_kv_append_slots, bcq_kv_attend, bcq_kv_attend_packed, bcq_kv_evict,
+                     bcq_kv_evict_workspace_bytes, bcq_kv_packed_workspace_bytes, bcq_kv_read,
+                     bcq_kv_read_slots, bcq_kv_reserve, bcq_kv_reserve_workspace_bytes,
+                     bcq_kv_workspace_bytes, bcq_rms_norm, new_int_workspace,
+                     new_kv_evict_workspace, new_kv_packed_workspace, new_kv_reserve_workspace,
+                     new_kv_workspace)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbcq.so")

@@ -18,7 +18,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbcq.so")
 SOURCES = ["bcq_api.hip", "pack.hip", "gemv_lut.hip", "gemm_mfma.hip", "lowrank.hip", "dequant.hip",
            "quantize.hip", "serve_api.hip", "int_gemm.hip", "norm.hip", "kv_cache.hip",
-           "kv_reserve.hip", "kv_attend.hip"]
+           "kv_reserve.hip", "kv_attend.hip", "kv_packed.hip"]
 # Per-file flags: the quantizers' codes are functions of exactly rounded values
 # (fp64 in the planes', fp32 in the key/value cache's), so no multiply-add there
 # is fused into one rounding; so are the norm's (fp32).
@@ -26,7 +26,8 @@ SOURCES = ["bcq_api.hip", "pack.hip", "gemv_lut.hip", "gemm_mfma.hip", "lowrank.
 # in the matrix cores' own ones every rescaling loop would copy them both ways.
 FILE_FLAGS = {"quantize.hip": ["-ffp-contract=off"], "kv_cache.hip": ["-ffp-contract=off"],
               "norm.hip": ["-ffp-contract=off"],
-              "kv_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+              "kv_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "kv_packed.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 # Measurement kernels of the benchmark's floor row (empty launch, plain
 # streaming read): a library of their own, outside the BCQ ABI.
 PROBE_LIB = os.path.join(HERE, "libbcq_probe.so")

@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "serve_internal.h"
 
 namespace {
@@ -129,6 +131,22 @@ bcq_status check_attend(const bcq_kv_cache *c, int32_t n, int32_t q_heads) {
   if (q_heads < 1 || q_heads > (1 << 16) || q_heads % c->heads != 0) return BCQ_ERR_INVALID_ARG;
   // rows are counted in 32 bits
   if ((int64_t)n * q_heads > 1 << 28 || (int64_t)c->batch * n * q_heads > (int64_t)1 << 29)
+    return BCQ_ERR_INVALID_ARG;
+  return BCQ_OK;
+}
+
+bcq_status check_attend_packed(const bcq_kv_cache *c, int32_t T, int32_t q_heads, int32_t max_n,
+                               int32_t shared_pages) {
+  BCQ_TRY(check_cache(c));
+  if (c->batch > BCQ_KV_PACKED_MAX_BATCH || T < 0 || T > BCQ_KV_MAX_TOKENS)
+    return BCQ_ERR_INVALID_ARG;
+  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % c->heads != 0 ||
+      (int64_t)T * q_heads > 1 << 28)
+    return BCQ_ERR_INVALID_ARG;
+  if ((max_n < 1 && T > 0) || shared_pages < 0 || shared_pages > c->max_pages)
+    return BCQ_ERR_INVALID_ARG;
+  if (T > 0 && bcq::packed_workspace_bytes(c->batch, c->heads, c->head_dim, room(c), T, q_heads,
+                                           std::min(max_n, T), shared_pages > 0) == 0)
     return BCQ_ERR_INVALID_ARG;
   return BCQ_OK;
 }
@@ -338,6 +356,45 @@ bcq_status bcq_kv_attend(const bcq_kv_cache *cache, const void *Q, int32_t n, in
   a.weights = weights;
   a.ws = workspace;
   return hip_status(bcq::launch_kv_attend(a, scale, cache->head_dim, dtype, stream));
+}
+
+size_t bcq_kv_packed_workspace_bytes(const bcq_kv_cache *cache, int32_t T, int32_t q_heads,
+                                     int32_t max_n, int32_t shared_pages) {
+  if (check_attend_packed(cache, T, q_heads, max_n, shared_pages) != BCQ_OK || T == 0) return 0;
+  return bcq::packed_workspace_bytes(cache->batch, cache->heads, cache->head_dim, room(cache), T,
+                                     q_heads, std::min(max_n, T), shared_pages > 0);
+}
+
+bcq_status bcq_kv_attend_packed(const bcq_kv_cache *cache, const void *Q, int32_t T,
+                                int32_t q_heads, int64_t q_token, int64_t q_head,
+                                const int32_t *starts, int32_t max_n, int32_t shared_pages,
+                                void *O, int64_t o_token, int64_t o_head, bcq_dtype dtype,
+                                float scale, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream) {
+  BCQ_TRY(check_attend_packed(cache, T, q_heads, max_n, shared_pages));
+  if (!dtype_valid(dtype) || !isfinite(scale)) return BCQ_ERR_INVALID_ARG;
+  if (T == 0) return BCQ_OK;
+  if (Q == nullptr || O == nullptr || starts == nullptr) return BCQ_ERR_INVALID_ARG;
+  const size_t es = dtype_size(dtype);
+  if (!aligned(Q, es) || !aligned(O, es) || !aligned(starts, 4)) return BCQ_ERR_ALIGNMENT;
+  const size_t need =
+      bcq_kv_packed_workspace_bytes(cache, T, q_heads, max_n, shared_pages);
+  if (workspace == nullptr || workspace_bytes < need) return BCQ_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16)) return BCQ_ERR_ALIGNMENT;
+  bcq::PackedCall a{};
+  a.c = view(cache);
+  a.q = Q;
+  a.out = O;
+  a.qs = {0, q_token, q_head};
+  a.os = {0, o_token, o_head};
+  a.starts = starts;
+  a.T = T;
+  a.q_heads = q_heads;
+  a.max_n = std::min(max_n, T);
+  a.shared = shared_pages * cache->page_tokens;
+  a.q_wide = aligned(Q, 16) && (q_token * es) % 16 == 0 && (q_head * es) % 16 == 0;
+  a.ws = workspace;
+  return hip_status(bcq::launch_kv_attend_packed(a, scale, cache->head_dim, dtype, stream));
 }
 
 size_t bcq_kv_evict_workspace_bytes(const bcq_kv_cache *cache, int32_t keep) {

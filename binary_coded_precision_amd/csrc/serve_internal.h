@@ -114,6 +114,23 @@ struct AttendArgs {
 hipError_t launch_kv_attend(const AttendArgs &call, float scale, int D, bcq_dtype dt,
                             hipStream_t s);
 
+// Attention of packed tokens (kv_packed.hip); see bcq_kv_attend_packed.
+struct PackedCall {
+  KvView c;
+  const void *q;
+  void *out;
+  KvStrides qs, os;  // token and head
+  const int32_t *starts;
+  int T, q_heads, max_n, shared;  // shared: tokens of the shared pages
+  bool q_wide;                    // 8 channels of q can be read at once
+  void *ws;
+};
+// 0 where the call has more rows than are counted.
+size_t packed_workspace_bytes(int B, int H, int D, int room, int T, int q_heads, int max_n,
+                              bool shared);
+hipError_t launch_kv_attend_packed(const PackedCall &call, float scale, int D, bcq_dtype dt,
+                                   hipStream_t s);
+
 size_t evict_workspace_bytes(int B, int H, int room, int keep);
 hipError_t launch_kv_evict(const KvView &c, int D, int keep, int recent, const float *weights,
                            const int32_t *pos, int32_t *lens_out, float *weights_out,

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 
 BCQ_KV_MAX_TOKENS = 1 << 24
+BCQ_KV_PACKED_MAX_BATCH = 1 << 12
 
 _vp, _i32, _i64, _sz, _int = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                               ctypes.c_int)
@@ -45,6 +46,9 @@ SIGNATURES = {
     "bcq_kv_attend": (_int, [_kc, _vp, _i32, _i32, *_strides, _vp, *_strides, _int,
                              ctypes.c_float, _vp, _vp, _sz, _vp]),
     "bcq_kv_workspace_bytes": (_sz, [_kc, _i32, _i32, _i32]),
+    "bcq_kv_attend_packed": (_int, [_kc, _vp, _i32, _i32, _i64, _i64, _vp, _i32, _i32, _vp, _i64,
+                                    _i64, _int, ctypes.c_float, _vp, _sz, _vp]),
+    "bcq_kv_packed_workspace_bytes": (_sz, [_kc, _i32, _i32, _i32, _i32]),
     "bcq_kv_evict": (_int, [_kc, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "bcq_kv_evict_workspace_bytes": (_sz, [_kc, _i32]),
 }
@@ -550,6 +554,52 @@ def bcq_kv_attend(cache: KVCache, Q, O, scale=None, weights=None, workspace=None
         *_space(workspace, dev), raw)
     if r:
         _fail("bcq_kv_attend", r)
+
+
+def bcq_kv_packed_workspace_bytes(cache: KVCache, T: int, q_heads: int, max_n: int,
+                                  shared_pages: int = 0) -> int:
+    return int(_lib.bcq_kv_packed_workspace_bytes(cache._ref, T, q_heads, max_n, shared_pages))
+
+
+def new_kv_packed_workspace(cache: KVCache, T: int, q_heads: int, max_n: int,
+                            shared_pages: int = 0):
+    """A device workspace for :func:`bcq_kv_attend_packed`; calls that may overlap need separate
+    ones."""
+    return _workspace(bcq_kv_packed_workspace_bytes(cache, T, q_heads, max_n, shared_pages),
+                      cache.lens.device, None)
+
+
+def bcq_kv_attend_packed(cache: KVCache, Q, O, starts, max_n: int, shared_pages: int = 0,
+                         scale=None, workspace=None, stream=None) -> None:
+    """Causal attention of packed tokens ``Q`` [T][q_heads][D], ``starts[b]`` to
+    ``starts[b + 1]`` (int32 [batch + 1]) the last of sequence b and at most ``max_n`` of each,
+    over the cache into ``O`` (same shape).  The first ``shared_pages`` entries of every
+    sequence's table are the same.  ``scale`` defaults to 1/sqrt(D)."""
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
+        return _there(dev, bcq_kv_attend_packed, cache, Q, O, starts, max_n, shared_pages, scale,
+                      workspace, stream)
+    raw = _raw(dev, stream)
+    dt = _float("Q", Q, dev)
+    shape = Q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or O.shape != shape or \
+            O.dtype is not Q.dtype or O.get_device() != dev:
+        raise ValueError("Q and O must be [T][q_heads][%d] of one dtype on the cache's device" %
+                         cache.head_dim)
+    qs, os = Q.stride(), O.stride()
+    if qs[2] != 1 or os[2] != 1:
+        raise ValueError("Q and O must have contiguous channels")
+    if workspace is None:
+        workspace = _workspace(
+            bcq_kv_packed_workspace_bytes(cache, shape[0], shape[1], max_n, shared_pages),
+            Q.device, stream)
+    r = _lib.bcq_kv_attend_packed(
+        cache._ref, Q.data_ptr(), shape[0], shape[1], qs[0], qs[1],
+        _plain("starts", starts, torch.int32, (cache.batch + 1,), dev), max_n, shared_pages,
+        O.data_ptr(), os[0], os[1], dt, shape[2] ** -0.5 if scale is None else scale,
+        *_space(workspace, dev), raw)
+    if r:
+        _fail("bcq_kv_attend_packed", r)
 
 
 def bcq_kv_evict_workspace_bytes(cache: KVCache, keep: int) -> int:

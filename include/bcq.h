@@ -64,6 +64,8 @@ extern "C" {
 #define BCQ_LOWRANK_FUSED_MAX_RANK 1024
 /* Largest number of tokens a sequence's page table may have room for. */
 #define BCQ_KV_MAX_TOKENS (1 << 24)
+/* Largest batch of a cache that bcq_kv_attend_packed takes. */
+#define BCQ_KV_PACKED_MAX_BATCH (1 << 12)
 /* Device scratch held by the library for bcq_gemm_skinny_noalloc, per GPU. */
 #define BCQ_NOALLOC_SCRATCH_BYTES (16u << 20)
 
@@ -660,6 +662,40 @@ bcq_status bcq_kv_attend(const bcq_kv_cache *cache, const void *Q, int32_t n, in
 /* Device workspace of bcq_kv_attend, 0 when none or for an invalid call. */
 size_t bcq_kv_workspace_bytes(const bcq_kv_cache *cache, int32_t n, int32_t q_heads,
                               int32_t with_weights);
+
+/*
+ * Attention of T packed tokens, the last starts[b + 1] - starts[b] of each sequence b,
+ * causal: with n that number, query i of the sequence (token starts[b] + i) sees slots
+ * 0 .. lens[b] - n + i, as in bcq_kv_attend; decode steps, drafted tokens and prompts
+ * in one call.
+ * starts: [batch + 1], not falling, from 0 or more up to at most T, as bcq_kv_reserve
+ *   writes them, read on the device.  Tokens of no sequence are left as they were.
+ * max_n: at least the largest number of tokens that a sequence has.
+ *   Where starts or max_n are not so, outputs are of no meaning, and all that is read
+ *   and written lies in its arrays.
+ * shared_pages: this many first entries are the same in every row of the page table
+ *   (0: none); the rows of sequences with few of them then read these pages together.
+ * Q, O: element (t, head, d) at t*_token + head*_head + d, q_heads heads (a multiple of
+ *   heads), dtype BCQ_F16 or BCQ_F32; O does not overlap Q.  scale: finite.
+ * What is rounded is as in bcq_kv_attend; weights are not summed.
+ * batch is at most BCQ_KV_PACKED_MAX_BATCH, T * q_heads at most 2^28, and the rows
+ * that a cached head's workspace holds (a few times T * q_heads / heads, and in tables
+ * with room past 2^16 tokens that times room / 2^16) fewer than 2^30.
+ * workspace: bcq_kv_packed_workspace_bytes(cache, T, q_heads, max_n, shared_pages)
+ *   bytes, 16-byte aligned, of no account before and after; calls that may run at the
+ *   same time need separate ones.
+ * T = 0 does nothing.  Validation and stream behaviour as in bcq_gemv.
+ */
+bcq_status bcq_kv_attend_packed(const bcq_kv_cache *cache, const void *Q, int32_t T,
+                                int32_t q_heads, int64_t q_token, int64_t q_head,
+                                const int32_t *starts, int32_t max_n, int32_t shared_pages,
+                                void *O, int64_t o_token, int64_t o_head, bcq_dtype dtype,
+                                float scale, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/* Device workspace of bcq_kv_attend_packed, 0 for T = 0 or an invalid call. */
+size_t bcq_kv_packed_workspace_bytes(const bcq_kv_cache *cache, int32_t T, int32_t q_heads,
+                                     int32_t max_n, int32_t shared_pages);
 
 /*
  * Shrinks every sequence longer than `keep` tokens to `keep`, each cached head

@@ -91,3 +91,43 @@ def test_reserve_workspace(lib):
     assert call(lib, "bcq_kv_reserve", RESERVE, bytes=need - 1) == INVALID
     # counted in 64 bits
     assert size(cache(batch=1 << 16, heads=1, page_tokens=16, max_pages=1 << 13)) > 1 << 31
+
+
+ATTEND = dict(cache=cache(), Q=A, T=9, heads=4, qt=1, qh=1, starts=A, max_n=5, shared=1, O=A, ot=1,
+              oh=1, dtype=F16, scale=ctypes.c_float(0.1), workspace=A, bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("change,want", CACHE_BAD + [(dict(batch=(1 << 12) + 1), INVALID)])
+def test_attend_caches(lib, change, want):
+    assert call(lib, "bcq_kv_attend_packed", ATTEND, cache=cache(**change)) == want
+    assert lib.bcq_kv_packed_workspace_bytes(cache(**change), 9, 4, 5, 1) == 0
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(cache=None), INVALID), (dict(T=-1), INVALID), (dict(T=(1 << 24) + 1), INVALID),
+    (dict(heads=0), INVALID), (dict(heads=3), INVALID), (dict(heads=1 << 17), INVALID),
+    (dict(T=1 << 24, heads=32), INVALID), (dict(max_n=0), INVALID), (dict(max_n=-1), INVALID),
+    (dict(shared=-1), INVALID), (dict(shared=5), INVALID), (dict(dtype=0), INVALID),
+    (dict(dtype=3), INVALID), (dict(scale=ctypes.c_float(float("inf"))), INVALID),
+    (dict(scale=ctypes.c_float(float("nan"))), INVALID), (dict(Q=None), INVALID),
+    (dict(O=None), INVALID), (dict(starts=None), INVALID), (dict(Q=A + 1), ALIGNMENT),
+    (dict(O=A + 2, dtype=F32), ALIGNMENT), (dict(starts=A + 2), ALIGNMENT),
+    (dict(workspace=None), INVALID), (dict(bytes=15), INVALID), (dict(workspace=A + 8), ALIGNMENT),
+    # more rows than a workspace counts
+    (dict(T=1 << 22, heads=64, max_n=1 << 22,
+          cache=cache(heads=1, page_tokens=256, max_pages=1 << 15)), INVALID),
+    (dict(T=0, Q=None, starts=None, O=None, workspace=None, bytes=0), OK),
+])
+def test_attend(lib, change, want):
+    assert call(lib, "bcq_kv_attend_packed", ATTEND, **change) == want
+
+
+def test_attend_workspace(lib):
+    size = lib.bcq_kv_packed_workspace_bytes
+    assert size(cache(), 0, 4, 5, 1) == size(cache(), 9, 3, 5, 1) == size(cache(), 9, 4, 0, 0) == 0
+    need = size(cache(), 9, 4, 5, 1)
+    assert need > 0 and need == size(cache(), 9, 4, 5, 2)
+    assert size(cache(), 9, 4, 1 << 30, 1) == size(cache(), 9, 4, 9, 1)  # at most T of one
+    assert call(lib, "bcq_kv_attend_packed", ATTEND, bytes=need - 1) == INVALID
+    # counted in 64 bits
+    assert size(cache(page_tokens=256, max_pages=1 << 13), 1 << 20, 64, 1 << 20, 0) > 1 << 36
