@@ -37,9 +37,18 @@ constexpr int kMaxGroups = (1 << 24) - 1;  // of 256 work items in a launch
 constexpr int kMostParts = 1 << 30;        // partial rows of a cached head
 constexpr int kMostSteps = 2048;  // of 32 tokens, that a wave sums in one go (kv_attend.hip)
 
-// Rows of a wave, tiles of 16 of them.
+// Rows of a wave in a block of many rows, tiles of 16 of them.
 constexpr int wave_tiles(int D) { return D <= 128 ? 2 : 1; }
 constexpr int wave_rows(int D) { return 16 * wave_tiles(D); }
+// Rows up to which blocks have 16 and their waves share the tokens.
+constexpr int kFewRows = 32;
+struct Shape {
+  int blocks, waves;  // waves that share a block's tokens
+};
+template <int U>
+__host__ __device__ constexpr Shape shape_of(int rows) {
+  return rows <= kFewRows ? Shape{(rows + 15) / 16, 4} : Shape{(rows + 4 * U - 1) / (4 * U), 1};
+}
 
 struct PlanHead {
   int items;       // in use
@@ -99,10 +108,10 @@ __device__ __forceinline__ Seq seq_of(const PackedArgs &a, int b, int base) {
   q.len = kv_len(a.c, b);
   q.rows = q.n * a.G;
   q.few = q.n > 0 && q.rows <= 2 * U;
-  q.blocks = q.n == 0 ? 0 : (q.rows + 4 * U - 1) / (4 * U);
+  const Shape shape = shape_of<U>(q.rows);
+  q.blocks = shape.blocks;
   const int tiles = (max(0, q.len - (q.few ? base : 0)) + 31) / 32;
-  const int share = q.rows <= U ? 4 : q.rows <= 2 * U ? 2 : 1;
-  q.steps = (tiles + share - 1) / share;
+  q.steps = (tiles + shape.waves - 1) / shape.waves;
   return q;
 }
 
@@ -163,9 +172,9 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
   // the shared items' shape, as a sequence's
   int few_blocks = 0, few_steps = 0;
   if (together) {
-    const int wt = h.few <= U ? 4 : h.few <= 2 * U ? 2 : 1;
-    few_blocks = (h.few + 4 * U - 1) / (4 * U);
-    few_steps = ((a.shared + 31) / 32 + wt - 1) / wt;
+    const Shape shape = shape_of<U>(h.few);
+    few_blocks = shape.blocks;
+    few_steps = ((a.shared + 31) / 32 + shape.waves - 1) / shape.waves;
   }
   float cost = 0.f;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
@@ -264,64 +273,186 @@ __device__ __forceinline__ void store_out(const PackedArgs &a, int64_t at, float
     static_cast<_Float16 *>(a.out)[at] = (_Float16)x;
 }
 
+// Waves of the same rows meet here.
 template <int D>
 struct Meet {
-  float o[kWaves][wave_rows(D)][D + 4];
-  float m[kWaves][wave_rows(D)], l[kWaves][wave_rows(D)];
+  float o[kWaves][16][D + 4];
+  float m[kWaves][16], l[kWaves][16];
 };
-
-// One item: CT tiles of 16 rows a wave; where rows are few the waves share the tokens.
+// The rows of a wave: the last slot that each lane's sees, and the wave's first and last.
+template <int CT>
+struct Rows {
+  int last[CT], high, low;
+};
 template <int D, int CT, bool F32>
-__device__ __forceinline__ void run(const PackedArgs &a, const Item &x, int base, int h,
-                                    Meet<D> &meet) {
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool shared = x.seq < 0;
-  const int R = x.n * a.G, U = CT * 16;
-  const int WT = R <= U ? 4 : R <= 2 * U ? 2 : 1;
-  const int wr = wave / WT, wt = wave - wr * WT;
-  const int row0 = (x.block * (kWaves / WT) + wr) * U;
-  const int b = shared ? 0 : x.seq, L = x.len;
-  const int t0 = shared || R > 2 * wave_rows(D) ? 0 : base;
-
-  RawQueries<D, CT, F32> raw;
-  int last[CT], token[CT], head[CT];
+__device__ __forceinline__ Rows<CT> rows_of(const PackedArgs &a, const Item &x, int h, int row0,
+                                            int lane, RawQueries<D, CT, F32> &raw) {
+  const int R = x.n * a.G;
+  Rows<CT> r;
   int high = -1, low = INT32_MAX;
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     const int row = min(row0 + ct * 16 + (lane & 15), R - 1);
     const int i = row / a.G;
-    head[ct] = h * a.G + row - i * a.G;
-    if (shared) {
-      token[ct] = a.few[i].token;
-      last[ct] = min(a.few[i].last, L - 1);
-    } else {
-      token[ct] = x.start + i;
-      last[ct] = L - x.n + i;
+    int64_t token = x.start + i;
+    r.last[ct] = x.len - x.n + i;
+    if (x.seq < 0) {
+      const FewToken t = a.few[i];
+      token = t.token;
+      r.last[ct] = min(t.last, x.len - 1);
     }
-    const int64_t at = token[ct] * a.q_token + head[ct] * a.q_head + g * (D / 4);
+    const int64_t at =
+        token * a.q_token + (int64_t)(h * a.G + row - i * a.G) * a.q_head + (lane >> 4) * (D / 4);
     fetch_query<D, CT, F32>(raw, ct, a.q, at, a.q_wide);
-    high = max(high, last[ct]);
-    low = min(low, last[ct]);
+    high = max(high, r.last[ct]);
+    low = min(low, r.last[ct]);
   }
 #pragma unroll
   for (int d = 1; d < 16; d <<= 1) {
     high = max(high, __shfl_xor(high, d));
     low = min(low, __shfl_xor(low, d));
   }
-  high = __builtin_amdgcn_readfirstlane(high);
-  low = __builtin_amdgcn_readfirstlane(low);
-
-  // tiles of 32 tokens of these rows and of this share
-  int tile = 0, tile_end = 0;
-  if (row0 < R) {
-    const int tiles = (max(0, high + 1 - t0) + 31) / 32;
-    // whole rounds of the waves that share the tokens
-    const int rounds = (tiles + WT - 1) / WT, chunk = (rounds + x.shares - 1) / x.shares * WT;
-    tile = x.share * chunk + wt;
-    tile_end = min(tiles, x.share * chunk + chunk);
+  r.high = __builtin_amdgcn_readfirstlane(high);
+  r.low = __builtin_amdgcn_readfirstlane(low);
+  return r;
+}
+template <int D, int CT>
+__device__ __forceinline__ void clear(Sums<D, CT> &A) {
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    A.m[ct] = kNegInf;
+    A.l[ct] = A.z[ct] = 0.f;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) A.o[ct][d] = float4v{0.f, 0.f, 0.f, 0.f};
   }
-  const int free_end = max(0, low + 1 - t0) / 32;  // tiles before it need no mask
+}
+
+// An item of few rows: 16 of them, four waves share the tokens.
+template <int D, bool F32>
+__device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, int base, int h,
+                                        Meet<D> &meet) {
+  int lane = threadIdx.x & 63;
+  // opaque, so that nothing formed from it is kept in registers from item to item
+  asm volatile("" : "+v"(lane));
+  const int g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool shared = x.seq < 0;
+  const int R = x.n * a.G, L = x.len, b = shared ? 0 : x.seq;
+  const int row0 = x.block * 16, t0 = shared ? 0 : base;
+
+  RawQueries<D, 1, F32> raw;
+  const Rows<1> rows = rows_of<D, 1, F32>(a, x, h, row0, lane, raw);
+  // tiles of 32 tokens of these rows and of this share, in whole rounds of the waves
+  const int tiles = (max(0, rows.high + 1 - t0) + 31) / 32;
+  const int rounds = (tiles + kWaves - 1) / kWaves;
+  const int chunk = (rounds + x.shares - 1) / x.shares * kWaves;
+  int tile = x.share * chunk + wave;
+  const int tile_end = min(tiles, x.share * chunk + chunk);
+  const int free_end = max(0, rows.low + 1 - t0) / 32;  // tiles before it need no mask
+  Tiles<D> T;
+  if (tile < tile_end) {
+    const Where w = where(a.c, b, h, t0 + tile * 32, L);
+    load_k(T, a.c, w, lane);
+    load_m(T, a.c, w, lane);
+    load_v(T, a.c, w, lane);
+  }
+  Queries<D, 1, F32> Q;
+  load_queries<D, 1, F32>(Q, raw, a.unit, row0, R, lane);
+  Sums<D, 1> A;
+  clear(A);
+  // the next tiles are asked for as soon as the registers of these are free, and
+  // the place of those after them is looked up a step earlier still
+  auto place_of = [&](int ti) {
+    return where(a.c, b, h, t0 + (ti < tile_end ? ti : tile) * 32, L);
+  };
+  Where ahead{};
+  if (tile < tile_end) ahead = place_of(tile + kWaves);
+  while (tile < tile_end) {
+    const int next = tile + kWaves;
+    const Where w = ahead;
+    ahead = place_of(next + kWaves);
+    float4v S[2][1];
+    scores<D, 1, F32>(S, T, Q, a.code_unit);
+    load_k(T, a.c, w, lane);
+    if (tile >= free_end) mask_scores<D, 1>(S, T, A, t0 + tile * 32 + 4 * g, rows.last);
+    Frag P[1], Plo[1];
+    softmax_tiles<D, 1>(A, P, Plo, S, T);
+    load_m(T, a.c, w, lane);
+    add_values<D, 1, F32>(A, P, Plo, T);
+    load_v(T, a.c, w, lane);
+    tile = next;
+  }
+
+  // the waves' rows are the same: they meet in shared memory, then a wave joins a row
+  A.l[0] = group_sum(A.l[0]);
+  A.z[0] = group_sum(A.z[0]);
+  const int col = lane & 15;
+  if (g == 0) {
+    meet.m[wave][col] = A.m[0];
+    meet.l[wave][col] = A.l[0];
+  }
+  if (row0 + col < R)
+#pragma unroll
+    for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float4v v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(A.o[0][4 * hh + j][i], kCentreScale, A.z[0]);
+        *reinterpret_cast<float4v *>(&meet.o[wave][col][64 * hh + 16 * g + 4 * i]) = v;
+      }
+  __syncthreads();
+  const int64_t part0 = (int64_t)h * a.part_cap + x.part + (int64_t)x.share * R;
+  for (int c = wave; c < 16 && row0 + c < R; c += kWaves) {
+    const int row = row0 + c;
+    const float mw = lane < kWaves ? meet.m[lane][c] : kNegInf;
+    float m = mw;
+#pragma unroll
+    for (int d = 1; d < kWaves; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float f = mw == kNegInf ? 0.f : exp2f(mw - m);
+    float l = lane < kWaves ? f * meet.l[lane][c] : 0.f;
+#pragma unroll
+    for (int d = 1; d < kWaves; d <<= 1) l += __shfl_xor(l, d);
+    m = __shfl(m, 0);
+    l = __shfl(l, 0);
+    const int i = row / a.G;
+    const int64_t at = (x.start + i) * a.o_token + (int64_t)(h * a.G + row - i * a.G) * a.o_head;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) o += __shfl(f, w) * meet.o[w][c][e * 64 + lane];
+      if (x.part < 0)
+        store_out(a, at + e * 64 + lane, l == 0.f ? 0.f : o / l, F32);
+      else
+        a.o[(part0 + row) * D + e * 64 + lane] = o;
+    }
+    if (lane == 0 && x.part >= 0) a.ml[part0 + row] = make_float2(m, l);
+  }
+}
+
+// An item of many rows: every wave has rows of its own.
+template <int D, bool F32>
+__device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, int base, int h) {
+  constexpr int CT = wave_tiles(D), U = wave_rows(D);
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // as in run_few
+  const int g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool shared = x.seq < 0;
+  const int R = x.n * a.G, L = x.len, b = shared ? 0 : x.seq;
+  const int row0 = (x.block * kWaves + wave) * U;
+  if (row0 >= R) return;
+  const int t0 = shared || R > 2 * U ? 0 : base;
+
+  RawQueries<D, CT, F32> raw;
+  const Rows<CT> rows = rows_of<D, CT, F32>(a, x, h, row0, lane, raw);
+  // tiles of 32 tokens of the wave's rows and of this share
+  const int tiles = (max(0, rows.high + 1 - t0) + 31) / 32;
+  const int chunk = (tiles + x.shares - 1) / x.shares;
+  int tile = x.share * chunk;
+  const int tile_end = min(tiles, tile + chunk);
+  const int free_end = max(0, rows.low + 1 - t0) / 32;
   Tiles<D> T;
   if (tile < tile_end) {
     const Where w = where(a.c, b, h, t0 + tile * 32, L);
@@ -332,121 +463,55 @@ __device__ __forceinline__ void run(const PackedArgs &a, const Item &x, int base
   Queries<D, CT, F32> Q;
   load_queries<D, CT, F32>(Q, raw, a.unit, row0, R, lane);
   Sums<D, CT> A;
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    A.m[ct] = kNegInf;
-    A.l[ct] = A.z[ct] = 0.f;
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) A.o[ct][d] = float4v{0.f, 0.f, 0.f, 0.f};
-  }
-  // the next tiles are asked for as soon as the registers of these are free, and
-  // the place of those after them is looked up a step earlier still
+  clear(A);
   auto place_of = [&](int ti) {
     return where(a.c, b, h, t0 + (ti < tile_end ? ti : tile) * 32, L);
   };
   Where ahead{};
-  if (tile < tile_end) ahead = place_of(tile + WT);
-  while (tile < tile_end) {
-    const int next = tile + WT;
+  if (tile < tile_end) ahead = place_of(tile + 1);
+  for (; tile < tile_end; ++tile) {
     const Where w = ahead;
-    ahead = place_of(next + WT);
+    ahead = place_of(tile + 2);
     float4v S[2][CT];
     scores<D, CT, F32>(S, T, Q, a.code_unit);
     load_k(T, a.c, w, lane);
-    if (tile >= free_end) mask_scores<D, CT>(S, T, A, t0 + tile * 32 + 4 * g, last);
+    if (tile >= free_end) mask_scores<D, CT>(S, T, A, t0 + tile * 32 + 4 * g, rows.last);
     Frag P[CT], Plo[CT];
     softmax_tiles<D, CT>(A, P, Plo, S, T);
     load_m(T, a.c, w, lane);
     add_values<D, CT, F32>(A, P, Plo, T);
     load_v(T, a.c, w, lane);
-    tile = next;
   }
 
-  // a row's sums over its four lanes; the zeros added to the outputs
+  asm volatile("" : "+v"(lane));  // nothing of the outputs' places is kept over the loop
+  const int64_t part0 = (int64_t)h * a.part_cap + x.part + (int64_t)x.share * R;
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
+    // a row's sums over its four lanes; the zeros added to the outputs
     A.l[ct] = group_sum(A.l[ct]);
     A.z[ct] = group_sum(A.z[ct]);
+    const int row = row0 + ct * 16 + (lane & 15);
+    if (row >= R) continue;
+    if (g == 0 && x.part >= 0) a.ml[part0 + row] = make_float2(A.m[ct], A.l[ct]);
+    const int i = row / a.G;
+    const int64_t at = (x.start + i) * a.o_token + (int64_t)(h * a.G + row - i * a.G) * a.o_head;
+    const float inv = A.l[ct] == 0.f ? 0.f : 1.f / A.l[ct];
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d)
+    for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        A.o[ct][d][i] = fmaf(A.o[ct][d][i], kCentreScale, A.z[ct]);
-  }
-  const int64_t part0 = (int64_t)h * a.part_cap + x.part + (int64_t)x.share * R;
-
-  if (WT > 1) {
-    // waves of the same rows meet in shared memory, then one joins a row
+      for (int i = 0; i < 4; ++i) {
+        const int d = 64 * hh + 16 * g + 4 * i;
+        float4v v;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const int col = ct * 16 + (lane & 15);
-      if (g == 0) {
-        meet.m[wave][col] = A.m[ct];
-        meet.l[wave][col] = A.l[ct];
-      }
-      if (row0 + col < R)
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(A.o[ct][4 * hh + j][i], kCentreScale, A.z[ct]);
+        if (x.part >= 0) {
+          *reinterpret_cast<float4v *>(&a.o[(part0 + row) * D + d]) = v;
+        } else {
 #pragma unroll
-        for (int hh = 0; hh < D / 64; ++hh)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4v v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = A.o[ct][4 * hh + j][i];
-            *reinterpret_cast<float4v *>(&meet.o[wave][col][64 * hh + 16 * g + 4 * i]) = v;
-          }
-    }
-    __syncthreads();
-    const int first = wr * WT;
-    for (int col = wt; col < U && row0 + col < R; col += WT) {
-      const int row = row0 + col;
-      const float mw = lane < WT ? meet.m[first + lane][col] : kNegInf;
-      float m = mw;
-#pragma unroll
-      for (int d = 1; d < kWaves; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-      const float f = mw == kNegInf ? 0.f : exp2f(mw - m);
-      float l = lane < WT ? f * meet.l[first + lane][col] : 0.f;
-#pragma unroll
-      for (int d = 1; d < kWaves; d <<= 1) l += __shfl_xor(l, d);
-      m = __shfl(m, 0);
-      l = __shfl(l, 0);
-      const int i = row / a.G;
-      const int64_t at = (x.start + i) * a.o_token + (int64_t)(h * a.G + row - i * a.G) * a.o_head;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        float o = 0.f;
-        for (int w = 0; w < WT; ++w) o += __shfl(f, w) * meet.o[first + w][col][c * 64 + lane];
-        if (x.part < 0)
-          store_out(a, at + c * 64 + lane, l == 0.f ? 0.f : o / l, F32);
-        else
-          a.o[(part0 + row) * D + c * 64 + lane] = o;
-      }
-      if (lane == 0 && x.part >= 0) a.ml[part0 + row] = make_float2(m, l);
-    }
-  } else {
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const int row = row0 + ct * 16 + (lane & 15);
-      if (row >= R) continue;
-      if (g == 0 && x.part >= 0) a.ml[part0 + row] = make_float2(A.m[ct], A.l[ct]);
-      const int64_t at = token[ct] * a.o_token + head[ct] * a.o_head;
-      const float inv = A.l[ct] == 0.f ? 0.f : 1.f / A.l[ct];
-#pragma unroll
-      for (int hh = 0; hh < D / 64; ++hh)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = 64 * hh + 16 * g + 4 * i;
-          float4v v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = A.o[ct][4 * hh + j][i];
-          if (x.part >= 0) {
-            *reinterpret_cast<float4v *>(&a.o[(part0 + row) * D + d]) = v;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              store_out(a, at + d + j, A.l[ct] == 0.f ? 0.f : v[j] * inv, F32);
-          }
+          for (int j = 0; j < 4; ++j)
+            store_out(a, at + d + j, A.l[ct] == 0.f ? 0.f : v[j] * inv, F32);
         }
-    }
+      }
   }
 }
 
@@ -457,10 +522,10 @@ __global__ __launch_bounds__(kThreads, 2) void packed_kernel(PackedArgs a) {
   // a launch has a workgroup for each item but where their number passes its limit
   for (int i = blockIdx.x / a.c.H; i < items; i += gridDim.x / a.c.H) {
     const Item x = a.items[i];
-    if (x.n * a.G <= 16)
-      run<D, 1, F32>(a, x, base, h, meet);
+    if (x.n * a.G <= kFewRows)
+      run_few<D, F32>(a, x, base, h, meet);
     else
-      run<D, wave_tiles(D), F32>(a, x, base, h, meet);
+      run_many<D, F32>(a, x, base, h);
     __syncthreads();  // meet is written again
   }
 }
@@ -552,17 +617,19 @@ PackedPlan packed_plan(int B, int H, int D, int room, int T, int q_heads, int ma
   const int64_t G = q_heads / H, U = wave_rows(D), block = 4 * U;
   const int64_t seqs = std::min(B, T), rows = (int64_t)T * G;
   const int64_t few = std::min<int64_t>(T, seqs * (2 * U / G));
-  const int64_t blocks = rows / block + seqs;
-  const int64_t few_blocks = shared ? (few * G + block - 1) / block : 0;
+  const int64_t blocks = rows / block + 2 * seqs;  // two of up to kFewRows rows
+  const int64_t few_blocks = shared ? few * G / block + 2 : 0;
   const int64_t target = kTarget / H + 1, past = room / (32 * kMostSteps) + 1;
   PackedPlan p;
   p.item_cap = (int)std::min<int64_t>(target + (blocks + few_blocks) * past, 1 << 30);
   p.few_cap = (int)std::max<int64_t>(few, 1);
   // rows of all the shares: a block's has at most `most`; blocks with one share have
   // none but those that meet the shared pages
-  const int64_t most = std::min<int64_t>(block, (int64_t)max_n * G);
+  const int64_t most = std::min<int64_t>((int64_t)max_n * G <= kFewRows ? 16 : block,
+                                         (int64_t)max_n * G);
   const int64_t own = std::min(target * most + rows, 2 * target * most + (shared ? few * G : 0));
-  const int64_t met = shared ? target * std::min(block, few * G) + few * G : 0;
+  const int64_t met =
+      shared ? target * std::min<int64_t>(few * G <= kFewRows ? 16 : block, few * G) + few * G : 0;
   p.part_cap = past == 1 ? own + met
                          : std::max(own, rows * past) + std::max(met, shared ? few * G * past : 0);
   size_t at = 256;

@@ -151,15 +151,17 @@ __device__ __forceinline__ half2v pair_of(uint32_t w) {
 // which fp16 does not hold of queries below 2^-10, and the matrix cores keep
 // fewer bits of a product with a smaller subnormal (measured: 1e-6 of a sum of 32
 // products with c * 2^-24, 2e-8 with c * 2^-20).
-template <int D>
-__device__ __forceinline__ half8 k_frag(const Tiles<D> &t, int s, int w) {
-  const uint32_t x = t.k[s][w];
+__device__ __forceinline__ half8 code_frag(uint32_t x) {
   Frag f;
   f.w[0] = (x << 4) & 0x00f000f0u;
   f.w[1] = x & 0x00f000f0u;
   f.w[2] = (x >> 4) & 0x00f000f0u;
   f.w[3] = (x >> 8) & 0x00f000f0u;
   return f.h;
+}
+template <int D>
+__device__ __forceinline__ half8 k_frag(const Tiles<D> &t, int s, int w) {
+  return code_frag(t.k[s][w]);
 }
 
 // (code - 7.5) / 512 of two tokens, the low (N = 0) or high nibbles of the bytes
@@ -402,6 +404,29 @@ __device__ __forceinline__ half2v cut(float a, float b) {
   return __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_pkrtz(a, b));
 }
 
+// Raises the reference of the row of tile ct where its largest term z asks for it (each
+// row by its own scores, so that no row depends on its neighbours) and rescales; `high`
+// is the largest score of the lane.
+template <int D, int CT>
+__device__ __forceinline__ void raise_row(Sums<D, CT> &A, int ct, float z, float high) {
+  float m = z > A.m[ct] + (kRaise + kSlack) ? z - kRaise : A.m[ct];
+  // Scores so large that such sums are rounded to units and more: the largest
+  // itself is the reference.  Terms are then at most the V scales.
+  const bool vast = fabsf(z) >= 0x1p22f && fabsf(z) < INFINITY;
+  if (__any(vast)) {
+    const float most = group_max(high);
+    m = vast ? fmaxf(A.m[ct], most) : m;
+  }
+  const float f = m == A.m[ct] ? 1.f : exp2f(A.m[ct] - m);
+  A.m[ct] = m;
+  A.l[ct] *= f;
+  A.z[ct] *= f;
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A.o[ct][d][i] *= f;
+}
+
 // The softmax's step over 32 tokens: raises the rows' references, rescales, adds
 // to their sums and leaves probability times V scale in P, what that rounds off in
 // Plo.
@@ -435,24 +460,7 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Fra
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           top = fmaxf(top, S[s][ct][i] + rough_log2(T.m[s][2 * i + 1] & 0xffffu));
-      // each row by its own scores, so that no row depends on its neighbours
-      const float z = group_max(top);
-      float m = z > A.m[ct] + (kRaise + kSlack) ? z - kRaise : A.m[ct];
-      // Scores so large that such sums are rounded to units and more: the largest
-      // itself is the reference.  Terms are then at most the V scales.
-      const bool vast = fabsf(z) >= 0x1p22f && fabsf(z) < INFINITY;
-      if (__any(vast)) {
-        const float most = group_max(high[ct]);
-        m = vast ? fmaxf(A.m[ct], most) : m;
-      }
-      const float f = m == A.m[ct] ? 1.f : exp2f(A.m[ct] - m);
-      A.m[ct] = m;
-      A.l[ct] *= f;
-      A.z[ct] *= f;
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) A.o[ct][d][i] *= f;
+      raise_row(A, ct, group_max(top), high[ct]);
     }
   }
   // a row that has seen nothing yet has no reference; its terms are 2^-inf
@@ -488,6 +496,35 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Fra
     }
 }
 
+// Channels 64hh .. 64hh + 63 of the outputs, from 32 tokens' V by the channel's place in
+// its four.
+template <int D, int CT, bool F32>
+__device__ __forceinline__ void add_block(Sums<D, CT> &A, const Frag (&P)[CT],
+                                          const Frag (&Plo)[CT], const half8 (&vf)[4], int hh) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float4v x = {0.f, 0.f, 0.f, 0.f};
+        x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct].h, x, 0, 0, 0);
+        A.o[ct][4 * hh + j] += __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct].h, x, 0, 0, 0);
+      }
+  } else {
+    // no product waits for the one before it
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float4v &o = A.o[ct][4 * hh + j];
+          const half8 p = part ? P[ct].h : Plo[ct].h;
+          o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], p, o, 0, 0, 0);
+        }
+  }
+}
+
 template <int D, int CT, bool F32>
 __device__ __forceinline__ void add_values(Sums<D, CT> &A, const Frag (&P)[CT],
                                            const Frag (&Plo)[CT], const Tiles<D> &T) {
@@ -501,29 +538,7 @@ __device__ __forceinline__ void add_values(Sums<D, CT> &A, const Frag (&P)[CT],
 #pragma unroll
       for (int j = 0; j < 4; ++j) vf[j][2 * e] = x[j][0], vf[j][2 * e + 1] = x[j][1];
     }
-    if constexpr (F32) {
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float4v x = {0.f, 0.f, 0.f, 0.f};
-          x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct].h, x, 0, 0, 0);
-          A.o[ct][4 * hh + j] +=
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct].h, x, 0, 0, 0);
-        }
-    } else {
-      // no product waits for the one before it
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float4v &o = A.o[ct][4 * hh + j];
-            const half8 p = part ? P[ct].h : Plo[ct].h;
-            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], p, o, 0, 0, 0);
-          }
-    }
+    add_block<D, CT, F32>(A, P, Plo, vf, hh);
   }
 }
 
