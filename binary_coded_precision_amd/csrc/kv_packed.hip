@@ -2,14 +2,14 @@
 // over the 4-bit key/value cache (bcq_kv_attend_packed); the mathematics and a
 // wave's steps are in kv_tiles.h.
 //
-// What a call has to do is known on the device only (starts, lengths), so a first
-// kernel of one workgroup cuts it into items, one a workgroup and cached head:
+// What a call has to do is known on the device only (starts, lengths).  It is cut into
+// items, one for a workgroup and cached head:
 //
 //  - A sequence's rows (its tokens, times the query heads of a cached head) are
-//    blocks of up to four waves' rows.  Where one wave or two hold them all, the
-//    waves share the tokens instead.
-//  - Its tokens are cut into `ns` shares, so that all items together are about as
-//    many as the card holds and none is longer than the others' average asks for.
+//    blocks of four waves' rows.  Where they are few, a block has 16 and its waves
+//    share the tokens instead.
+//  - Its tokens are cut into shares, so that all items together are about as many as
+//    the card holds and none is much longer than the others.
 //  - Rows of sequences with few of them (decode steps, drafted tokens) all meet the
 //    shared pages together, as the rows of one sequence: those pages are read
 //    once, and up to 128 rows share the unpacking of their codes.  The sequences'
@@ -18,6 +18,9 @@
 //
 // Shares leave sums and outputs before the division, which a last kernel joins; what
 // has one share only is written at once.
+//
+// Up to 64 sequences every wave works all that out by itself, a sequence a lane (a
+// kernel for it took 6 us of a small call's 18); for more a first kernel writes it down.
 #include <algorithm>
 
 #include "kv_tiles.h"
@@ -32,7 +35,6 @@ constexpr int kMaxShares = 64;  // of a row, one a lane where they are joined
 // Workgroups that a call is cut into when there is enough to do: two a compute unit,
 // as many as their registers leave room for.
 constexpr int kTarget = 512;
-constexpr int kLeastSteps = 1;
 constexpr int kMaxGroups = (1 << 24) - 1;  // of 256 work items in a launch
 constexpr int kMostParts = 1 << 30;        // partial rows of a cached head
 constexpr int kMostSteps = 2048;  // of 32 tokens, that a wave sums in one go (kv_attend.hip)
@@ -43,19 +45,20 @@ constexpr int wave_rows(int D) { return 16 * wave_tiles(D); }
 // Rows up to which blocks have 16 and their waves share the tokens.
 constexpr int kFewRows = 32;
 struct Shape {
-  int blocks, waves;  // waves that share a block's tokens
+  int blocks, waves, weight;  // waves that share a block's tokens; weight of a step
 };
 template <int U>
 __host__ __device__ constexpr Shape shape_of(int rows) {
-  return rows <= kFewRows ? Shape{(rows + 15) / 16, 4} : Shape{(rows + 4 * U - 1) / (4 * U), 1};
+  return rows <= kFewRows ? Shape{(rows + 15) / 16, 4, 1}
+                          : Shape{(rows + 4 * U - 1) / (4 * U), 1, U / 16};
 }
 
 struct PlanHead {
-  int items;       // in use
+  int items;       // in use, the shared pages' first
+  int few_items;   // those
   int base;        // tokens that sequences with few rows leave to the shared items
-  int few;         // such rows
+  int few;         // such sequences' tokens
   int few_shares;  // of the shared pages
-  int few_at;      // their partial rows
   int split;       // rows of the sequences of many rows that are to be joined
   int splits;      // such sequences
 };
@@ -71,9 +74,14 @@ struct FewToken {
   int rows_shares;  // rows of the sequence << 8 | own shares
 };
 struct SplitSeq {
-  int row, seq;  // rows before it; the sequence
+  int row;  // rows before it
   int start, n, part, shares;
 };
+// What a row of the shared items needs to know of its token.
+struct Listed {
+  int token, last;
+};
+constexpr int kListed = 130;  // tokens that a block's rows belong to, at most
 
 struct PackedArgs {
   KvView c;
@@ -94,37 +102,196 @@ struct PackedArgs {
 };
 
 struct Seq {
-  int start, n, len, rows, blocks, steps;
+  int start, n, len, rows, blocks, steps, weight;
   bool few;
 };
-// U: rows of a wave; base: tokens that sequences with few rows do not walk.
+// U: rows of a wave.
 template <int U>
-__device__ __forceinline__ Seq seq_of(const PackedArgs &a, int b, int base) {
+__device__ __forceinline__ Seq seq_of(const PackedArgs &a, int start, int end, int len) {
   Seq q{};
-  if (b >= a.c.B) return q;
-  const int s0 = min(max(a.starts[b], 0), a.T), s1 = min(max(a.starts[b + 1], 0), a.T);
-  q.start = s0;
-  q.n = min(max(s1 - s0, 0), a.max_n);
-  q.len = kv_len(a.c, b);
+  q.start = min(max(start, 0), a.T);
+  q.n = min(max(min(max(end, 0), a.T) - q.start, 0), a.max_n);
+  q.len = len;
   q.rows = q.n * a.G;
   q.few = q.n > 0 && q.rows <= 2 * U;
-  const Shape shape = shape_of<U>(q.rows);
-  q.blocks = shape.blocks;
-  const int tiles = (max(0, q.len - (q.few ? base : 0)) + 31) / 32;
-  q.steps = (tiles + shape.waves - 1) / shape.waves;
   return q;
 }
+template <int U>
+__device__ __forceinline__ Seq seq_at(const PackedArgs &a, int b) {
+  if (b >= a.c.B) return Seq{};
+  return seq_of<U>(a, a.starts[b], a.starts[b + 1], kv_len(a.c, b));
+}
+// Blocks and their steps, of 32 tokens for each wave; base: tokens that sequences with few
+// rows do not walk.
+template <int U>
+__device__ __forceinline__ void shape(Seq &q, int base) {
+  const Shape s = shape_of<U>(q.rows);
+  const int tiles = (max(0, q.len - (q.few ? base : 0)) + 31) / 32;
+  q.blocks = s.blocks;
+  q.steps = (tiles + s.waves - 1) / s.waves;
+  q.weight = s.weight;
+}
 
-__device__ __forceinline__ int capped(int a, int b) { return min(a + b, 1 << 30); }
-// Inclusive sum over the workgroup and the sum of all, each up to 2^30.
-__device__ __forceinline__ int2 scan(int x, int *part) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x = capped(x, y);
+// Sums stop at 2^30: starts that are none could pass 32 bits.
+__device__ __forceinline__ int capped(int a, int b) {
+  return (int)min((unsigned)a + (unsigned)b, 1u << 30);
+}
+__device__ __forceinline__ int product(int a, int b) {
+  return (int)min((int64_t)a * b, (int64_t)1 << 30);
+}
+
+// Lengths are cut by chunk: the steps' weight that a share should have.
+__device__ __forceinline__ int chunk_of(const PackedArgs &a, float cost) {
+  return max(1, (int)fminf(ceilf(cost * (float)a.c.H * (1.f / kTarget)), (float)(1 << 24)));
+}
+__device__ __forceinline__ int shares_of(int steps, int weight, int chunk, int most) {
+  const int by_chunk = (steps * weight + chunk - 1) / chunk;
+  return min(max(max(by_chunk, (steps + kMostSteps - 1) / kMostSteps), 1), most);
+}
+
+// What the whole call is: the first part of a plan, from the sums over the sequences.
+template <int U>
+struct Whole {
+  PlanHead h{};
+  bool together;
+  int few_blocks = 0, few_steps = 0, few_weight = 0, chunk, most, used = 0;
+
+  // sequences with few rows, and their tokens
+  __device__ __forceinline__ Whole(const PackedArgs &a, int seqs, int tokens) {
+    together = a.shared > 0 && seqs > 1 && tokens <= a.few_cap;
+    h.base = together ? a.shared : 0;
+    h.few = min(tokens, a.few_cap);
+    if (together) {
+      const Shape shape = shape_of<U>(h.few * a.G);
+      few_blocks = shape.blocks;
+      few_steps = ((a.shared + 31) / 32 + shape.waves - 1) / shape.waves;
+      few_weight = shape.weight;
+    }
+    most = together ? kMaxShares / 2 : kMaxShares;
   }
-  if (lane == 63) part[wave] = x;
+  // the weight of all the sequences' own steps
+  __device__ __forceinline__ void divide(const PackedArgs &a, float cost) {
+    cost += (float)few_blocks * (float)few_steps * (float)few_weight;
+    chunk = chunk_of(a, cost);
+    if (!together) return;
+    h.few_shares = shares_of(few_steps, few_weight, chunk, most);
+    if ((int64_t)h.few_shares * h.few * a.G > a.part_cap) h.few_shares = 0;
+    used = h.few_shares * h.few * a.G;
+    h.few_items = few_blocks * h.few_shares;
+  }
+  // shares of a sequence's blocks, and the partial rows that they leave
+  __device__ __forceinline__ int shares(const Seq &q) const {
+    if (q.blocks == 0 || (together && q.few && q.steps == 0)) return 0;
+    return shares_of(q.steps, q.weight, chunk, most);
+  }
+  __device__ __forceinline__ int rows(const Seq &q, int shares) const {
+    return shares > 1 || (together && q.few) ? product(q.rows, shares) : 0;
+  }
+  __device__ __forceinline__ Item few_item(const PackedArgs &a, int i) const {
+    return few_item(a, h, i);
+  }
+  // shares of one block are neighbours
+  static __device__ __forceinline__ Item few_item(const PackedArgs &a, const PlanHead &h, int i) {
+    return Item{-1, i / h.few_shares, i % h.few_shares, h.few_shares, 0, h.few, a.shared, 0};
+  }
+};
+// Item j of a sequence: the last rows, which see the most, first.
+__device__ __forceinline__ void pick(Item &x, int blocks, int j) {
+  x.block = blocks - 1 - j / x.shares;
+  x.share = j % x.shares;
+}
+
+// ---- up to 64 sequences, one a lane
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int moved(int x) {  // 0 where nothing is moved to
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int lane_scan(int x) {
+  x = capped(x, moved<0x111, 0xf>(x));  // within 16 lanes
+  x = capped(x, moved<0x112, 0xf>(x));
+  x = capped(x, moved<0x114, 0xf>(x));
+  x = capped(x, moved<0x118, 0xf>(x));
+  x = capped(x, moved<0x142, 0xa>(x));  // the rows before
+  return capped(x, moved<0x143, 0xc>(x));
+}
+__device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, 63); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float x) {
+  return __int_as_float(moved<CTRL, ROWS>(__float_as_int(x)));
+}
+__device__ __forceinline__ float lane_sum(float x) {
+  x += moved<0x111, 0xf>(x);
+  x += moved<0x112, 0xf>(x);
+  x += moved<0x114, 0xf>(x);
+  x += moved<0x118, 0xf>(x);
+  x += moved<0x142, 0xa>(x);
+  x += moved<0x143, 0xc>(x);
+  return __int_as_float(last_lane(__float_as_int(x)));
+}
+
+struct LanePlan {
+  PlanHead h;
+  Seq q;  // the lane's sequence
+  int shares, part, item, few, split;  // partial rows, items, few tokens, split rows before it
+  bool many;                           // its rows are split ones
+};
+template <int U>
+__device__ __forceinline__ LanePlan lane_plan(const PackedArgs &a, int lane) {
+  LanePlan p;
+  p.q = seq_at<U>(a, lane);
+  const int few = lane_scan(p.q.few ? p.q.n : 0);
+  Whole<U> whole(a, __popcll(__ballot(p.q.few)), last_lane(few));
+  shape<U>(p.q, whole.h.base);
+  whole.divide(a, lane_sum((float)p.q.blocks * (float)p.q.steps * (float)p.q.weight));
+  p.shares = whole.shares(p.q);
+  const int rows = whole.rows(p.q, p.shares), end = capped(whole.used, lane_scan(rows));
+  if (rows > 0 && end > a.part_cap) p.shares = 0;  // starts that are none
+  p.part = rows > 0 && p.shares > 0 ? end - rows : -1;
+  p.few = few - (p.q.few ? p.q.n : 0);
+  p.many = p.shares > 1 && !p.q.few;
+  const int split = lane_scan(p.many ? p.q.rows : 0), items = product(p.q.blocks, p.shares);
+  p.split = split - (p.many ? p.q.rows : 0);
+  const int total = lane_scan(items);
+  p.item = total - items;
+  if (__ballot(p.q.n > 0 && !p.q.few)) {
+    // the longest sequences' items first, as workgroups are handed out in order
+    p.item = 0;
+    for (int j = 0; j < a.c.B; ++j) {
+      const int steps = __builtin_amdgcn_readlane(p.q.steps, j);
+      const int theirs = __builtin_amdgcn_readlane(items, j);
+      const bool before = steps > p.q.steps || (steps == p.q.steps && j < lane);
+      p.item = capped(p.item, before ? theirs : 0);
+    }
+  }
+  p.item = capped(p.item, whole.h.few_items);
+  p.h = whole.h;
+  p.h.items = min(capped(last_lane(total), whole.h.few_items), a.item_cap);
+  p.h.split = last_lane(split);
+  return p;
+}
+// Item i, below p.h.items (one without rows where it is nobody's).
+template <int U>
+__device__ __forceinline__ Item lane_item(const PackedArgs &a, const LanePlan &p, int i) {
+  if (i < p.h.few_items) return Whole<U>::few_item(a, p.h, i);
+  const int items = product(p.q.blocks, p.shares);
+  const uint64_t whose = __ballot(i >= p.item && i - p.item < items);
+  if (whose == 0) return Item{};
+  const int b = __builtin_ctzll(whose);
+  const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, b); };
+  Item x{b, 0, 0, of(p.shares), of(p.q.start), of(p.q.n), of(p.q.len), of(p.part)};
+  pick(x, of(p.q.blocks), i - of(p.item));
+  return x;
+}
+
+// ---- more sequences
+
+// Inclusive sum over the workgroup and the sum of all.
+__device__ __forceinline__ int2 scan(int x, int *part) {
+  const int wave = threadIdx.x >> 6;
+  x = lane_scan(x);
+  if ((threadIdx.x & 63) == 63) part[wave] = x;
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
@@ -137,8 +304,7 @@ __device__ __forceinline__ int2 scan(int x, int *part) {
   return make_int2(capped(x, before), all);
 }
 __device__ __forceinline__ float sum_of(float x, float *part) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+  x = lane_sum(x);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
   __syncthreads();
   x = (part[0] + part[1]) + (part[2] + part[3]);
@@ -146,96 +312,53 @@ __device__ __forceinline__ float sum_of(float x, float *part) {
   return x;
 }
 
-__device__ __forceinline__ int shares_of(int steps, int chunk, int most) {
-  return min(max((steps + chunk - 1) / chunk, 1), most);
-}
-
 template <int U>
 __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
   __shared__ int part[kWaves];
   __shared__ float partf[kWaves];
-  __shared__ int offset[BCQ_KV_PACKED_MAX_BATCH + 1];  // of a sequence's items, in order
-  __shared__ uint16_t order[BCQ_KV_PACKED_MAX_BATCH];
+  __shared__ int offset[BCQ_KV_PACKED_MAX_BATCH];  // of a sequence's items
   const int tid = threadIdx.x, B = a.c.B;
-  // tokens of sequences with few rows
   int seqs = 0, tokens = 0;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
-    const Seq q = seq_of<U>(a, b0 + tid, 0);
+    const Seq q = seq_at<U>(a, b0 + tid);
     seqs += scan(q.few, part).y;
     tokens = capped(tokens, scan(q.few ? q.n : 0, part).y);
   }
-  PlanHead h{};
-  const bool together = a.shared > 0 && seqs > 1 && tokens <= a.few_cap;
-  h.base = together ? a.shared : 0;
-  tokens = min(tokens, a.few_cap);
-  h.few = tokens * a.G;
-  // the shared items' shape, as a sequence's
-  int few_blocks = 0, few_steps = 0;
-  if (together) {
-    const Shape shape = shape_of<U>(h.few);
-    few_blocks = shape.blocks;
-    few_steps = ((a.shared + 31) / 32 + shape.waves - 1) / shape.waves;
-  }
+  Whole<U> whole(a, seqs, tokens);
   float cost = 0.f;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
-    const Seq q = seq_of<U>(a, b0 + tid, h.base);
-    cost += sum_of((float)q.blocks * (float)q.steps, partf);
+    Seq q = seq_at<U>(a, b0 + tid);
+    shape<U>(q, whole.h.base);
+    cost += sum_of((float)q.blocks * (float)q.steps * (float)q.weight, partf);
   }
-  cost += (float)few_blocks * (float)few_steps;
-  const int chunk = max(
-      kLeastSteps, (int)fminf(ceilf(cost * (float)a.c.H * (1.f / kTarget)), (float)kMostSteps));
-  const int most = together ? kMaxShares / 2 : kMaxShares;
-  int used = 0;  // partial rows
-  if (together) {
-    h.few_shares = shares_of(few_steps, chunk, most);
-    if ((int64_t)h.few_shares * h.few > a.part_cap) h.few_shares = 0;
-    used = h.few_shares * h.few;
-  }
-  int items = few_blocks * h.few_shares;
-  const int few_items = items;
-  // the longest sequences' items first, as workgroups are handed out in order
-  if (B <= kThreads) {
-    const Seq q = seq_of<U>(a, tid, h.base);
-    offset[tid] = tid < B ? q.steps : -1;
-    __syncthreads();
-    int rank = 0;
-    for (int j = 0; j < B; ++j) rank += offset[j] > q.steps || (offset[j] == q.steps && j < tid);
-    if (tid < B) order[rank] = (uint16_t)tid;
-  } else {
-    for (int b = tid; b < B; b += kThreads) order[b] = (uint16_t)b;
-  }
-  __syncthreads();
-  int few_before = 0, split = 0, splits = 0;
-  for (int r0 = 0; r0 < B; r0 += kThreads) {
-    const int r = r0 + tid, b = r < B ? order[r] : B;
-    const Seq q = seq_of<U>(a, b, h.base);
-    const bool joined = together && q.few;
-    int shares = q.blocks == 0 ? 0 : shares_of(q.steps, chunk, most);
-    if (joined && q.steps == 0) shares = 0;
-    const bool parts = shares > 1 || (joined && shares > 0);
-    const int rows = parts ? (int)min((int64_t)q.rows * shares, (int64_t)1 << 30) : 0;
+  whole.divide(a, cost);
+  int used = whole.used, items = whole.h.few_items, few_before = 0, split = 0, splits = 0;
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
+    const int b = b0 + tid;
+    Seq q = seq_at<U>(a, b);
+    shape<U>(q, whole.h.base);
+    int shares = whole.shares(q);
+    const int rows = whole.rows(q, shares);
     const int2 pr = scan(rows, part);
-    const int at = capped(used, pr.x) - rows;
-    if (parts && capped(used, pr.x) > a.part_cap) shares = 0;  // starts that are none
-    const int2 it = scan((int)min((int64_t)q.blocks * shares, (int64_t)1 << 30), part);
-    const int2 fw = scan(q.few ? q.n : 0, part);
+    const int end = capped(used, pr.x);
+    if (rows > 0 && end > a.part_cap) shares = 0;  // starts that are none
+    const int at = rows > 0 && shares > 0 ? end - rows : -1, mine = product(q.blocks, shares);
+    const int2 it = scan(mine, part), fw = scan(q.few ? q.n : 0, part);
     const bool many = shares > 1 && !q.few;
     const int2 sr = scan(many ? q.rows : 0, part), sn = scan(many, part);
-    if (r < B) {
-      offset[r] = capped(items, it.x) - q.blocks * shares;
+    if (b < B) {
+      offset[b] = capped(items, it.x) - mine;
       // an item's description, for those who write the items
-      a.items[a.item_cap + b] =
-          Item{b, q.blocks, 0, shares, q.start, q.n, q.len, parts && shares > 0 ? at : -1};
+      a.items[a.item_cap + b] = Item{b, q.blocks, 0, shares, q.start, q.n, q.len, at};
       if (q.few)
         for (int i = 0; i < q.n; ++i) {
           const int k = few_before + fw.x - q.n + i;
           if (k < a.few_cap)
-            a.few[k] = FewToken{q.start + i, q.len - q.n + i,
-                                parts && shares > 0 ? at + i * a.G : -1, q.rows << 8 | shares};
+            a.few[k] = FewToken{q.start + i, q.len - q.n + i, at < 0 ? -1 : at + i * a.G,
+                                q.rows << 8 | shares};
         }
       if (many)
-        a.splits[splits + sn.x - 1] =
-            SplitSeq{split + sr.x - q.rows, b, q.start, q.n, at, shares};
+        a.splits[splits + sn.x - 1] = SplitSeq{split + sr.x - q.rows, q.start, q.n, at, shares};
     }
     used = capped(used, pr.y);
     items = capped(items, it.y);
@@ -243,6 +366,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
     split = capped(split, sr.y);
     splits += sn.y;
   }
+  PlanHead h = whole.h;
   h.items = min(items, a.item_cap);
   h.split = split;
   h.splits = splits;
@@ -250,17 +374,14 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
   __syncthreads();
   for (int i = tid; i < h.items; i += kThreads) {
     Item x;
-    if (i < few_items) {
-      // shares of one block are neighbours
-      x = Item{-1, i / h.few_shares, i % h.few_shares, h.few_shares, 0, tokens, a.shared, 0};
+    if (i < h.few_items) {
+      x = whole.few_item(a, i);
     } else {
-      int r = 0;
+      int b = 0;
       for (int step = 1 << (31 - __clz(B)); step > 0; step >>= 1)
-        if (r + step < B && offset[r + step] <= i) r += step;
-      x = a.items[a.item_cap + order[r]];
-      const int j = i - offset[r];
-      x.block = x.block - 1 - j / x.shares;  // the last rows, which see the most, first
-      x.share = j % x.shares;
+        if (b + step < B && offset[b + step] <= i) b += step;
+      x = a.items[a.item_cap + b];
+      pick(x, x.block, i - offset[b]);
     }
     a.items[i] = x;
   }
@@ -279,14 +400,20 @@ struct Meet {
   float o[kWaves][16][D + 4];
   float m[kWaves][16], l[kWaves][16];
 };
+// The first token of the list that a shared item's rows belong to.
+template <int D>
+__device__ __forceinline__ int listed_from(const PackedArgs &a, const Item &x) {
+  return x.block * (x.n * a.G <= kFewRows ? 16 : kWaves * wave_rows(D)) / a.G;
+}
 // The rows of a wave: the last slot that each lane's sees, and the wave's first and last.
 template <int CT>
 struct Rows {
   int last[CT], high, low;
 };
 template <int D, int CT, bool F32>
-__device__ __forceinline__ Rows<CT> rows_of(const PackedArgs &a, const Item &x, int h, int row0,
-                                            int lane, RawQueries<D, CT, F32> &raw) {
+__device__ __forceinline__ Rows<CT> rows_of(const PackedArgs &a, const Item &x,
+                                            const Listed *list, int h, int row0, int lane,
+                                            RawQueries<D, CT, F32> &raw) {
   const int R = x.n * a.G;
   Rows<CT> r;
   int high = -1, low = INT32_MAX;
@@ -297,7 +424,7 @@ __device__ __forceinline__ Rows<CT> rows_of(const PackedArgs &a, const Item &x, 
     int64_t token = x.start + i;
     r.last[ct] = x.len - x.n + i;
     if (x.seq < 0) {
-      const FewToken t = a.few[i];
+      const Listed t = list[i - listed_from<D>(a, x)];
       token = t.token;
       r.last[ct] = min(t.last, x.len - 1);
     }
@@ -329,8 +456,8 @@ __device__ __forceinline__ void clear(Sums<D, CT> &A) {
 
 // An item of few rows: 16 of them, four waves share the tokens.
 template <int D, bool F32>
-__device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, int base, int h,
-                                        Meet<D> &meet) {
+__device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, const Listed *list,
+                                        int base, int h, Meet<D> &meet) {
   int lane = threadIdx.x & 63;
   // opaque, so that nothing formed from it is kept in registers from item to item
   asm volatile("" : "+v"(lane));
@@ -341,7 +468,7 @@ __device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, int 
   const int row0 = x.block * 16, t0 = shared ? 0 : base;
 
   RawQueries<D, 1, F32> raw;
-  const Rows<1> rows = rows_of<D, 1, F32>(a, x, h, row0, lane, raw);
+  const Rows<1> rows = rows_of<D, 1, F32>(a, x, list, h, row0, lane, raw);
   // tiles of 32 tokens of these rows and of this share, in whole rounds of the waves
   const int tiles = (max(0, rows.high + 1 - t0) + 31) / 32;
   const int rounds = (tiles + kWaves - 1) / kWaves;
@@ -433,7 +560,8 @@ __device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, int 
 
 // An item of many rows: every wave has rows of its own.
 template <int D, bool F32>
-__device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, int base, int h) {
+__device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, const Listed *list,
+                                         int base, int h) {
   constexpr int CT = wave_tiles(D), U = wave_rows(D);
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));  // as in run_few
@@ -446,7 +574,7 @@ __device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, int
   const int t0 = shared || R > 2 * U ? 0 : base;
 
   RawQueries<D, CT, F32> raw;
-  const Rows<CT> rows = rows_of<D, CT, F32>(a, x, h, row0, lane, raw);
+  const Rows<CT> rows = rows_of<D, CT, F32>(a, x, list, h, row0, lane, raw);
   // tiles of 32 tokens of the wave's rows and of this share
   const int tiles = (max(0, rows.high + 1 - t0) + 31) / 32;
   const int chunk = (tiles + x.shares - 1) / x.shares;
@@ -516,17 +644,47 @@ __device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, int
 }
 
 template <int D, bool F32>
+__device__ __forceinline__ void run(const PackedArgs &a, const Item &x, const Listed *list, int base,
+                                    int h, Meet<D> &meet) {
+  if (x.n * a.G <= kFewRows)
+    run_few<D, F32>(a, x, list, base, h, meet);
+  else
+    run_many<D, F32>(a, x, list, base, h);
+}
+
+// SMALL: up to 64 sequences, and a workgroup for each item that there can be.
+template <int D, bool F32, bool SMALL>
 __global__ __launch_bounds__(kThreads, 2) void packed_kernel(PackedArgs a) {
   __shared__ Meet<D> meet;
-  const int h = blockIdx.x % a.c.H, items = a.head->items, base = a.head->base;
-  // a launch has a workgroup for each item but where their number passes its limit
-  for (int i = blockIdx.x / a.c.H; i < items; i += gridDim.x / a.c.H) {
-    const Item x = a.items[i];
-    if (x.n * a.G <= kFewRows)
-      run_few<D, F32>(a, x, base, h, meet);
-    else
-      run_many<D, F32>(a, x, base, h);
-    __syncthreads();  // meet is written again
+  __shared__ Listed list[kListed];
+  const int h = blockIdx.x % a.c.H, tid = threadIdx.x;
+  if constexpr (SMALL) {
+    const LanePlan p = lane_plan<wave_rows(D)>(a, tid & 63);
+    const int i = blockIdx.x / a.c.H;
+    if (i >= p.h.items) return;
+    const Item x = lane_item<wave_rows(D)>(a, p, i);
+    if (x.n == 0) return;
+    if (x.seq < 0) {
+      const int from = listed_from<D>(a, x);
+      if (tid < 64 && p.q.few)
+        for (int j = max(0, from - p.few); j < p.q.n && p.few + j < from + kListed; ++j)
+          list[p.few + j - from] = Listed{p.q.start + j, p.q.len - p.q.n + j};
+      __syncthreads();
+    }
+    run<D, F32>(a, x, list, p.h.base, h, meet);
+  } else {
+    // a launch has a workgroup for each item but where their number passes its limit
+    const PlanHead head = *a.head;
+    for (int i = blockIdx.x / a.c.H; i < head.items; i += gridDim.x / a.c.H) {
+      const Item x = a.items[i];
+      if (x.seq < 0) {
+        const int k = listed_from<D>(a, x) + tid;
+        if (tid < kListed && k < head.few) list[tid] = Listed{a.few[k].token, a.few[k].last};
+        __syncthreads();
+      }
+      run<D, F32>(a, x, list, head.base, h, meet);
+      __syncthreads();  // the shared memory is written again
+    }
   }
 }
 
@@ -568,22 +726,39 @@ __device__ __forceinline__ void join_row(const PackedArgs &a, int64_t own, int64
 
 // A wave a row: blocks [0, few_blocks) for the rows of sequences with few of them, the
 // others for what is split of those with many.
-template <int D, bool F32>
+template <int D, bool F32, bool SMALL>
 __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a, int few_blocks) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const PlanHead h = *a.head;
+  LanePlan p;
+  PlanHead h;
+  if constexpr (SMALL) {
+    p = lane_plan<wave_rows(D)>(a, lane);
+    h = p.h;
+  } else {
+    h = *a.head;
+  }
   const int Hq = a.G * a.c.H;
   if ((int)blockIdx.x < few_blocks) {
     const int64_t r = (int64_t)blockIdx.x * kWaves + wave;
-    const int k = (int)(r / Hq), hq = (int)(r % Hq);
-    if (k * a.G >= h.few) return;
-    const FewToken t = a.few[k];
+    const int k = (int)(r / Hq), hq = (int)(r % Hq), g = hq % a.G;
+    if (k >= h.few) return;
+    FewToken t;
+    if constexpr (SMALL) {
+      const uint64_t whose = __ballot(p.q.few && k >= p.few && k - p.few < p.q.n);
+      if (whose == 0) return;
+      const int b = __builtin_ctzll(whose);
+      const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, b); };
+      const int i = k - of(p.few), part = of(p.part);
+      t = FewToken{of(p.q.start) + i, 0, part < 0 ? -1 : part + i * a.G,
+                   of(p.q.rows) << 8 | of(p.shares)};
+    } else {
+      t = a.few[k];
+    }
     if (t.part < 0 && h.base == 0) return;
-    const int g = hq % a.G;
     const int64_t at = (int64_t)(hq / a.G) * a.part_cap;
     join_row<D, F32>(a, at + t.part + g, t.rows_shares >> 8, t.part < 0 ? 0 : t.rows_shares & 255,
-                     at + k * a.G + g, h.few, h.base > 0 ? h.few_shares : 0,
+                     at + k * a.G + g, h.few * a.G, h.base > 0 ? h.few_shares : 0,
                      t.token * a.o_token + hq * a.o_head, lane);
     return;
   }
@@ -591,10 +766,19 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a, int few_bl
   for (int64_t r = (int64_t)(blockIdx.x - few_blocks) * kWaves + wave;
        r < (int64_t)h.split * a.c.H; r += stride) {
     const int row = (int)(r / a.c.H), head = (int)(r % a.c.H);
-    int j = 0;
-    for (int step = 1 << (31 - __clz(h.splits)); step > 0; step >>= 1)
-      if (j + step < h.splits && a.splits[j + step].row <= row) j += step;
-    const SplitSeq s = a.splits[j];
+    SplitSeq s;
+    if constexpr (SMALL) {
+      const uint64_t whose = __ballot(p.many && row >= p.split && row - p.split < p.q.rows);
+      if (whose == 0) return;
+      const int b = __builtin_ctzll(whose);
+      const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, b); };
+      s = SplitSeq{of(p.split), of(p.q.start), of(p.q.n), of(p.part), of(p.shares)};
+    } else {
+      int j = 0;
+      for (int step = 1 << (31 - __clz(h.splits)); step > 0; step >>= 1)
+        if (j + step < h.splits && a.splits[j + step].row <= row) j += step;
+      s = a.splits[j];
+    }
     const int mine = row - s.row, i = mine / a.G, hq = head * a.G + mine - i * a.G;
     join_row<D, F32>(a, (int64_t)head * a.part_cap + s.part + mine, (int64_t)s.n * a.G, s.shares,
                      0, 0, 0, (s.start + i) * a.o_token + hq * a.o_head, lane);
@@ -659,16 +843,24 @@ hipError_t launch_dim(PackedArgs a, int q_heads, void *ws, hipStream_t s) {
   a.ml = reinterpret_cast<float2 *>(w + p.off_ml);
   a.o = reinterpret_cast<float *>(w + p.off_o);
   a.item_cap = p.item_cap, a.few_cap = p.few_cap, a.part_cap = (int)p.part_cap;
+  const int few_blocks = (int)(((int64_t)p.few_cap * q_heads + kWaves - 1) / kWaves);
+  const int joins = few_blocks + ((int64_t)a.max_n * a.G > 2 * wave_rows(D) ? 1024 : 0);
+  const int most = kMaxGroups / a.c.H;
+  if (a.c.B <= 64 && p.item_cap <= most) {
+    packed_kernel<D, F32, true><<<(unsigned)p.item_cap * a.c.H, kThreads, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    join_kernel<D, F32, true><<<joins, kThreads, 0, s>>>(a, few_blocks);
+    return hipGetLastError();
+  }
   plan_kernel<wave_rows(D)><<<1, kThreads, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  packed_kernel<D, F32><<<(unsigned)std::min(p.item_cap, kMaxGroups / a.c.H) * a.c.H, kThreads, 0,
-                          s>>>(a);
+  packed_kernel<D, F32, false>
+      <<<(unsigned)std::min(p.item_cap, most) * a.c.H, kThreads, 0, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int few_blocks = (int)(((int64_t)p.few_cap * q_heads + kWaves - 1) / kWaves);
-  const int many_blocks = (int64_t)a.max_n * a.G > 2 * wave_rows(D) ? 1024 : 0;
-  join_kernel<D, F32><<<few_blocks + many_blocks, kThreads, 0, s>>>(a, few_blocks);
+  join_kernel<D, F32, false><<<joins, kThreads, 0, s>>>(a, few_blocks);
   return hipGetLastError();
 }
 
