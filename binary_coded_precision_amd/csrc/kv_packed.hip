@@ -49,8 +49,8 @@ struct Shape {
 };
 template <int U>
 __host__ __device__ constexpr Shape shape_of(int rows) {
-  return rows <= kFewRows ? Shape{(rows + 15) / 16, 4, 1}
-                          : Shape{(rows + 4 * U - 1) / (4 * U), 1, U / 16};
+  return rows <= kFewRows ? Shape{(rows + 15) / 16, 4, 2}
+                          : Shape{(rows + 4 * U - 1) / (4 * U), 1, 1 + U / 16};
 }
 
 struct PlanHead {
@@ -140,6 +140,12 @@ __device__ __forceinline__ int product(int a, int b) {
   return (int)min((int64_t)a * b, (int64_t)1 << 30);
 }
 
+// What a sequence's blocks take, in half steps of few rows; an item's start and end are
+// worth kStart of them.
+constexpr int kStart = 8;
+__device__ __forceinline__ float weight_of(int blocks, int steps, int weight) {
+  return (float)blocks * ((float)steps * (float)weight + (float)kStart);
+}
 // Lengths are cut by chunk: the steps' weight that a share should have.
 __device__ __forceinline__ int chunk_of(const PackedArgs &a, float cost) {
   return max(1, (int)fminf(ceilf(cost * (float)a.c.H * (1.f / kTarget)), (float)(1 << 24)));
@@ -171,7 +177,7 @@ struct Whole {
   }
   // the weight of all the sequences' own steps
   __device__ __forceinline__ void divide(const PackedArgs &a, float cost) {
-    cost += (float)few_blocks * (float)few_steps * (float)few_weight;
+    cost += weight_of(few_blocks, few_steps, few_weight);
     chunk = chunk_of(a, cost);
     if (!together) return;
     h.few_shares = shares_of(few_steps, few_weight, chunk, most);
@@ -244,7 +250,7 @@ __device__ __forceinline__ LanePlan lane_plan(const PackedArgs &a, int lane) {
   const int few = lane_scan(p.q.few ? p.q.n : 0);
   Whole<U> whole(a, __popcll(__ballot(p.q.few)), last_lane(few));
   shape<U>(p.q, whole.h.base);
-  whole.divide(a, lane_sum((float)p.q.blocks * (float)p.q.steps * (float)p.q.weight));
+  whole.divide(a, lane_sum(weight_of(p.q.blocks, p.q.steps, p.q.weight)));
   p.shares = whole.shares(p.q);
   const int rows = whole.rows(p.q, p.shares), end = capped(whole.used, lane_scan(rows));
   if (rows > 0 && end > a.part_cap) p.shares = 0;  // starts that are none
@@ -329,7 +335,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     Seq q = seq_at<U>(a, b0 + tid);
     shape<U>(q, whole.h.base);
-    cost += sum_of((float)q.blocks * (float)q.steps * (float)q.weight, partf);
+    cost += sum_of(weight_of(q.blocks, q.steps, q.weight), partf);
   }
   whole.divide(a, cost);
   int used = whole.used, items = whole.h.few_items, few_before = 0, split = 0, splits = 0;
