@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "kv_tiles.h"
+#include "lane_sums.h"
 
 namespace bcq {
 namespace {
@@ -132,10 +133,6 @@ __device__ __forceinline__ void shape(Seq &q, int base) {
   q.weight = s.weight;
 }
 
-// Sums stop at 2^30: starts that are none could pass 32 bits.
-__device__ __forceinline__ int capped(int a, int b) {
-  return (int)min((unsigned)a + (unsigned)b, 1u << 30);
-}
 __device__ __forceinline__ int product(int a, int b) {
   return (int)min((int64_t)a * b, (int64_t)1 << 30);
 }
@@ -209,34 +206,6 @@ __device__ __forceinline__ void pick(Item &x, int blocks, int j) {
 
 // ---- up to 64 sequences, one a lane
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int moved(int x) {  // 0 where nothing is moved to
-  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
-}
-// Inclusive sum over the lanes.
-__device__ __forceinline__ int lane_scan(int x) {
-  x = capped(x, moved<0x111, 0xf>(x));  // within 16 lanes
-  x = capped(x, moved<0x112, 0xf>(x));
-  x = capped(x, moved<0x114, 0xf>(x));
-  x = capped(x, moved<0x118, 0xf>(x));
-  x = capped(x, moved<0x142, 0xa>(x));  // the rows before
-  return capped(x, moved<0x143, 0xc>(x));
-}
-__device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, 63); }
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float moved(float x) {
-  return __int_as_float(moved<CTRL, ROWS>(__float_as_int(x)));
-}
-__device__ __forceinline__ float lane_sum(float x) {
-  x += moved<0x111, 0xf>(x);
-  x += moved<0x112, 0xf>(x);
-  x += moved<0x114, 0xf>(x);
-  x += moved<0x118, 0xf>(x);
-  x += moved<0x142, 0xa>(x);
-  x += moved<0x143, 0xc>(x);
-  return __int_as_float(last_lane(__float_as_int(x)));
-}
-
 struct LanePlan {
   PlanHead h;
   Seq q;  // the lane's sequence
@@ -293,22 +262,6 @@ __device__ __forceinline__ Item lane_item(const PackedArgs &a, const LanePlan &p
 
 // ---- more sequences
 
-// Inclusive sum over the workgroup and the sum of all.
-__device__ __forceinline__ int2 scan(int x, int *part) {
-  const int wave = threadIdx.x >> 6;
-  x = lane_scan(x);
-  if ((threadIdx.x & 63) == 63) part[wave] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int y = part[w];
-    if (w < wave) before = capped(before, y);
-    all = capped(all, y);
-  }
-  __syncthreads();
-  return make_int2(capped(x, before), all);
-}
 __device__ __forceinline__ float sum_of(float x, float *part) {
   x = lane_sum(x);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
@@ -327,8 +280,8 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
   int seqs = 0, tokens = 0;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     const Seq q = seq_at<U>(a, b0 + tid);
-    seqs += scan(q.few, part).y;
-    tokens = capped(tokens, scan(q.few ? q.n : 0, part).y);
+    seqs += block_scan<kWaves>(q.few, part).y;
+    tokens = capped(tokens, block_scan<kWaves>(q.few ? q.n : 0, part).y);
   }
   Whole<U> whole(a, seqs, tokens);
   float cost = 0.f;
@@ -345,13 +298,13 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
     shape<U>(q, whole.h.base);
     int shares = whole.shares(q);
     const int rows = whole.rows(q, shares);
-    const int2 pr = scan(rows, part);
+    const int2 pr = block_scan<kWaves>(rows, part);
     const int end = capped(used, pr.x);
     if (rows > 0 && end > a.part_cap) shares = 0;  // starts that are none
     const int at = rows > 0 && shares > 0 ? end - rows : -1, mine = product(q.blocks, shares);
-    const int2 it = scan(mine, part), fw = scan(q.few ? q.n : 0, part);
+    const int2 it = block_scan<kWaves>(mine, part), fw = block_scan<kWaves>(q.few ? q.n : 0, part);
     const bool many = shares > 1 && !q.few;
-    const int2 sr = scan(many ? q.rows : 0, part), sn = scan(many, part);
+    const int2 sr = block_scan<kWaves>(many ? q.rows : 0, part), sn = block_scan<kWaves>(many, part);
     if (b < B) {
       offset[b] = capped(items, it.x) - mine;
       // an item's description, for those who write the items

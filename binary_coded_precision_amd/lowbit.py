@@ -164,6 +164,19 @@ def _rows(name: str, t, rows: int, cols: int, read: int) -> int:
     return ld
 
 
+def _like(name: str, t, shape, dtype, dev: int):
+    """(address, leading dimension) of a matrix of this shape [T][K] and dtype with unit inner
+    stride on the call's device."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise ValueError("%s must be a %s device tensor of shape %s on device %d, got %s of %s on %s"
+                         % (name, dtype, tuple(shape), dev, tuple(t.shape), t.dtype, t.device))
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError("%s must have unit inner stride" % name)
+    # a single row has no next one to be aligned with
+    return t.data_ptr(), ld if shape[0] > 1 else _pad16(shape[1])
+
+
 # ----------------------------------------------------------------------------- 8-bit products
 
 
@@ -278,18 +291,14 @@ def bcq_rms_norm(X, gamma, eps, residual=None, H=None, Y=None, codes=None, scale
     if torch._C._cuda_getDevice() != dev:
         return _there(dev, bcq_rms_norm, X, gamma, eps, residual, H, Y, codes, scales, stream)
     raw = _raw(dev, stream)
-    dt = _float("X", X, dev)
-    T, K = X.shape
-
-    def rows(name, t):
-        if t is None:
-            return 0, 0
-        if t.dtype is not X.dtype or t.get_device() != dev:
-            raise ValueError("%s must be a device tensor of X's dtype on its device" % name)
-        ld = _rows(name, t, T, K, K)
-        # a single row has no next one to be aligned with
-        return t.data_ptr(), _pad16(ld) if T == 1 else ld
-
+    dt, shape, dtype = _float("X", X, dev), X.shape, X.dtype
+    if len(shape) != 2:
+        raise ValueError("X must be [T][K], got %s" % (tuple(shape),))
+    T, K = shape
+    xp, ldx = _like("X", X, shape, dtype, dev)
+    rp, ldr = (0, 0) if residual is None else _like("residual", residual, shape, dtype, dev)
+    hp, ldh = (0, 0) if H is None else _like("H", H, shape, dtype, dev)
+    yp, ldy = (0, 0) if Y is None else _like("Y", Y, shape, dtype, dev)
     cp = ldc = sp = 0
     if codes is not None:
         if codes.dtype is not torch.int8 or codes.get_device() != dev:
@@ -297,9 +306,8 @@ def bcq_rms_norm(X, gamma, eps, residual=None, H=None, Y=None, codes=None, scale
         cp, ldc = codes.data_ptr(), _rows("codes", codes, T, K, _pad16(K))
     if scales is not None:
         sp = _plain("scales", scales, torch.float32, (T,), dev)
-    r = lib.bcq_rms_norm(*rows("X", X), *rows("residual", residual),
-                         _plain("gamma", gamma, X.dtype, (K,), dev), eps, T, K, dt,
-                         *rows("H", H), *rows("Y", Y), cp, ldc, sp, raw)
+    r = lib.bcq_rms_norm(xp, ldx, rp, ldr, _plain("gamma", gamma, dtype, (K,), dev), eps, T, K, dt,
+                         hp, ldh, yp, ldy, cp, ldc, sp, raw)
     if r:
         _fail("bcq_rms_norm", r)
 
