@@ -96,14 +96,29 @@ struct Coded {
   uint32_t word;
   _Float16 scale, zero;
 };
+// Those of 16 lanes, a rotation by N at a time.
+template <int N>
+__device__ __forceinline__ float rotated(float x) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, false));
+}
+template <int N>
+__device__ __forceinline__ void extremes(float &lo, float &hi) {
+  lo = nan_min(lo, rotated<N>(lo));
+  hi = nan_max(hi, rotated<N>(hi));
+}
 template <int D, typename T, bool VEC>
 __device__ __forceinline__ Coded code_vector(const T *src) {
   float x[4];
   load4<T, VEC>(x, src);
   float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
   float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
+  extremes<8>(lo, hi);
+  extremes<4>(lo, hi);
+  extremes<2>(lo, hi);
+  extremes<1>(lo, hi);
 #pragma unroll
-  for (int d = 1; d < D / 4; d <<= 1) {
+  for (int d = 16; d < D / 4; d <<= 1) {
     lo = nan_min(lo, __shfl_xor(lo, d));
     hi = nan_max(hi, __shfl_xor(hi, d));
   }
@@ -250,11 +265,13 @@ __global__ __launch_bounds__(256) void append_slots_kernel(KvView c, int n, cons
   const int i = threadIdx.x % L;
   if (vec >= vecs) return;
   const PackedPlace p = packed_place(c, slots, n, vec);
-  const int64_t token = slot_token(c, p.slot, p.h);
-  if (token < 0) return;  // whole groups of L lanes leave together
+  // the vector is on its way while its slot is read
   const KvStrides st = p.v ? vs : ks;
-  put_vector<D>(c, code_vector<D, T, VEC>((p.v ? v : k) + p.t * st.token + p.h * st.head + i * 4),
-                token, p.v, i);
+  const int64_t t = min(p.t, (int64_t)n - 1);
+  const Coded x =
+      code_vector<D, T, VEC>((p.v ? v : k) + t * st.token + p.h * st.head + i * 4);
+  const int64_t token = slot_token(c, p.slot, p.h);
+  if (token >= 0) put_vector<D>(c, x, token, p.v, i);
 }
 
 template <int D, typename T, bool VEC>

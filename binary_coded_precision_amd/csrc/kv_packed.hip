@@ -353,6 +353,118 @@ __device__ __forceinline__ void store_out(const PackedArgs &a, int64_t at, float
     static_cast<_Float16 *>(a.out)[at] = (_Float16)x;
 }
 
+// ---- a wave's step over 32 tokens
+//
+// As in kv_tiles.h, with the reference taken off inside a score's own sum: d = s - ref
+// comes out of fma(q . c, ks, fma(kz, sum(q), -ref)), one operation a score less, and the
+// factors enter as the fp16 that they are.  For references up to 2^18 that rounds no
+// more than s itself would be; a row past that has ref 0 and `rest` taken off
+// afterwards.
+struct Ref {
+  float ref, rest;  // their sum is the reference; rest is -inf where there is none yet
+};
+__device__ __forceinline__ Ref ref_of(float m) {
+  return fabsf(m) < 0x1p18f ? Ref{m, 0.f} : Ref{0.f, m};
+}
+
+template <int D, int CT, bool F32>
+__device__ __forceinline__ void step_scores(float4v (&S)[2][CT], const Tiles<D> &T,
+                                            const Queries<D, CT, F32> &Q, const Sums<D, CT> &A,
+                                            float code_unit) {
+  float minus[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) minus[ct] = -ref_of(A.m[ct]).ref;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    tile_scores<D, CT, F32>(S[s], T, s, Q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const half2v f = pair_of(T.m[s][2 * i]);
+      const float ks = F32 ? 0.f : fmaf((float)f[0], code_unit, 0.f);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const float t = fmaf((float)f[1], Q.sum[ct], minus[ct]);
+        S[s][ct][i] = F32 ? fmaf((float)f[0], S[s][ct][i], t) : fmaf(S[s][ct][i], ks, t);
+      }
+    }
+  }
+}
+
+template <int D, int CT>
+__device__ __forceinline__ void step_softmax(Sums<D, CT> &A, Frag (&P)[CT], Frag (&Plo)[CT],
+                                             float4v (&S)[2][CT], const Tiles<D> &T) {
+  ushort2v scales = pair16(T.m[0][1]);
+  float high[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) high[ct] = S[0][ct][0];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      scales = __builtin_elementwise_max(scales, pair16(T.m[s][2 * i + 1]));
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) high[ct] = fmaxf(high[ct], S[s][ct][i]);
+    }
+  const float room = kRaise + kSlack - rough_log2((uint32_t)scales[0]);
+  bool raise = false, rests = false;
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const float rest = ref_of(A.m[ct]).rest;
+    raise |= high[ct] - rest > room;
+    rests |= rest != 0.f;
+  }
+  if (__any(raise || rests)) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const Ref was = ref_of(A.m[ct]);
+      float top = kNegInf;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = fmaxf(top, S[s][ct][i] + rough_log2(T.m[s][2 * i + 1] & 0xffffu));
+      raise_row(A, ct, group_max(top) + was.ref, high[ct] + was.ref);
+      const Ref now = ref_of(A.m[ct]);
+      // from the old reference to the new one; a row that has seen nothing has -inf
+      // only, and no reference
+      const float by = was.ref - now.ref - (now.rest > kNegInf ? now.rest : 0.f);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[s][ct][i] += by;
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      half2v f[2];
+      float mid[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f[j] = pair_of(T.m[s][2 * (i + j) + 1]);
+        mid[j] = fmaf(7.5f, (float)f[j][0], (float)f[j][1]);
+      }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float p[2], pv[2], rest[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(S[s][ct][i + j]);
+          A.l[ct] += p[j];
+          A.z[ct] = fmaf(p[j], mid[j], A.z[ct]);
+          pv[j] = fmaf((float)f[j][0], p[j], 0.f);
+        }
+        // cut off rather than rounded: what is left goes to Plo either way
+        const half2v part = kv::cut(pv[0], pv[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) rest[j] = fmaf((float)f[j][0], p[j], -(float)part[j]);
+        P[ct].p[2 * s + (i >> 1)] = part;
+        Plo[ct].p[2 * s + (i >> 1)] = kv::cut(rest[0], rest[1]);
+      }
+    }
+}
+
 // Waves of the same rows meet here.
 template <int D>
 struct Meet {
@@ -458,11 +570,11 @@ __device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, cons
     const Where w = ahead;
     ahead = place_of(next + kWaves);
     float4v S[2][1];
-    scores<D, 1, F32>(S, T, Q, a.code_unit);
+    step_scores<D, 1, F32>(S, T, Q, A, a.code_unit);
     load_k(T, a.c, w, lane);
     if (tile >= free_end) mask_scores<D, 1>(S, T, A, t0 + tile * 32 + 4 * g, rows.last);
     Frag P[1], Plo[1];
-    softmax_tiles<D, 1>(A, P, Plo, S, T);
+    step_softmax<D, 1>(A, P, Plo, S, T);
     load_m(T, a.c, w, lane);
     add_values<D, 1, F32>(A, P, Plo, T);
     load_v(T, a.c, w, lane);
@@ -560,11 +672,11 @@ __device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, con
     const Where w = ahead;
     ahead = place_of(tile + 2);
     float4v S[2][CT];
-    scores<D, CT, F32>(S, T, Q, a.code_unit);
+    step_scores<D, CT, F32>(S, T, Q, A, a.code_unit);
     load_k(T, a.c, w, lane);
     if (tile >= free_end) mask_scores<D, CT>(S, T, A, t0 + tile * 32 + 4 * g, rows.last);
     Frag P[CT], Plo[CT];
-    softmax_tiles<D, CT>(A, P, Plo, S, T);
+    step_softmax<D, CT>(A, P, Plo, S, T);
     load_m(T, a.c, w, lane);
     add_values<D, CT, F32>(A, P, Plo, T);
     load_v(T, a.c, w, lane);
