@@ -156,14 +156,17 @@ def main():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         server.run(one)
-    graph.replay()  # the first brings the graph to the device
-    torch.cuda.synchronize()
-    start = time.perf_counter()
-    for _ in range(a.steps):
-        graph.replay()
-        one.x.copy_(one.x / one.x.float().pow(2).mean(1, keepdim=True).sqrt().half())
-    torch.cuda.synchronize()
-    us = (time.perf_counter() - start) / a.steps * 1e6
+
+    def run(steps):
+        start = time.perf_counter()
+        for _ in range(steps):
+            graph.replay()
+            one.x.copy_(one.x / one.x.float().pow(2).mean(1, keepdim=True).sqrt().half())
+        torch.cuda.synchronize()
+        return (time.perf_counter() - start) / steps * 1e6
+
+    run(1)  # the first brings graph and kernels to the device
+    us = run(a.steps)
     print("%d steps of %d requests through %d layers, %.1f us each; lengths %d to %d, %d of %d pages "
           "free" % (a.steps, a.batch, a.layers, us, int(server.lens.min()), int(server.lens.max()),
                     int(server.count), server.pages))
