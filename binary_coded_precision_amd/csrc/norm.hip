@@ -86,10 +86,8 @@ __device__ __forceinline__ void scale_row8(float (&y)[8], const float (&h)[8], f
 // One workgroup a row.  Rows of up to 8 N THREADS elements are held in registers;
 // longer ones (N = 0) are read again from the caches for each of three passes.
 template <typename T, int N, int THREADS>
-__global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
-  __shared__ double red_sum[THREADS / 64];
-  __shared__ float red_max[THREADS / 64];
-  const int64_t row = blockIdx.x;
+__device__ __forceinline__ void norm_row(const NormArgs &a, int64_t row, double *red_sum,
+                                         float *red_max) {
   const int tid = threadIdx.x, K = a.K;
   const T *x = static_cast<const T *>(a.x) + row * a.ldx;
   const T *r = a.residual == nullptr ? nullptr
@@ -164,18 +162,35 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
   }
 }
 
+template <typename T, int N, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a, int rows) {
+  __shared__ double red_sum[THREADS / 64];
+  __shared__ float red_max[THREADS / 64];
+  if constexpr (THREADS <= 256) {
+    norm_row<T, N, THREADS>(a, blockIdx.x, red_sum, red_max);
+  } else {
+    // a launch's work items are counted in 32 bits: more rows take turns
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+      norm_row<T, N, THREADS>(a, row, red_sum, red_max);
+      __syncthreads();  // the sums are written again
+    }
+  }
+}
+
 template <typename T>
-hipError_t norm_type(const NormArgs &a, int T_, hipStream_t s) {
+hipError_t norm_type(const NormArgs &a, int rows, hipStream_t s) {
+  constexpr int kMostRows = (1 << 22) - 1;  // of 1024 threads
+  const int turns = rows < kMostRows ? rows : kMostRows;
   if (a.K <= 2048)
-    norm_kernel<T, 1, 256><<<T_, 256, 0, s>>>(a);
+    norm_kernel<T, 1, 256><<<rows, 256, 0, s>>>(a, rows);
   else if (a.K <= 4096)
-    norm_kernel<T, 2, 256><<<T_, 256, 0, s>>>(a);
+    norm_kernel<T, 2, 256><<<rows, 256, 0, s>>>(a, rows);
   else if (a.K <= 8192)
-    norm_kernel<T, 4, 256><<<T_, 256, 0, s>>>(a);
+    norm_kernel<T, 4, 256><<<rows, 256, 0, s>>>(a, rows);
   else if (a.K <= 16384)
-    norm_kernel<T, 2, 1024><<<T_, 1024, 0, s>>>(a);
+    norm_kernel<T, 2, 1024><<<turns, 1024, 0, s>>>(a, rows);
   else
-    norm_kernel<T, 0, 1024><<<T_, 1024, 0, s>>>(a);
+    norm_kernel<T, 0, 1024><<<turns, 1024, 0, s>>>(a, rows);
   return hipGetLastError();
 }
 

@@ -161,3 +161,24 @@ def test_feeds_the_integer_product():
 def test_no_rows():
     e = torch.empty((0, 64), device="cuda")
     bcq.bcq_rms_norm(e, torch.ones(64, device="cuda"), EPS, H=e)
+
+
+def test_more_long_rows_than_a_launch_has_room_for():
+    """Long rows take 1024 work items each, of which a launch has less than 2^32."""
+    T, K = (1 << 22) + 1, 8200
+    say("rms_norm", T, K)
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("takes 104 GB of device memory")
+    x = torch.empty((T, 8208), dtype=torch.float16, device="cuda")
+    codes = torch.full((T, 8208), 7, dtype=torch.int8, device="cuda")
+    scales = torch.full((T,), 7.0, device="cuda")
+    gamma = torch.ones(K, dtype=torch.float16, device="cuda")
+    x[:] = torch.randn(8208, dtype=torch.float16, device="cuda")
+    bcq.bcq_rms_norm(x[:, :K], gamma, EPS, codes=codes[:, :K], scales=scales)
+    check(x[:1, :K].cpu().numpy(), None, gamma.cpu().numpy(), EPS, "f16", None, None,
+          (codes[:1, :K], codes[:1]), scales[:1])
+    assert (scales == scales[0]).all()
+    for rows in codes.split(1 << 16):
+        assert (rows == codes[0]).all()
+    del x, codes
+    torch.cuda.empty_cache()
