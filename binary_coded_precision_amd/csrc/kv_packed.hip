@@ -138,13 +138,16 @@ __device__ __forceinline__ int product(int a, int b) {
 }
 
 // What a sequence's blocks take, in half steps of few rows; an item's start and end are
-// worth kStart of them.
+// worth kStart of them.  Two kernels work out the same plan: no two operations of it
+// become one, which the compiler could do in one of them alone.
 constexpr int kStart = 8;
 __device__ __forceinline__ float weight_of(int blocks, int steps, int weight) {
+#pragma clang fp contract(off)
   return (float)blocks * ((float)steps * (float)weight + (float)kStart);
 }
 // Lengths are cut by chunk: the steps' weight that a share should have.
 __device__ __forceinline__ int chunk_of(const PackedArgs &a, float cost) {
+#pragma clang fp contract(off)
   return max(1, (int)fminf(ceilf(cost * (float)a.c.H * (1.f / kTarget)), (float)(1 << 24)));
 }
 __device__ __forceinline__ int shares_of(int steps, int weight, int chunk, int most) {
@@ -174,6 +177,7 @@ struct Whole {
   }
   // the weight of all the sequences' own steps
   __device__ __forceinline__ void divide(const PackedArgs &a, float cost) {
+#pragma clang fp contract(off)
     cost += weight_of(few_blocks, few_steps, few_weight);
     chunk = chunk_of(a, cost);
     if (!together) return;
@@ -189,9 +193,6 @@ struct Whole {
   }
   __device__ __forceinline__ int rows(const Seq &q, int shares) const {
     return shares > 1 || (together && q.few) ? product(q.rows, shares) : 0;
-  }
-  __device__ __forceinline__ Item few_item(const PackedArgs &a, int i) const {
-    return few_item(a, h, i);
   }
   // shares of one block are neighbours
   static __device__ __forceinline__ Item few_item(const PackedArgs &a, const PlanHead &h, int i) {
@@ -263,6 +264,7 @@ __device__ __forceinline__ Item lane_item(const PackedArgs &a, const LanePlan &p
 // ---- more sequences
 
 __device__ __forceinline__ float sum_of(float x, float *part) {
+#pragma clang fp contract(off)
   x = lane_sum(x);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
   __syncthreads();
@@ -304,7 +306,8 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
     const int at = rows > 0 && shares > 0 ? end - rows : -1, mine = product(q.blocks, shares);
     const int2 it = block_scan<kWaves>(mine, part), fw = block_scan<kWaves>(q.few ? q.n : 0, part);
     const bool many = shares > 1 && !q.few;
-    const int2 sr = block_scan<kWaves>(many ? q.rows : 0, part), sn = block_scan<kWaves>(many, part);
+    const int2 sr = block_scan<kWaves>(many ? q.rows : 0, part);
+    const int2 sn = block_scan<kWaves>(many, part);
     if (b < B) {
       offset[b] = capped(items, it.x) - mine;
       // an item's description, for those who write the items
@@ -334,7 +337,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
   for (int i = tid; i < h.items; i += kThreads) {
     Item x;
     if (i < h.few_items) {
-      x = whole.few_item(a, i);
+      x = whole.few_item(a, h, i);
     } else {
       int b = 0;
       for (int step = 1 << (31 - __clz(B)); step > 0; step >>= 1)
@@ -715,8 +718,8 @@ __device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, con
 }
 
 template <int D, bool F32>
-__device__ __forceinline__ void run(const PackedArgs &a, const Item &x, const Listed *list, int base,
-                                    int h, Meet<D> &meet) {
+__device__ __forceinline__ void run(const PackedArgs &a, const Item &x, const Listed *list,
+                                    int base, int h, Meet<D> &meet) {
   if (x.n * a.G <= kFewRows)
     run_few<D, F32>(a, x, list, base, h, meet);
   else
@@ -811,26 +814,27 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a, int few_bl
   }
   const int Hq = a.G * a.c.H;
   if ((int)blockIdx.x < few_blocks) {
-    const int64_t r = (int64_t)blockIdx.x * kWaves + wave;
-    const int k = (int)(r / Hq), hq = (int)(r % Hq), g = hq % a.G;
-    if (k >= h.few) return;
-    FewToken t;
-    if constexpr (SMALL) {
-      const uint64_t whose = __ballot(p.q.few && k >= p.few && k - p.few < p.q.n);
-      if (whose == 0) return;
-      const int b = __builtin_ctzll(whose);
-      const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, b); };
-      const int i = k - of(p.few), part = of(p.part);
-      t = FewToken{of(p.q.start) + i, 0, part < 0 ? -1 : part + i * a.G,
-                   of(p.q.rows) << 8 | of(p.shares)};
-    } else {
-      t = a.few[k];
+    for (int64_t r = (int64_t)blockIdx.x * kWaves + wave; r < (int64_t)h.few * Hq;
+         r += (int64_t)few_blocks * kWaves) {
+      const int k = (int)(r / Hq), hq = (int)(r % Hq), g = hq % a.G;
+      FewToken t;
+      if constexpr (SMALL) {
+        const uint64_t whose = __ballot(p.q.few && k >= p.few && k - p.few < p.q.n);
+        if (whose == 0) continue;
+        const int b = __builtin_ctzll(whose);
+        const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, b); };
+        const int i = k - of(p.few), part = of(p.part);
+        t = FewToken{of(p.q.start) + i, 0, part < 0 ? -1 : part + i * a.G,
+                     of(p.q.rows) << 8 | of(p.shares)};
+      } else {
+        t = a.few[k];
+      }
+      if (t.part < 0 && h.base == 0) continue;
+      const int64_t at = (int64_t)(hq / a.G) * a.part_cap;
+      join_row<D, F32>(a, at + t.part + g, t.rows_shares >> 8, t.part < 0 ? 0 : t.rows_shares & 255,
+                       at + k * a.G + g, h.few * a.G, h.base > 0 ? h.few_shares : 0,
+                       t.token * a.o_token + hq * a.o_head, lane);
     }
-    if (t.part < 0 && h.base == 0) return;
-    const int64_t at = (int64_t)(hq / a.G) * a.part_cap;
-    join_row<D, F32>(a, at + t.part + g, t.rows_shares >> 8, t.part < 0 ? 0 : t.rows_shares & 255,
-                     at + k * a.G + g, h.few * a.G, h.base > 0 ? h.few_shares : 0,
-                     t.token * a.o_token + hq * a.o_head, lane);
     return;
   }
   const int64_t stride = (int64_t)(gridDim.x - few_blocks) * kWaves;
@@ -861,7 +865,7 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 // How many items, tokens and partial rows a call can have.  With C the blocks' steps
 // in all, shares have at least C H / kTarget steps, so that the sum of steps / share
 // over the blocks is at most kTarget / H, and a block has at most one share more than
-// that; or, where kMostSteps is less, a block has at most `past`.
+// that; where kMostSteps cuts a block further, it has at most `past` besides.
 struct PackedPlan {
   int item_cap, few_cap;
   int64_t part_cap;
@@ -876,7 +880,8 @@ PackedPlan packed_plan(int B, int H, int D, int room, int T, int q_heads, int ma
   const int64_t few_blocks = shared ? few * G / block + 2 : 0;
   const int64_t target = kTarget / H + 1, past = room / (32 * kMostSteps) + 1;
   PackedPlan p;
-  p.item_cap = (int)std::min<int64_t>(target + (blocks + few_blocks) * past, 1 << 30);
+  const int64_t cuts = past == 1 ? 1 : past + 1;  // of a block, but for the target's
+  p.item_cap = (int)std::min<int64_t>(target + (blocks + few_blocks) * cuts, 1 << 30);
   p.few_cap = (int)std::max<int64_t>(few, 1);
   // rows of all the shares: a block's has at most `most`; blocks with one share have
   // none but those that meet the shared pages
@@ -885,8 +890,7 @@ PackedPlan packed_plan(int B, int H, int D, int room, int T, int q_heads, int ma
   const int64_t own = std::min(target * most + rows, 2 * target * most + (shared ? few * G : 0));
   const int64_t met =
       shared ? target * std::min<int64_t>(few * G <= kFewRows ? 16 : block, few * G) + few * G : 0;
-  p.part_cap = past == 1 ? own + met
-                         : std::max(own, rows * past) + std::max(met, shared ? few * G * past : 0);
+  p.part_cap = own + met + (past == 1 ? 0 : (rows + (shared ? few * G : 0)) * past);
   size_t at = 256;
   p.off_items = at;
   at += pad256((size_t)(p.item_cap + B) * sizeof(Item));
@@ -914,7 +918,8 @@ hipError_t launch_dim(PackedArgs a, int q_heads, void *ws, hipStream_t s) {
   a.ml = reinterpret_cast<float2 *>(w + p.off_ml);
   a.o = reinterpret_cast<float *>(w + p.off_o);
   a.item_cap = p.item_cap, a.few_cap = p.few_cap, a.part_cap = (int)p.part_cap;
-  const int few_blocks = (int)(((int64_t)p.few_cap * q_heads + kWaves - 1) / kWaves);
+  const int few_blocks =
+      (int)std::min<int64_t>(((int64_t)p.few_cap * q_heads + kWaves - 1) / kWaves, 1 << 20);
   const int joins = few_blocks + ((int64_t)a.max_n * a.G > 2 * wave_rows(D) ? 1024 : 0);
   const int most = kMaxGroups / a.c.H;
   if (a.c.B <= 64 && p.item_cap <= most) {

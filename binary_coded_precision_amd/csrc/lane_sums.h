@@ -30,6 +30,7 @@ __device__ __forceinline__ float moved(float x) {
   return __int_as_float(moved<CTRL, ROWS>(__float_as_int(x)));
 }
 __device__ __forceinline__ float lane_sum(float x) {
+#pragma clang fp contract(off)
   x += moved<0x111, 0xf>(x);
   x += moved<0x112, 0xf>(x);
   x += moved<0x114, 0xf>(x);

@@ -677,7 +677,8 @@ size_t bcq_kv_workspace_bytes(const bcq_kv_cache *cache, int32_t n, int32_t q_he
  *   (0: none); the rows of sequences with few of them then read these pages together.
  * Q, O: element (t, head, d) at t*_token + head*_head + d, q_heads heads (a multiple of
  *   heads), dtype BCQ_F16 or BCQ_F32; O does not overlap Q.  scale: finite.
- * What is rounded is as in bcq_kv_attend; weights are not summed.
+ * What is rounded is as in bcq_kv_attend, but that in tables with room past 2^21 tokens
+ * sums of up to a 32nd of that are left to the matrix cores; weights are not summed.
  * batch is at most BCQ_KV_PACKED_MAX_BATCH, T * q_heads at most 2^28, and the rows
  * that a cached head's workspace holds (a few times T * q_heads / heads, and in tables
  * with room past 2^16 tokens that times room / 2^16) fewer than 2^30.

@@ -258,3 +258,28 @@ def test_not_finite_values():
                 assert (got[same] == want[same]).all(), (D, part, value)
                 assert not np.isfinite(got[16:31]).any() or (part < 2 and value == np.inf)
                 c.s = kept
+
+
+def test_more_rows_to_join_than_a_launch_has_room_for():
+    """Past 2^22 rows the workgroups that join them take turns."""
+    B, n, H, D, page = 4096, 8, 160, 64, 16
+    say("kv_attend_packed joins", B * n * H, "rows")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    cache = bcq.KVCache.pool(B, 2 * page, B + 1, H, D, page)[0]
+    cache.page_table[:, 0] = 0
+    cache.page_table[:, 1] = torch.arange(1, B + 1, device="cuda")
+    slots = torch.cat([torch.arange(page), torch.arange(B * n) // n * page + page
+                       + torch.arange(B * n) % n]).cuda()
+    for at in slots.split(4096):
+        kv = torch.randn((2, len(at), H, D), generator=gen, device="cuda").half()
+        bcq.bcq_kv_append_slots(cache, kv[0], kv[1], at)
+    cache.lens[:] = page + n
+    q = torch.randn((B * n, H, D), generator=gen, device="cuda").half()
+    got, want = torch.full_like(q, 7), torch.empty_like(q)
+    starts = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    bcq.bcq_kv_attend_packed(cache, q, got, starts, n, shared_pages=1)
+    bcq.bcq_kv_attend(cache, q.view(B, n, H, D), want.view(B, n, H, D))
+    # both round sums of 24 terms that agree to 1e-5 of the largest |v|, 4, once: half a
+    # step each
+    off = (got.float() - want.float()).abs()
+    assert (off <= 2.0**-10 * want.float().abs() + 4e-5).all()
