@@ -96,11 +96,11 @@ struct Coded {
   uint32_t word;
   _Float16 scale, zero;
 };
-// Those of 16 lanes, a rotation by N at a time.
+// Of 16 lanes, the value N lanes further on, the first behind the last.
 template <int N>
 __device__ __forceinline__ float rotated(float x) {
   return __int_as_float(
-      __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, false));
+      __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x130 - N, 0xf, 0xf, false));
 }
 template <int N>
 __device__ __forceinline__ void extremes(float &lo, float &hi) {
@@ -113,10 +113,12 @@ __device__ __forceinline__ Coded code_vector(const T *src) {
   load4<T, VEC>(x, src);
   float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
   float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
-  extremes<8>(lo, hi);
-  extremes<4>(lo, hi);
-  extremes<2>(lo, hi);
+  // in the order of a butterfly for lane 0, which stores them: a zero's sign is that of
+  // the last one among equals
   extremes<1>(lo, hi);
+  extremes<2>(lo, hi);
+  extremes<4>(lo, hi);
+  extremes<8>(lo, hi);
 #pragma unroll
   for (int d = 16; d < D / 4; d <<= 1) {
     lo = nan_min(lo, __shfl_xor(lo, d));

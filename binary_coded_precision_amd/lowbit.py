@@ -1,6 +1,6 @@
 """Binding of the low-bit serving operators: the 8-bit integer linear layer, the norm before it
-and the 4-bit key/value cache (reserve, append, read, attend, evict).  Names and semantics are those of
-``include/bcq.h``; the package exports everything here.
+and the 4-bit key/value cache (reserve, append, read, attend, evict).  Names and semantics are
+those of ``include/bcq.h``; the package exports everything here.
 
 The tensors of a call, and its ``stream`` if one is given, belong to one device, which need not be
 the current one.

@@ -476,6 +476,7 @@ size_t bcq_int_workspace_bytes(int32_t T, int32_t M, int32_t K);
  * codes: [T][ldc], scales: [T], as bcq_int_quantize writes them and bcq_int_gemm
  *   reads them (ldc a multiple of 16, at least K rounded up to one, zeros from K up
  *   to that multiple), or both NULL.  One of H, Y and codes at least is given.
+ * Y, codes and scales overlap nothing that the call reads or writes besides.
  * X, residual, gamma, H and Y are of dtype (BCQ_F16 or BCQ_F32), 16-byte aligned
  *   with ld*size a multiple of 16 bytes and ld >= K; codes are 16-byte aligned.
  *   Nothing past K is read, or written but for those zeros.

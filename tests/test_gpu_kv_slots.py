@@ -254,3 +254,32 @@ def test_the_same_as_append():
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
     assert positions.view(B, n).tolist() == [list(range(n))] * B
     assert int(count) == 12 - B * 2
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_sign_of_a_zero(D):
+    """A vector whose least element is a zero of either sign: four elements meet, then those of
+    neighbours, pairs of them and so on, the later one winning among equals."""
+    say("kv_append zeros", D)
+    rng = np.random.default_rng(D)
+    x = np.where(rng.random((40, 1, D)) < 0.5, 0.0, -0.0).astype(np.float32)
+    x[::3] = np.where(rng.random(x[::3].shape) < 0.7, 1.5, x[::3])
+    least = x[:, 0]
+    pick = lambda a, b: np.where((a < b) | (a != a), a, b)  # noqa: E731
+    for _ in range(2):
+        least = pick(least[:, ::2], least[:, 1::2])
+    at = np.arange(D // 4)
+    for d in [1 << i for i in range(20) if 1 << i < D // 4]:
+        least = pick(least, least[:, at ^ d])
+    want = least[:, 0].astype(np.float16).view(np.uint16)
+    k = up(x)
+    cache = bcq.KVCache.new(1, 64, 1, D)
+    cache.lens[:] = 40
+    bcq.bcq_kv_append(cache, k.view(1, 40, 1, D), k.view(1, 40, 1, D))
+    one = cache.scales.clone()
+    cache.scales.fill_(7)
+    bcq.bcq_kv_append_slots(cache, k, k, torch.arange(40, device="cuda"))
+    for got in (one, cache.scales):
+        got = got.cpu().numpy().view(np.uint16)[0, 0, :40]
+        np.testing.assert_array_equal(got[:, 1], want)
+        np.testing.assert_array_equal(got[:, 3], want)
