@@ -36,6 +36,8 @@ constexpr int kMaxShares = 64;  // of a row, one a lane where they are joined
 // Workgroups that a call is cut into when there is enough to do: two a compute unit,
 // as many as their registers leave room for.
 constexpr int kTarget = 512;
+constexpr int kUnits = kTarget / 2;
+constexpr int kNearTurn = kUnits / 5;
 constexpr int kMaxGroups = (1 << 24) - 1;  // of 256 work items in a launch
 constexpr int kMostParts = 1 << 30;        // partial rows of a cached head
 constexpr int kMostSteps = 2048;  // of 32 tokens, that a wave sums in one go (kv_attend.hip)
@@ -182,6 +184,16 @@ struct Whole {
     chunk = chunk_of(a, cost);
     if (!together) return;
     h.few_shares = shares_of(few_steps, few_weight, chunk, most);
+    // The shared items are much alike and start first, one on each compute unit, then a
+    // second: with a second on half of the units the others would wait for those.  So
+    // whole turns of them, the sequences' own items beside the last.  64 decode steps
+    // behind 16384 tokens: 256 items in 54 us, 288 in 54, 384 (what the weights say) in 61,
+    // 464 in 67; four fifths of a turn are made a whole one (480 items 89 us; 256 93, 512
+    // 87).
+    const int wide = few_blocks * a.c.H, turns = (h.few_shares * wide + kNearTurn) / kUnits;
+    if (h.few_shares * wide >= kUnits)
+      h.few_shares = min(max(max(turns * kUnits / wide, 1),
+                             (few_steps + kMostSteps - 1) / kMostSteps), most);
     if ((int64_t)h.few_shares * h.few * a.G > a.part_cap) h.few_shares = 0;
     used = h.few_shares * h.few * a.G;
     h.few_items = few_blocks * h.few_shares;
@@ -798,8 +810,12 @@ __device__ __forceinline__ void join_row(const PackedArgs &a, int64_t own, int64
     store_out(a, out + c * 64 + lane, l == 0.f ? 0.f : o[c] / l, F32);
 }
 
-// A wave a row: blocks [0, few_blocks) for the rows of sequences with few of them, the
-// others for what is split of those with many.
+// A wave a row at a time: blocks [0, few_blocks) for the rows of sequences with few of
+// them, the others for what is split of those with many.  Every block works the plan out,
+// so there are no more than the card holds at once a few times over: 31 decode steps
+// beside 1024 rows of a prompt 206 us (4096 + 1024 blocks 211, 512 + 512 217, 1024 + 8192
+// 210).
+constexpr int kJoinsFew = 1024, kJoinsMany = 2048;
 template <int D, bool F32, bool SMALL>
 __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a, int few_blocks) {
   const int lane = threadIdx.x & 63;
@@ -864,8 +880,8 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 // How many items, tokens and partial rows a call can have.  With C the blocks' steps
 // in all, shares have at least C H / kTarget steps, so that the sum of steps / share
-// over the blocks is at most kTarget / H, and a block has at most one share more than
-// that; where kMostSteps cuts a block further, it has at most `past` besides.
+// over the blocks is at most kTarget / H (and kNearTurn / H for the shared pages'), and a
+// block has at most one share more than that; where kMostSteps cuts a block further, it has at most `past` besides.
 struct PackedPlan {
   int item_cap, few_cap;
   int64_t part_cap;
@@ -878,7 +894,7 @@ PackedPlan packed_plan(int B, int H, int D, int room, int T, int q_heads, int ma
   const int64_t few = std::min<int64_t>(T, seqs * (2 * U / G));
   const int64_t blocks = rows / block + 2 * seqs;  // two of up to kFewRows rows
   const int64_t few_blocks = shared ? few * G / block + 2 : 0;
-  const int64_t target = kTarget / H + 1, past = room / (32 * kMostSteps) + 1;
+  const int64_t target = (kTarget + kNearTurn) / H + 1, past = room / (32 * kMostSteps) + 1;
   PackedPlan p;
   const int64_t cuts = past == 1 ? 1 : past + 1;  // of a block, but for the target's
   p.item_cap = (int)std::min<int64_t>(target + (blocks + few_blocks) * cuts, 1 << 30);
@@ -919,8 +935,8 @@ hipError_t launch_dim(PackedArgs a, int q_heads, void *ws, hipStream_t s) {
   a.o = reinterpret_cast<float *>(w + p.off_o);
   a.item_cap = p.item_cap, a.few_cap = p.few_cap, a.part_cap = (int)p.part_cap;
   const int few_blocks =
-      (int)std::min<int64_t>(((int64_t)p.few_cap * q_heads + kWaves - 1) / kWaves, 1 << 20);
-  const int joins = few_blocks + ((int64_t)a.max_n * a.G > 2 * wave_rows(D) ? 1024 : 0);
+      (int)std::min<int64_t>(((int64_t)p.few_cap * q_heads + kWaves - 1) / kWaves, kJoinsFew);
+  const int joins = few_blocks + ((int64_t)a.max_n * a.G > 2 * wave_rows(D) ? kJoinsMany : 0);
   const int most = kMaxGroups / a.c.H;
   if (a.c.B <= 64 && p.item_cap <= most) {
     packed_kernel<D, F32, true><<<(unsigned)p.item_cap * a.c.H, kThreads, 0, s>>>(a);
