@@ -107,10 +107,8 @@ __device__ __forceinline__ void extremes(float &lo, float &hi) {
   lo = nan_min(lo, rotated<N>(lo));
   hi = nan_max(hi, rotated<N>(hi));
 }
-template <int D, typename T, bool VEC>
-__device__ __forceinline__ Coded code_vector(const T *src) {
-  float x[4];
-  load4<T, VEC>(x, src);
+template <int D>
+__device__ __forceinline__ Coded code_vector(const float (&x)[4]) {
   float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
   float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
   // in the order of a butterfly for lane 0, which stores them: a zero's sign is that of
@@ -203,8 +201,9 @@ __global__ __launch_bounds__(256) void append_kernel(KvView c, int n, const T *k
   const Place p = place(c, n, vec);
   if (!p.in) return;
   const KvStrides st = p.v ? vs : ks;
-  const Coded x = code_vector<D, T, VEC>((p.v ? v : k) + p.b * st.batch + p.i * st.token +
-                                         p.h * st.head + i * 4);
+  float values[4];
+  load4<T, VEC>(values, (p.v ? v : k) + p.b * st.batch + p.i * st.token + p.h * st.head + i * 4);
+  const Coded x = code_vector<D>(values);
   if (p.slot < 0) return;
   const int64_t token = kv_token(c, p.b, p.h, p.slot);
   if (token < 0) return;
@@ -233,20 +232,18 @@ __global__ __launch_bounds__(256) void read_kernel(KvView c, int n, T *k, KvStri
 }
 
 // Packed tokens, each with its slot among all the pages.  Four tokens that follow
-// each other are neighbours, K before V, then heads, so that what they write of a
-// block of V mostly comes from one wave.
+// each other are neighbours, then heads, so that what they write of a block of V
+// mostly comes from one wave.
 struct PackedPlace {
   int64_t t, slot;
   int h;
-  bool v;
 };
 __device__ __forceinline__ PackedPlace packed_place(const KvView &c, const int64_t *slots, int T,
-                                                    uint32_t vec) {
+                                                    uint32_t pair) {
   PackedPlace p;
-  p.v = vec >> 2 & 1;
-  const uint32_t quad = (vec >> 3) / (uint32_t)c.H;
-  p.h = (int)((vec >> 3) - quad * (uint32_t)c.H);
-  p.t = (int64_t)quad * 4 + (vec & 3);
+  const uint32_t quad = (pair >> 2) / (uint32_t)c.H;
+  p.h = (int)((pair >> 2) - quad * (uint32_t)c.H);
+  p.t = (int64_t)quad * 4 + (pair & 3);
   p.slot = p.t < T ? slots[p.t] : -1;
   return p;
 }
@@ -258,37 +255,41 @@ __device__ __forceinline__ int64_t slot_token(const KvView &c, int64_t slot, int
   return ((page * c.H + h) << c.page_log) + (slot & ((1 << c.page_log) - 1));
 }
 
+// A token's K and V of a head by D/4 lanes.
 template <int D, typename T, bool VEC>
 __global__ __launch_bounds__(256) void append_slots_kernel(KvView c, int n, const int64_t *slots,
                                                            const T *k, KvStrides ks, const T *v,
-                                                           KvStrides vs, uint32_t vecs) {
+                                                           KvStrides vs, uint32_t pairs) {
   constexpr int L = D / 4;
-  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const uint32_t pair = blockIdx.x * (256 / L) + threadIdx.x / L;
   const int i = threadIdx.x % L;
-  if (vec >= vecs) return;
-  const PackedPlace p = packed_place(c, slots, n, vec);
-  // the vector is on its way while its slot is read
-  const KvStrides st = p.v ? vs : ks;
+  if (pair >= pairs) return;  // whole groups of L lanes leave together
+  const PackedPlace p = packed_place(c, slots, n, pair);
+  // the vectors are on their way while their slot is read
   const int64_t t = min(p.t, (int64_t)n - 1);
-  const Coded x =
-      code_vector<D, T, VEC>((p.v ? v : k) + t * st.token + p.h * st.head + i * 4);
+  float x[4], y[4];
+  load4<T, VEC>(x, k + t * ks.token + p.h * ks.head + i * 4);
+  load4<T, VEC>(y, v + t * vs.token + p.h * vs.head + i * 4);
   const int64_t token = slot_token(c, p.slot, p.h);
-  if (token >= 0) put_vector<D>(c, x, token, p.v, i);
+  const Coded kc = code_vector<D>(x), vc = code_vector<D>(y);
+  if (token < 0) return;
+  put_vector<D>(c, kc, token, false, i);
+  put_vector<D>(c, vc, token, true, i);
 }
 
 template <int D, typename T, bool VEC>
 __global__ __launch_bounds__(256) void read_slots_kernel(KvView c, int n, const int64_t *slots,
                                                          T *k, KvStrides ks, T *v, KvStrides vs,
-                                                         uint32_t vecs) {
+                                                         uint32_t pairs) {
   constexpr int L = D / 4;
-  const uint32_t vec = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const uint32_t pair = blockIdx.x * (256 / L) + threadIdx.x / L;
   const int i = threadIdx.x % L;
-  if (vec >= vecs) return;
-  const PackedPlace p = packed_place(c, slots, n, vec);
+  if (pair >= pairs) return;
+  const PackedPlace p = packed_place(c, slots, n, pair);
   if (p.t >= n) return;
-  const KvStrides st = p.v ? vs : ks;
-  get_vector<D, T, VEC>(c, (p.v ? v : k) + p.t * st.token + p.h * st.head + i * 4,
-                        slot_token(c, p.slot, p.h), p.v, i);
+  const int64_t token = slot_token(c, p.slot, p.h);
+  get_vector<D, T, VEC>(c, k + p.t * ks.token + p.h * ks.head + i * 4, token, false, i);
+  get_vector<D, T, VEC>(c, v + p.t * vs.token + p.h * vs.head + i * 4, token, true, i);
 }
 
 bool vec_ok(const void *p, KvStrides s, size_t size) {
@@ -326,22 +327,22 @@ hipError_t read_dim(const KvView &c, int n, void *k, KvStrides ks, void *v, KvSt
 template <int D, typename T, typename K>
 hipError_t slots_dim(const KvView &c, int n, const int64_t *slots, K *k, KvStrides ks, K *v,
                      KvStrides vs, hipStream_t s) {
-  const uint32_t vecs = (uint32_t)c.H * 8 * (((uint32_t)n + 3) / 4), per = 256 / (D / 4);
-  const uint32_t grid = (vecs + per - 1) / per;
+  const uint32_t pairs = (uint32_t)c.H * 4 * (((uint32_t)n + 3) / 4), per = 256 / (D / 4);
+  const uint32_t grid = (pairs + per - 1) / per;
   const bool vec = vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T));
   if constexpr (std::is_const<K>::value) {
     if (vec)
       append_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (const T *)k, ks,
-                                                           (const T *)v, vs, vecs);
+                                                           (const T *)v, vs, pairs);
     else
       append_slots_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, slots, (const T *)k, ks,
-                                                            (const T *)v, vs, vecs);
+                                                            (const T *)v, vs, pairs);
   } else {
     if (vec)
-      read_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs, vecs);
+      read_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs, pairs);
     else
       read_slots_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs,
-                                                          vecs);
+                                                          pairs);
   }
   return hipGetLastError();
 }
