@@ -99,28 +99,47 @@ struct Coded {
 // Of 16 lanes, the value N lanes further on, the first behind the last.
 template <int N>
 __device__ __forceinline__ float rotated(float x) {
-  return __int_as_float(
-      __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x130 - N, 0xf, 0xf, false));
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x130 - N, 0xf, 0xf, false));
 }
 template <int N>
-__device__ __forceinline__ void extremes(float &lo, float &hi) {
+__device__ __forceinline__ void ordered_extremes(float &lo, float &hi) {
   lo = nan_min(lo, rotated<N>(lo));
   hi = nan_max(hi, rotated<N>(hi));
 }
+template <int N>
+__device__ __forceinline__ void extremes(float &lo, float &hi) {
+  lo = __builtin_elementwise_minimum(lo, rotated<N>(lo));
+  hi = __builtin_elementwise_maximum(hi, rotated<N>(hi));
+}
 template <int D>
 __device__ __forceinline__ Coded code_vector(const float (&x)[4]) {
-  float lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
-  float hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
-  // in the order of a butterfly for lane 0, which stores them: a zero's sign is that of
-  // the last one among equals
+  const auto least = [](float a, float b) { return __builtin_elementwise_minimum(a, b); };
+  const auto largest = [](float a, float b) { return __builtin_elementwise_maximum(a, b); };
+  float lo = least(least(x[0], x[1]), least(x[2], x[3]));
+  float hi = largest(largest(x[0], x[1]), largest(x[2], x[3]));
   extremes<1>(lo, hi);
   extremes<2>(lo, hi);
   extremes<4>(lo, hi);
   extremes<8>(lo, hi);
 #pragma unroll
   for (int d = 16; d < D / 4; d <<= 1) {
-    lo = nan_min(lo, __shfl_xor(lo, d));
-    hi = nan_max(hi, __shfl_xor(hi, d));
+    lo = least(lo, __shfl_xor(lo, d));
+    hi = largest(hi, __shfl_xor(hi, d));
+  }
+  // Which of zeros of both signs, and of NaN, is stored depends on the order: there it is
+  // that of a butterfly for lane 0, which stores it, the later one winning.
+  if (__builtin_expect(__any(!(fabsf(lo) > 0.f)), 0)) {
+    lo = nan_min(nan_min(x[0], x[1]), nan_min(x[2], x[3]));
+    hi = nan_max(nan_max(x[0], x[1]), nan_max(x[2], x[3]));
+    ordered_extremes<1>(lo, hi);
+    ordered_extremes<2>(lo, hi);
+    ordered_extremes<4>(lo, hi);
+    ordered_extremes<8>(lo, hi);
+#pragma unroll
+    for (int d = 16; d < D / 4; d <<= 1) {
+      lo = nan_min(lo, __shfl_xor(lo, d));
+      hi = nan_max(hi, __shfl_xor(hi, d));
+    }
   }
   float step = (hi - lo) * (1.f / 15.f);
   asm volatile("" : "+v"(step));  // rounded to fp32 first: one instruction could do both at once
@@ -129,25 +148,26 @@ __device__ __forceinline__ Coded code_vector(const float (&x)[4]) {
   const bool good = (float)near_step < INFINITY && fabsf(zero) < INFINITY;
   const _Float16 sh = good ? near_step : (_Float16)NAN;
   const float scale = (float)sh;
-  uint32_t word = 0;
-  // the quotient's neighbour y * (1 / scale) is less than 1e-5 off it and rounds
+  // the quotient's neighbour y * rcp(scale) is less than 1e-5 off it and rounds
   // to the same integer unless it lies that close to a half
-  const float inv = scale > 0.f ? 1.f / scale : 0.f;
-  float q[4];
-  bool near = false;
+  const float inv = __builtin_amdgcn_rcpf(scale);
+  float q[4], off[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float y = (x[e] - zero) * inv;
     q[e] = rintf(y);
-    near |= !(fabsf(y - q[e]) < 0.4999f);
+    off[e] = fabsf(y - q[e]);
   }
-  if (__builtin_expect(near, 0) && scale > 0.f) {
+  const bool near = !(fmaxf(fmaxf(off[0], off[1]), fmaxf(off[2], off[3])) < 0.4999f);
+  if (__builtin_expect(near, 0)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) q[e] = rintf((x[e] - zero) / scale);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    word |= (scale > 0.f ? (uint32_t)fminf(fmaxf(q[e], 0.f), 15.f) : 0u) << (4 * e);
+  for (int e = 0; e < 4; ++e) q[e] = __builtin_amdgcn_fmed3f(q[e], 0.f, 15.f);
+  // whole numbers below 2^16, so their sum in fp32 is exact
+  const float all = fmaf(q[3], 4096.f, fmaf(q[2], 256.f, fmaf(q[1], 16.f, q[0])));
+  const uint32_t word = scale > 0.f ? (uint32_t)all : 0u;
   return {word, sh, zh};
 }
 // Stored as K or V of cached token `token` (lane i of the vector's).
@@ -231,65 +251,63 @@ __global__ __launch_bounds__(256) void read_kernel(KvView c, int n, T *k, KvStri
                         token, p.v, i);
 }
 
-// Packed tokens, each with its slot among all the pages.  Four tokens that follow
-// each other are neighbours, then heads, so that what they write of a block of V
-// mostly comes from one wave.
+// Packed tokens, each with its slot among all the pages: a workgroup has a head's K and
+// V of 1024 / D tokens that follow each other, D/4 lanes a token, so that what is
+// written of a block of V mostly comes from one wave.  Places are formed once a
+// workgroup, but for the token within it.
+template <int D>
 struct PackedPlace {
-  int64_t t, slot;
-  int h;
+  static constexpr int L = D / 4, PER = 256 / L;
+  int64_t t0;  // the workgroup's first token
+  int h, i, j, last;
+  // workgroups past the last token have none
+  __device__ __forceinline__ PackedPlace(int n) {
+    h = blockIdx.x;
+    i = threadIdx.x % L;
+    t0 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * PER;
+    last = (int)min((int64_t)PER, n - t0) - 1;
+    j = min((int)threadIdx.x / L, last);
+  }
+  __device__ __forceinline__ bool mine() const { return (int)threadIdx.x / L <= last; }
+  __device__ __forceinline__ int64_t at(const KvStrides &s) const {
+    return t0 * s.token + (int64_t)h * s.head + (int64_t)j * s.token + i * 4;
+  }
 };
-__device__ __forceinline__ PackedPlace packed_place(const KvView &c, const int64_t *slots, int T,
-                                                    uint32_t pair) {
-  PackedPlace p;
-  const uint32_t quad = (pair >> 2) / (uint32_t)c.H;
-  p.h = (int)((pair >> 2) - quad * (uint32_t)c.H);
-  p.t = (int64_t)quad * 4 + (pair & 3);
-  p.slot = p.t < T ? slots[p.t] : -1;
-  return p;
-}
 // Index of a slot's token within all the pages of cached head h, as kv_token, or -1
 // for a slot that no page has.
 __device__ __forceinline__ int64_t slot_token(const KvView &c, int64_t slot, int h) {
   const int64_t page = slot >> c.page_log;
   if ((uint64_t)page >= (uint64_t)c.num_pages) return -1;
-  return ((page * c.H + h) << c.page_log) + (slot & ((1 << c.page_log) - 1));
+  const int64_t rows = (int64_t)((uint64_t)(uint32_t)page * (uint32_t)c.H + (uint32_t)h);
+  return (rows << c.page_log) + ((int)slot & ((1 << c.page_log) - 1));
 }
 
-// A token's K and V of a head by D/4 lanes.
 template <int D, typename T, bool VEC>
 __global__ __launch_bounds__(256) void append_slots_kernel(KvView c, int n, const int64_t *slots,
                                                            const T *k, KvStrides ks, const T *v,
-                                                           KvStrides vs, uint32_t pairs) {
-  constexpr int L = D / 4;
-  const uint32_t pair = blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int i = threadIdx.x % L;
-  if (pair >= pairs) return;  // whole groups of L lanes leave together
-  const PackedPlace p = packed_place(c, slots, n, pair);
-  // the vectors are on their way while their slot is read
-  const int64_t t = min(p.t, (int64_t)n - 1);
+                                                           KvStrides vs) {
+  const PackedPlace<D> p(n);
+  if (p.last < 0) return;
+  const int64_t slot = slots[p.t0 + p.j];
   float x[4], y[4];
-  load4<T, VEC>(x, k + t * ks.token + p.h * ks.head + i * 4);
-  load4<T, VEC>(y, v + t * vs.token + p.h * vs.head + i * 4);
-  const int64_t token = slot_token(c, p.slot, p.h);
+  load4<T, VEC>(x, k + p.at(ks));
+  load4<T, VEC>(y, v + p.at(vs));
   const Coded kc = code_vector<D>(x), vc = code_vector<D>(y);
-  if (token < 0) return;
-  put_vector<D>(c, kc, token, false, i);
-  put_vector<D>(c, vc, token, true, i);
+  const int64_t token = slot_token(c, slot, p.h);
+  if (token < 0 || !p.mine()) return;
+  put_vector<D>(c, kc, token, false, p.i);
+  put_vector<D>(c, vc, token, true, p.i);
 }
 
 template <int D, typename T, bool VEC>
 __global__ __launch_bounds__(256) void read_slots_kernel(KvView c, int n, const int64_t *slots,
-                                                         T *k, KvStrides ks, T *v, KvStrides vs,
-                                                         uint32_t pairs) {
-  constexpr int L = D / 4;
-  const uint32_t pair = blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int i = threadIdx.x % L;
-  if (pair >= pairs) return;
-  const PackedPlace p = packed_place(c, slots, n, pair);
-  if (p.t >= n) return;
-  const int64_t token = slot_token(c, p.slot, p.h);
-  get_vector<D, T, VEC>(c, k + p.t * ks.token + p.h * ks.head + i * 4, token, false, i);
-  get_vector<D, T, VEC>(c, v + p.t * vs.token + p.h * vs.head + i * 4, token, true, i);
+                                                         T *k, KvStrides ks, T *v,
+                                                         KvStrides vs) {
+  const PackedPlace<D> p(n);
+  if (p.last < 0 || !p.mine()) return;
+  const int64_t token = slot_token(c, slots[p.t0 + p.j], p.h);
+  get_vector<D, T, VEC>(c, k + p.at(ks), token, false, p.i);
+  get_vector<D, T, VEC>(c, v + p.at(vs), token, true, p.i);
 }
 
 bool vec_ok(const void *p, KvStrides s, size_t size) {
@@ -327,22 +345,22 @@ hipError_t read_dim(const KvView &c, int n, void *k, KvStrides ks, void *v, KvSt
 template <int D, typename T, typename K>
 hipError_t slots_dim(const KvView &c, int n, const int64_t *slots, K *k, KvStrides ks, K *v,
                      KvStrides vs, hipStream_t s) {
-  const uint32_t pairs = (uint32_t)c.H * 4 * (((uint32_t)n + 3) / 4), per = 256 / (D / 4);
-  const uint32_t grid = (pairs + per - 1) / per;
+  const uint32_t groups = ((uint32_t)n + PackedPlace<D>::PER - 1) / PackedPlace<D>::PER;
+  const uint32_t deep = (groups + 65534) / 65535;  // a grid's limit but for x
+  const dim3 grid(c.H, (groups + deep - 1) / deep, deep);
   const bool vec = vec_ok(k, ks, sizeof(T)) && vec_ok(v, vs, sizeof(T));
   if constexpr (std::is_const<K>::value) {
     if (vec)
       append_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (const T *)k, ks,
-                                                           (const T *)v, vs, pairs);
+                                                           (const T *)v, vs);
     else
       append_slots_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, slots, (const T *)k, ks,
-                                                            (const T *)v, vs, pairs);
+                                                            (const T *)v, vs);
   } else {
     if (vec)
-      read_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs, pairs);
+      read_slots_kernel<D, T, true><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs);
     else
-      read_slots_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs,
-                                                          pairs);
+      read_slots_kernel<D, T, false><<<grid, 256, 0, s>>>(c, n, slots, (T *)k, ks, (T *)v, vs);
   }
   return hipGetLastError();
 }
