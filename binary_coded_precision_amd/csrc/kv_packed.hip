@@ -152,6 +152,18 @@ __device__ __forceinline__ int chunk_of(const PackedArgs &a, float cost) {
 #pragma clang fp contract(off)
   return max(1, (int)fminf(ceilf(cost * (float)a.c.H * (1.f / kTarget)), (float)(1 << 24)));
 }
+// A share of 128 rows costs its partial rows too, written and read again: with all the
+// compute units at it some 0.03 of a step (half of that for rows of half the work).  N
+// shares of c steps, W = N c in all, take c + 0.03 N steps, least for c = sqrt(0.03 W);
+// 0.02 a unit of weight is what measured best.  It counts where the card is not full
+// without: a prompt's 225 tokens in 40 heads 24 us, cut for 512 workgroups 31; 30 tokens
+// of five in 28 heads of 256 channels 17 and 21.5.
+template <int U>
+__device__ __forceinline__ int wide_chunk_of(const PackedArgs &a, int chunk, float cost) {
+#pragma clang fp contract(off)
+  constexpr float kPart = 0.06f * (1 + U / 16);
+  return max(chunk, (int)sqrtf(kPart * (float)a.c.H * cost));
+}
 __device__ __forceinline__ int shares_of(int steps, int weight, int chunk, int most) {
   const int by_chunk = (steps * weight + chunk - 1) / chunk;
   return min(max(max(by_chunk, (steps + kMostSteps - 1) / kMostSteps), 1), most);
@@ -162,7 +174,7 @@ template <int U>
 struct Whole {
   PlanHead h{};
   bool together;
-  int few_blocks = 0, few_steps = 0, few_weight = 0, chunk, most, used = 0;
+  int few_blocks = 0, few_steps = 0, few_weight = 0, chunk, wide_chunk, most, used = 0;
 
   // sequences with few rows, and their tokens
   __device__ __forceinline__ Whole(const PackedArgs &a, int seqs, int tokens) {
@@ -178,12 +190,14 @@ struct Whole {
     most = together ? kMaxShares / 2 : kMaxShares;
   }
   // the weight of all the sequences' own steps
-  __device__ __forceinline__ void divide(const PackedArgs &a, float cost) {
+  __device__ __forceinline__ void divide(const PackedArgs &a, float cost, float wide_cost) {
 #pragma clang fp contract(off)
-    cost += weight_of(few_blocks, few_steps, few_weight);
-    chunk = chunk_of(a, cost);
+    const bool wide_few = h.few * a.G > kFewRows;
+    const float few_cost = weight_of(few_blocks, few_steps, few_weight);
+    chunk = chunk_of(a, cost + few_cost);
+    wide_chunk = wide_chunk_of<U>(a, chunk, wide_cost + (wide_few ? few_cost : 0.f));
     if (!together) return;
-    h.few_shares = shares_of(few_steps, few_weight, chunk, most);
+    h.few_shares = shares_of(few_steps, few_weight, wide_few ? wide_chunk : chunk, most);
     // The shared items are much alike and start first, one on each compute unit, then a
     // second: with a second on half of the units the others would wait for those.  So
     // whole turns of them, the sequences' own items beside the last.  64 decode steps
@@ -201,7 +215,7 @@ struct Whole {
   // shares of a sequence's blocks, and the partial rows that they leave
   __device__ __forceinline__ int shares(const Seq &q) const {
     if (q.blocks == 0 || (together && q.few && q.steps == 0)) return 0;
-    return shares_of(q.steps, q.weight, chunk, most);
+    return shares_of(q.steps, q.weight, q.rows > kFewRows ? wide_chunk : chunk, most);
   }
   __device__ __forceinline__ int rows(const Seq &q, int shares) const {
     return shares > 1 || (together && q.few) ? product(q.rows, shares) : 0;
@@ -232,7 +246,8 @@ __device__ __forceinline__ LanePlan lane_plan(const PackedArgs &a, int lane) {
   const int few = lane_scan(p.q.few ? p.q.n : 0);
   Whole<U> whole(a, __popcll(__ballot(p.q.few)), last_lane(few));
   shape<U>(p.q, whole.h.base);
-  whole.divide(a, lane_sum(weight_of(p.q.blocks, p.q.steps, p.q.weight)));
+  const float weight = weight_of(p.q.blocks, p.q.steps, p.q.weight);
+  whole.divide(a, lane_sum(weight), lane_sum(p.q.rows > kFewRows ? weight : 0.f));
   p.shares = whole.shares(p.q);
   const int rows = whole.rows(p.q, p.shares), end = capped(whole.used, lane_scan(rows));
   if (rows > 0 && end > a.part_cap) p.shares = 0;  // starts that are none
@@ -298,13 +313,15 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PackedArgs a) {
     tokens = capped(tokens, block_scan<kWaves>(q.few ? q.n : 0, part).y);
   }
   Whole<U> whole(a, seqs, tokens);
-  float cost = 0.f;
+  float cost = 0.f, wide_cost = 0.f;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     Seq q = seq_at<U>(a, b0 + tid);
     shape<U>(q, whole.h.base);
-    cost += sum_of(weight_of(q.blocks, q.steps, q.weight), partf);
+    const float weight = weight_of(q.blocks, q.steps, q.weight);
+    cost += sum_of(weight, partf);
+    wide_cost += sum_of(q.rows > kFewRows ? weight : 0.f, partf);
   }
-  whole.divide(a, cost);
+  whole.divide(a, cost, wide_cost);
   int used = whole.used, items = whole.h.few_items, few_before = 0, split = 0, splits = 0;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     const int b = b0 + tid;
@@ -810,14 +827,13 @@ __device__ __forceinline__ void join_row(const PackedArgs &a, int64_t own, int64
     store_out(a, out + c * 64 + lane, l == 0.f ? 0.f : o[c] / l, F32);
 }
 
-// A wave a row at a time: blocks [0, few_blocks) for the rows of sequences with few of
-// them, the others for what is split of those with many.  Every block works the plan out,
-// so there are no more than the card holds at once a few times over: 31 decode steps
-// beside 1024 rows of a prompt 206 us (4096 + 1024 blocks 211, 512 + 512 217, 1024 + 8192
-// 210).
-constexpr int kJoinsFew = 1024, kJoinsMany = 2048;
+// A wave a row at a time, those of sequences with few of them first, then what is split of
+// those with many.  Every wave works the plan out, so there are no more than the card
+// holds at once: 31 decode steps beside a prompt's 1024 tokens 206 us (1024 workgroups
+// 210, 4096 207, 8192 210).
+constexpr int kJoins = 2048;
 template <int D, bool F32, bool SMALL>
-__global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a, int few_blocks) {
+__global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   LanePlan p;
@@ -829,9 +845,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a, int few_bl
     h = *a.head;
   }
   const int Hq = a.G * a.c.H;
-  if ((int)blockIdx.x < few_blocks) {
-    for (int64_t r = (int64_t)blockIdx.x * kWaves + wave; r < (int64_t)h.few * Hq;
-         r += (int64_t)few_blocks * kWaves) {
+  const int64_t few = (int64_t)h.few * Hq, all = few + (int64_t)h.split * a.c.H;
+  for (int64_t r = (int64_t)blockIdx.x * kWaves + wave; r < all;
+       r += (int64_t)gridDim.x * kWaves) {
+    if (r < few) {
       const int k = (int)(r / Hq), hq = (int)(r % Hq), g = hq % a.G;
       FewToken t;
       if constexpr (SMALL) {
@@ -850,13 +867,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a, int few_bl
       join_row<D, F32>(a, at + t.part + g, t.rows_shares >> 8, t.part < 0 ? 0 : t.rows_shares & 255,
                        at + k * a.G + g, h.few * a.G, h.base > 0 ? h.few_shares : 0,
                        t.token * a.o_token + hq * a.o_head, lane);
+      continue;
     }
-    return;
-  }
-  const int64_t stride = (int64_t)(gridDim.x - few_blocks) * kWaves;
-  for (int64_t r = (int64_t)(blockIdx.x - few_blocks) * kWaves + wave;
-       r < (int64_t)h.split * a.c.H; r += stride) {
-    const int row = (int)(r / a.c.H), head = (int)(r % a.c.H);
+    const int row = (int)((r - few) / a.c.H), head = (int)((r - few) % a.c.H);
     SplitSeq s;
     if constexpr (SMALL) {
       const uint64_t whose = __ballot(p.many && row >= p.split && row - p.split < p.q.rows);
@@ -934,15 +947,13 @@ hipError_t launch_dim(PackedArgs a, int q_heads, void *ws, hipStream_t s) {
   a.ml = reinterpret_cast<float2 *>(w + p.off_ml);
   a.o = reinterpret_cast<float *>(w + p.off_o);
   a.item_cap = p.item_cap, a.few_cap = p.few_cap, a.part_cap = (int)p.part_cap;
-  const int few_blocks =
-      (int)std::min<int64_t>(((int64_t)p.few_cap * q_heads + kWaves - 1) / kWaves, kJoinsFew);
-  const int joins = few_blocks + ((int64_t)a.max_n * a.G > 2 * wave_rows(D) ? kJoinsMany : 0);
+  const int joins = (int)std::min<int64_t>(((int64_t)a.T * q_heads + kWaves - 1) / kWaves, kJoins);
   const int most = kMaxGroups / a.c.H;
   if (a.c.B <= 64 && p.item_cap <= most) {
     packed_kernel<D, F32, true><<<(unsigned)p.item_cap * a.c.H, kThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    join_kernel<D, F32, true><<<joins, kThreads, 0, s>>>(a, few_blocks);
+    join_kernel<D, F32, true><<<joins, kThreads, 0, s>>>(a);
     return hipGetLastError();
   }
   plan_kernel<wave_rows(D)><<<1, kThreads, 0, s>>>(a);
@@ -952,7 +963,7 @@ hipError_t launch_dim(PackedArgs a, int q_heads, void *ws, hipStream_t s) {
       <<<(unsigned)std::min(p.item_cap, most) * a.c.H, kThreads, 0, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  join_kernel<D, F32, false><<<joins, kThreads, 0, s>>>(a, few_blocks);
+  join_kernel<D, F32, false><<<joins, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
