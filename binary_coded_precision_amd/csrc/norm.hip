@@ -83,12 +83,23 @@ __device__ __forceinline__ void scale_row8(float (&y)[8], const float (&h)[8], f
   for (int e = 0; e < 8; ++e) y[e] = (h[e] * inv) * g[e];
 }
 
-// One workgroup a row.  Rows of up to 8 N THREADS elements are held in registers;
+// A row by THREADS threads.  Rows of up to 8 N THREADS elements are held in registers;
 // longer ones (N = 0) are read again from the caches for each of three passes.
+//
+// Bound by the bytes of x, the residual, h, y and codes, each passed once: 4096 x 4096 in
+// fp16 with h and codes (117 MB) 24.7 us, 4.7 TB/s; 30000 x 512 25 us, 4.3 TB/s.  Few
+// rows are bound by one pass's latency, 3 us for one of 4096.
+//
+// Rows of up to 512 elements are a wave's, four to a workgroup: as fast as a workgroup a
+// row for one row (4.0 us), 25 us rather than 59 for 30000 rows of 512, which are bound
+// by workgroups started.  Rows of up to 1024 too from 4096 of them on (30000 x 1024 41 us,
+// not 68; 1024 rows take the same, one row 4.6 us, not 3.9).  With more than that in a
+// wave's registers, or longer rows, more threads are better (1 x 2048: 4.3 us, by one
+// wave 6.8).
 template <typename T, int N, int THREADS>
 __device__ __forceinline__ void norm_row(const NormArgs &a, int64_t row, double *red_sum,
                                          float *red_max) {
-  const int tid = threadIdx.x, K = a.K;
+  const int tid = threadIdx.x % THREADS, K = a.K;
   const T *x = static_cast<const T *>(a.x) + row * a.ldx;
   const T *r = a.residual == nullptr ? nullptr
                                      : static_cast<const T *>(a.residual) + row * a.ldr;
@@ -163,10 +174,13 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int64_t row, double 
 }
 
 template <typename T, int N, int THREADS>
-__global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a, int rows) {
+__global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void norm_kernel(NormArgs a, int rows) {
   __shared__ double red_sum[THREADS / 64];
   __shared__ float red_max[THREADS / 64];
-  if constexpr (THREADS <= 256) {
+  if constexpr (THREADS == 64) {
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row < rows) norm_row<T, N, THREADS>(a, row, nullptr, nullptr);
+  } else if constexpr (THREADS == 256) {
     norm_row<T, N, THREADS>(a, blockIdx.x, red_sum, red_max);
   } else {
     // a launch's work items are counted in 32 bits: more rows take turns
@@ -181,7 +195,12 @@ template <typename T>
 hipError_t norm_type(const NormArgs &a, int rows, hipStream_t s) {
   constexpr int kMostRows = (1 << 22) - 1;  // of 1024 threads
   const int turns = rows < kMostRows ? rows : kMostRows;
-  if (a.K <= 2048)
+  const int quads = (int)(((int64_t)rows + 3) / 4);
+  if (a.K <= 512)
+    norm_kernel<T, 1, 64><<<quads, 256, 0, s>>>(a, rows);
+  else if (a.K <= 1024 && rows >= 4096)
+    norm_kernel<T, 2, 64><<<quads, 256, 0, s>>>(a, rows);
+  else if (a.K <= 2048)
     norm_kernel<T, 1, 256><<<rows, 256, 0, s>>>(a, rows);
   else if (a.K <= 4096)
     norm_kernel<T, 2, 256><<<rows, 256, 0, s>>>(a, rows);
