@@ -95,7 +95,9 @@ __device__ __forceinline__ void scale_row8(float (&y)[8], const float (&h)[8], f
 // by workgroups started.  Rows of up to 1024 too from 4096 of them on (30000 x 1024 41 us,
 // not 68; 1024 rows take the same, one row 4.6 us, not 3.9).  With more than that in a
 // wave's registers, or longer rows, more threads are better (1 x 2048: 4.3 us, by one
-// wave 6.8).
+// wave 6.8).  Longer rows than 2048 are 512 threads' where there is at most one for each
+// compute unit (1 x 8192 5.6 us, by 256 threads 7.0), else 256 threads', which leave room
+// for more rows (8192 x 4096 41 us, by 512 threads 49).
 template <typename T, int N, int THREADS>
 __device__ __forceinline__ void norm_row(const NormArgs &a, int64_t row, double *red_sum,
                                          float *red_max) {
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void norm_kernel(Nor
   if constexpr (THREADS == 64) {
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (row < rows) norm_row<T, N, THREADS>(a, row, nullptr, nullptr);
-  } else if constexpr (THREADS == 256) {
+  } else if constexpr (THREADS <= 512) {
     norm_row<T, N, THREADS>(a, blockIdx.x, red_sum, red_max);
   } else {
     // a launch's work items are counted in 32 bits: more rows take turns
@@ -195,6 +197,7 @@ template <typename T>
 hipError_t norm_type(const NormArgs &a, int rows, hipStream_t s) {
   constexpr int kMostRows = (1 << 22) - 1;  // of 1024 threads
   const int turns = rows < kMostRows ? rows : kMostRows;
+  const bool few = rows <= 256;
   const int quads = (int)(((int64_t)rows + 3) / 4);
   if (a.K <= 512)
     norm_kernel<T, 1, 64><<<quads, 256, 0, s>>>(a, rows);
@@ -202,6 +205,10 @@ hipError_t norm_type(const NormArgs &a, int rows, hipStream_t s) {
     norm_kernel<T, 2, 64><<<quads, 256, 0, s>>>(a, rows);
   else if (a.K <= 2048)
     norm_kernel<T, 1, 256><<<rows, 256, 0, s>>>(a, rows);
+  else if (a.K <= 4096 && few)
+    norm_kernel<T, 1, 512><<<rows, 512, 0, s>>>(a, rows);
+  else if (a.K <= 8192 && few)
+    norm_kernel<T, 2, 512><<<rows, 512, 0, s>>>(a, rows);
   else if (a.K <= 4096)
     norm_kernel<T, 2, 256><<<rows, 256, 0, s>>>(a, rows);
   else if (a.K <= 8192)
