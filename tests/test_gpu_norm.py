@@ -184,7 +184,8 @@ def test_more_long_rows_than_a_launch_has_room_for():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("T,K", [(4095, 1000), (4097, 1000), (4099, 513), (4101, 72), (4096, 1024)])
+@pytest.mark.parametrize("T,K", [(4095, 1000), (4097, 1000), (4099, 513), (4101, 72), (4096, 1024),
+                                 (256, 4096), (257, 4096), (300, 2050), (257, 8191)])
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
-def test_many_short_rows(T, K, dtype):
+def test_many_rows(T, K, dtype):
     test_norm(T, K, dtype)
