@@ -791,40 +791,59 @@ __global__ __launch_bounds__(kThreads, 2) void packed_kernel(PackedArgs a) {
   }
 }
 
-// Joins the shares of one row: own ones [own, + stride, ..), then the shared pages'.
-template <int D, bool F32>
-__device__ __forceinline__ void join_row(const PackedArgs &a, int64_t own, int64_t stride,
-                                         int shares, int64_t few, int64_t few_stride,
-                                         int few_shares, int64_t out, int lane) {
+// Joins the shares of ROWS rows, which have the same number of them: own ones [own, +
+// stride, ..), then the shared pages'.
+template <int ROWS>
+struct JoinRows {
+  int64_t own[ROWS], few[ROWS], out[ROWS];
+  int live;  // of them; the others are not stored
+};
+template <int D, bool F32, int ROWS>
+__device__ __forceinline__ void join_rows(const PackedArgs &a, const JoinRows<ROWS> &j,
+                                          int64_t stride, int shares, int64_t few_stride,
+                                          int few_shares, int lane) {
   const int all = shares + few_shares;
-  const auto place = [&](int s) {
-    return s < shares ? own + s * stride : few + (s - shares) * few_stride;
+  const auto place = [&](int k, int s) {
+    return s < shares ? j.own[k] + s * stride : j.few[k] + (s - shares) * few_stride;
   };
-  const float2 x = lane < all ? a.ml[place(lane)] : make_float2(kNegInf, 0.f);
-  float m = x.x;
+  float2 x[ROWS];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const float f = x.x == kNegInf ? 0.f : exp2f(x.x - m);
-  float l = x.y * f;
+  for (int k = 0; k < ROWS; ++k)
+    x[k] = lane < all ? a.ml[place(k, lane)] : make_float2(kNegInf, 0.f);
+  float f[ROWS], l[ROWS], o[ROWS][D / 64] = {};
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-  float o[D / 64] = {};
+  for (int k = 0; k < ROWS; ++k) {
+    float m = x[k].x;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    f[k] = x[k].x == kNegInf ? 0.f : exp2f(x[k].x - m);
+    l[k] = x[k].y * f[k];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) l[k] += __shfl_xor(l[k], d);
+  }
   for (int s0 = 0; s0 < all; s0 += 4) {  // four shares' reads in flight
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int s = min(s0 + k, all - 1);
-      const float fs = s0 + k < all ? __shfl(f, s) : 0.f;
-      const float *from = a.o + place(s) * D;
+    for (int t = 0; t < 4; ++t) {
+      const int s = min(s0 + t, all - 1);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const float v = from[c * 64 + lane];
-        o[c] += s0 + k < all ? fs * v : 0.f;
+      for (int k = 0; k < ROWS; ++k) {
+        const float fs = s0 + t < all ? __shfl(f[k], s) : 0.f;
+        const float *from = a.o + place(k, s) * D;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const float v = from[c * 64 + lane];
+          o[k][c] += s0 + t < all ? fs * v : 0.f;
+        }
       }
     }
   }
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c)
-    store_out(a, out + c * 64 + lane, l == 0.f ? 0.f : o[c] / l, F32);
+  for (int k = 0; k < ROWS; ++k) {
+    if (k >= j.live) continue;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      store_out(a, j.out[k] + c * 64 + lane, l[k] == 0.f ? 0.f : o[k][c] / l[k], F32);
+  }
 }
 
 // A wave a row at a time, those of sequences with few of them first, then what is split of
@@ -845,7 +864,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a) {
     h = *a.head;
   }
   const int Hq = a.G * a.c.H;
-  const int64_t few = (int64_t)h.few * Hq, all = few + (int64_t)h.split * a.c.H;
+  // a split row of two cached heads at a time, so that twice as many reads are on their way:
+  // a prompt's 2252 tokens 62 us, one at a time 67
+  const int halves = (a.c.H + 1) / 2;
+  const int64_t few = (int64_t)h.few * Hq, all = few + (int64_t)h.split * halves;
   for (int64_t r = (int64_t)blockIdx.x * kWaves + wave; r < all;
        r += (int64_t)gridDim.x * kWaves) {
     if (r < few) {
@@ -864,12 +886,13 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a) {
       }
       if (t.part < 0 && h.base == 0) continue;
       const int64_t at = (int64_t)(hq / a.G) * a.part_cap;
-      join_row<D, F32>(a, at + t.part + g, t.rows_shares >> 8, t.part < 0 ? 0 : t.rows_shares & 255,
-                       at + k * a.G + g, h.few * a.G, h.base > 0 ? h.few_shares : 0,
-                       t.token * a.o_token + hq * a.o_head, lane);
+      const JoinRows<1> rows{
+          {at + t.part + g}, {at + k * a.G + g}, {t.token * a.o_token + hq * a.o_head}, 1};
+      join_rows<D, F32, 1>(a, rows, t.rows_shares >> 8, t.part < 0 ? 0 : t.rows_shares & 255,
+                           h.few * a.G, h.base > 0 ? h.few_shares : 0, lane);
       continue;
     }
-    const int row = (int)((r - few) / a.c.H), head = (int)((r - few) % a.c.H);
+    const int row = (int)((r - few) / halves), head = (int)((r - few) % halves);
     SplitSeq s;
     if constexpr (SMALL) {
       const uint64_t whose = __ballot(p.many && row >= p.split && row - p.split < p.q.rows);
@@ -883,9 +906,15 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PackedArgs a) {
         if (j + step < h.splits && a.splits[j + step].row <= row) j += step;
       s = a.splits[j];
     }
-    const int mine = row - s.row, i = mine / a.G, hq = head * a.G + mine - i * a.G;
-    join_row<D, F32>(a, (int64_t)head * a.part_cap + s.part + mine, (int64_t)s.n * a.G, s.shares,
-                     0, 0, 0, (s.start + i) * a.o_token + hq * a.o_head, lane);
+    const int mine = row - s.row, i = mine / a.G, next = min(head + halves, a.c.H - 1);
+    JoinRows<2> rows{{}, {}, {}, head + halves < a.c.H ? 2 : 1};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int at = k == 0 ? head : next;
+      rows.own[k] = (int64_t)at * a.part_cap + s.part + mine;
+      rows.out[k] = (s.start + i) * a.o_token + (int64_t)(at * a.G + mine - i * a.G) * a.o_head;
+    }
+    join_rows<D, F32, 2>(a, rows, (int64_t)s.n * a.G, s.shares, 0, 0, lane);
   }
 }
 
