@@ -283,3 +283,11 @@ def test_the_sign_of_a_zero(D):
         got = got.cpu().numpy().view(np.uint16)[0, 0, :40]
         np.testing.assert_array_equal(got[:, 1], want)
         np.testing.assert_array_equal(got[:, 3], want)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("B,page,shared,longest", [(50, 16, 2, 700), (64, 64, 0, 2000),
+                                                   (65, 16, 0, 3), (200, 16, 1, 3),
+                                                   (256, 256, 1, 2), (257, 32, 0, 20)])
+def test_a_server_of_any_size(B, page, shared, longest, in_place):
+    test_a_server_at_work(B, page, shared, longest, in_place)
