@@ -45,7 +45,10 @@ constexpr int kMostSteps = 2048;  // of 32 tokens, that a wave sums in one go (k
 // Rows of a wave in a block of many rows, tiles of 16 of them.
 constexpr int wave_tiles(int D) { return D <= 128 ? 2 : 1; }
 constexpr int wave_rows(int D) { return 16 * wave_tiles(D); }
-// Rows up to which blocks have 16 and their waves share the tokens.
+// Rows up to which blocks have 16 and their waves share the tokens.  Four waves with rows of
+// their own would leave two or three idle up to 64 rows of 128, but split blocks of 16
+// unpack the codes again for each: past two of them that costs more.  Blocks of 32 with
+// shared tokens took 42 us for 16 x 8 drafted tokens over 3000, two of 16 take 32.
 constexpr int kFewRows = 32;
 struct Shape {
   int blocks, waves, weight;  // waves that share a block's tokens; weight of a step
@@ -557,7 +560,8 @@ __device__ __forceinline__ void clear(Sums<D, CT> &A) {
   }
 }
 
-// An item of few rows: 16 of them, four waves share the tokens.
+// An item of few rows: 16 of them, four waves share the tokens.  A step is bound by its
+// loads: 32 decode steps over 8192 tokens (215 MB) take 48 us, 4.5 TB/s.
 template <int D, bool F32>
 __device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, const Listed *list,
                                         int base, int h, Meet<D> &meet) {
@@ -661,7 +665,12 @@ __device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, cons
   }
 }
 
-// An item of many rows: every wave has rows of its own.
+// An item of many rows: every wave has rows of its own, 32 (16 of 256 channels, as many as
+// its registers hold).  Bound by instructions: a step of 32 rows over 32 tokens of 128
+// channels has 48 matrix instructions and about 300 others, of which unpacking is a
+// third, and the two kinds hardly overlap on a SIMD (48 beside 240: 1033 ns for two
+// waves, alone 665 and 543).  Six prompts of 2334 to 4001 tokens, 443 us at the rate of a
+// large matrix product, take 805 us; the probabilities' second fp16 is 16 of the 48.
 template <int D, bool F32>
 __device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, const Listed *list,
                                          int base, int h) {
@@ -755,7 +764,9 @@ __device__ __forceinline__ void run(const PackedArgs &a, const Item &x, const Li
     run_many<D, F32>(a, x, list, base, h);
 }
 
-// SMALL: up to 64 sequences, and a workgroup for each item that there can be.
+// SMALL: up to 64 sequences, and a workgroup for each item that there can be.  The smallest
+// calls are a chain of latencies: lengths, pages, codes, then partial rows (8.8 us, and
+// 4.4 for the join).
 template <int D, bool F32, bool SMALL>
 __global__ __launch_bounds__(kThreads, 2) void packed_kernel(PackedArgs a) {
   __shared__ Meet<D> meet;
@@ -923,7 +934,8 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 // How many items, tokens and partial rows a call can have.  With C the blocks' steps
 // in all, shares have at least C H / kTarget steps, so that the sum of steps / share
 // over the blocks is at most kTarget / H (and kNearTurn / H for the shared pages'), and a
-// block has at most one share more than that; where kMostSteps cuts a block further, it has at most `past` besides.
+// block has at most one share more than that; where kMostSteps cuts a block further, it
+// has at most `past` besides.
 struct PackedPlan {
   int item_cap, few_cap;
   int64_t part_cap;

@@ -15,10 +15,11 @@
 namespace bcq {
 namespace {
 
-// Entries, tokens and stack places up to which one workgroup does everything, for up to 64
-// and up to 256 sequences; a second launch costs 3 us or so, and one workgroup comes to
-// little.  64 sequences with 64, 4096, 8192 tokens: 3.9, 6.8, 10.1 us, two launches 6.9,
-// 9.2, 9.0; 200 with 200, 4096: 5.8, 22, two launches 7.4, 7.4.
+// Tokens up to which one workgroup does everything, for up to 64 and up to 256 sequences;
+// entries of tables and places of the stack, which are copied and seldom all in use, count
+// a quarter.  A second launch costs 3 us or so, and one workgroup comes to little.  64
+// sequences with 64, 4096, 8192 tokens: 3.9, 6.8, 10.1 us, two launches 6.9, 9.2, 9.0; 200
+// with 200, 4096: 5.8, 22, two launches 7.4, 7.4.
 constexpr int64_t kAloneSmall = 6144, kAlone = 512;
 // Sequences whose starts, or pages, a workgroup looks up in shared memory.
 constexpr int kStarts = 4096;
@@ -283,11 +284,12 @@ hipError_t launch_kv_reserve(const KvView &c, const ReserveCall &r, void *ws, hi
   a.staged = reinterpret_cast<int32_t *>(w);
   const int64_t copies = (a.table_out != c.table ? (int64_t)c.B * c.max_pages : c.B) + r.T +
                          (a.free_out != a.free_in ? c.num_pages : 0);
-  if (c.B <= 64 && copies <= kAloneSmall) {
+  const int64_t work = r.T + (copies - r.T) / 4;
+  if (c.B <= 64 && work <= kAloneSmall) {
     small_kernel<1024><<<1, 1024, 0, s>>>(a);
     return hipGetLastError();
   }
-  if (c.B <= 256 && copies <= kAlone) {
+  if (c.B <= 256 && work <= kAlone) {
     reserve_kernel<true, 256><<<1, 256, 0, s>>>(a);
     return hipGetLastError();
   }

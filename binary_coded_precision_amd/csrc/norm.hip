@@ -87,8 +87,8 @@ __device__ __forceinline__ void scale_row8(float (&y)[8], const float (&h)[8], f
 // longer ones (N = 0) are read again from the caches for each of three passes.
 //
 // Bound by the bytes of x, the residual, h, y and codes, each passed once: 4096 x 4096 in
-// fp16 with h and codes (117 MB) 24.7 us, 4.7 TB/s; 30000 x 512 25 us, 4.3 TB/s.  Few
-// rows are bound by one pass's latency, 3 us for one of 4096.
+// fp16 with h and codes (118 MB) 28.8 us, 4.1 TB/s; 30000 x 512 25 us, 4.3 TB/s.  Few
+// rows are bound by one pass's latency, 2.6 us for one of 4096.
 //
 // Rows of up to 512 elements are a wave's, four to a workgroup: as fast as a workgroup a
 // row for one row (4.0 us), 25 us rather than 59 for 30000 rows of 512, which are bound
