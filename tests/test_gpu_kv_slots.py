@@ -291,3 +291,23 @@ def test_the_sign_of_a_zero(D):
                                                    (256, 256, 1, 2), (257, 32, 0, 20)])
 def test_a_server_of_any_size(B, page, shared, longest, in_place):
     test_a_server_at_work(B, page, shared, longest, in_place)
+
+
+def test_more_tokens_than_a_grid_is_wide():
+    """A grid's second dimension has 65535 workgroups at most, of four tokens of 256 channels."""
+    T, D, page = 262150, 256, 256
+    say("kv_append_slots", T, D)
+    a, b = (bcq.KVCache.pool(1, T + page, T // page + 2, 1, D, page)[0] for _ in range(2))
+    k, v = (torch.randn((T, 1, D), device="cuda").half() for _ in range(2))
+    slots = torch.arange(T, device="cuda") + 3
+    bcq.bcq_kv_append_slots(a, k, v, slots)
+    for part in torch.arange(T, device="cuda").split(100000):
+        bcq.bcq_kv_append_slots(b, k[part], v[part], slots[part])
+    for x, y in ((a.k_codes, b.k_codes), (a.v_codes, b.v_codes), (a.scales, b.scales)):
+        assert x.any() and torch.equal(x, y)
+    got = torch.full((2, T, 1, D), 7.0, device="cuda", dtype=torch.float16)
+    bcq.bcq_kv_read_slots(a, got[0], got[1], slots)
+    for whole, x in zip(got, (k, v)):
+        # half a step of 15, and the roundings of scale, zero and value
+        step = (x.float().amax(2) - x.float().amin(2)) / 15
+        assert ((whole.float() - x.float()).abs().amax(2) <= 0.5 * step + 0.02).all()
