@@ -99,12 +99,12 @@ class Server:
         bcq.bcq_rms_norm(s.x, layer.norms[0], EPS, residual=added, H=s.x, codes=s.codes,
                          scales=s.scales)
         bcq.bcq_int_gemm(s.codes, s.scales, *layer.qkv, s.qkv, workspace=s.products)
-        q, k, v = s.qkv.view(s.T, -1, self.dim).split((self.heads, self.kv_heads, self.kv_heads),
-                                                      dim=1)
+        heads = (self.heads, self.kv_heads, self.kv_heads)
+        q, k, v = s.qkv.view(s.T, sum(heads), self.dim).split(heads, dim=1)
         bcq.bcq_kv_append_slots(layer.cache, k, v, s.slots)
         bcq.bcq_kv_attend_packed(layer.cache, q, s.context, s.starts, s.max_n,
                                  shared_pages=self.shared_pages, workspace=s.attend)
-        bcq.bcq_int_linear(s.context.view(s.T, -1), *layer.out, s.sub, workspace=s.products)
+        bcq.bcq_int_linear(s.context.flatten(1), *layer.out, s.sub, workspace=s.products)
 
     def feed_forward(self, layer, s):
         bcq.bcq_rms_norm(s.x, layer.norms[1], EPS, residual=s.sub, H=s.x, codes=s.codes,
