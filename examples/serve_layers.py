@@ -116,10 +116,16 @@ class Server:
 
     def common(self, x):
         """Reads a prompt common to all requests, x [n][hidden] of whole pages, into pages that
-        every table then begins with."""
+        every table then begins with; before any request is served."""
         n = len(x)
         if n % self.page:
             raise ValueError("a common prompt of %d tokens, pages of %d" % (n, self.page))
+        if self.lens.any():
+            raise ValueError("a common prompt where tokens are cached")
+        # a step leaves a request out that there is no room for
+        if n > self.page * min(self.table.shape[1], int(self.count)):
+            raise ValueError("a common prompt of %d tokens, %d free pages of %d and room for %d in a "
+                             "table" % (n, int(self.count), self.page, self.table.shape[1]))
         s = Step(self, n, n)
         s.x.copy_(x)
         s.new[0] = n
