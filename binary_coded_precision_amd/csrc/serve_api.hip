@@ -116,8 +116,10 @@ bcq_status check_packed(const bcq_kv_cache *c, int32_t T, const int64_t *slots, 
                         const void *v, bcq_dtype dtype) {
   BCQ_TRY(check_cache(c));
   if (!dtype_valid(dtype) || T < 0 || T > BCQ_KV_MAX_TOKENS) return BCQ_ERR_INVALID_ARG;
-  // a work item takes four channels of K or V, of up to three tokens more than T
-  if ((int64_t)c->heads * ((int64_t)T + 3) * c->head_dim >= ((int64_t)1 << 33) - 512)
+  // A work item takes four channels of K and of V, a workgroup 1024 / head_dim tokens of a
+  // head; the last one's spare tokens and the spare groups of the grid's rows come to less
+  // than 2^17 channels of a head.  Work items of a launch stay below 2^32.
+  if ((int64_t)c->heads * ((int64_t)T * c->head_dim + (1 << 17)) >= (int64_t)1 << 34)
     return BCQ_ERR_INVALID_ARG;
   if (T > 0 && (slots == nullptr || k == nullptr || v == nullptr)) return BCQ_ERR_INVALID_ARG;
   if (!aligned(slots, 8) || !aligned(k, dtype_size(dtype)) || !aligned(v, dtype_size(dtype)))

@@ -618,7 +618,7 @@ size_t bcq_kv_reserve_workspace_bytes(const bcq_kv_cache *cache);
  * bcq_kv_reserve writes them; of a call's tokens no two in one).  A slot that lies in
  * no page is never followed: nothing is written there, and zeros are read.
  * K, V: element (t, h, d) at t*_token + h*_head + d.  The table and lengths of the
- * cache are not read.  heads * (T + 3) * head_dim below 2^33 - 512; T = 0 does nothing.
+ * cache are not read.  heads * (T * head_dim + 2^17) below 2^34; T = 0 does nothing.
  */
 bcq_status bcq_kv_append_slots(const bcq_kv_cache *cache, int32_t T, const int64_t *slots,
                                const void *K, int64_t k_token, int64_t k_head, const void *V,
