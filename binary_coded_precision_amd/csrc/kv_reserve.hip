@@ -15,11 +15,18 @@
 namespace bcq {
 namespace {
 
-// Tokens up to which one workgroup does everything, for up to 64 and up to 256 sequences;
-// entries of tables and places of the stack, which are copied and seldom all in use, count
-// a quarter.  A second launch costs 3 us or so, and one workgroup comes to little.  64
-// sequences with 64, 4096, 8192 tokens: 3.9, 6.8, 10.1 us, two launches 6.9, 9.2, 9.0; 200
-// with 200, 4096: 5.8, 22, two launches 7.4, 7.4.
+// Tokens up to which one workgroup does everything, for up to 64 and up to 256 sequences.  A
+// second launch costs 3 us or so, and one workgroup comes to little.  64 sequences with 64,
+// 4096, 8192 tokens: 3.9, 6.8, 10.1 us, two launches 6.9, 9.2, 9.0; 200 with 200, 4096: 5.8,
+// 22, two launches 7.4, 7.4.
+// A place of a stack that is copied counts a quarter: 64 sequences with 64 tokens and 8000,
+// 16000, 24000, 32000 places 5.1, 6.1, 7.1, 8.1 us, two launches 7.1.  Entries of tables that
+// are copied have 16 lanes a sequence in either form: up to 64 sequences they count nothing (64
+// full tables of 128, 256, 512 pages 5.3, 6.7, 9.5 us, two launches 8.3, 9.6, 12.1; one of 8192
+// pages 70 and 74).  Past that the one workgroup, of 256 threads, has a few sequences' copies
+// one behind the other; there an entry counts a quarter (100 sequences with 17 entries 6.9 us,
+// two launches 7.2; 200 with 5 entries 9.2 and 7.6; 70 with 21 entries, the worst, are given two
+// launches, 7.2, where one workgroup takes 6.2).
 constexpr int64_t kAloneSmall = 6144, kAlone = 512;
 // Sequences whose starts, or pages, a workgroup looks up in shared memory.
 constexpr int kStarts = 4096;
@@ -282,14 +289,14 @@ hipError_t launch_kv_reserve(const KvView &c, const ReserveCall &r, void *ws, hi
   a.back = reinterpret_cast<int *>(w);
   w += pad256((size_t)c.B * sizeof(int));
   a.staged = reinterpret_cast<int32_t *>(w);
-  const int64_t copies = (a.table_out != c.table ? (int64_t)c.B * c.max_pages : c.B) + r.T +
-                         (a.free_out != a.free_in ? c.num_pages : 0);
-  const int64_t work = r.T + (copies - r.T) / 4;
-  if (c.B <= 64 && work <= kAloneSmall) {
+  const int64_t places = a.free_out != a.free_in ? c.num_pages : 0;
+  const int64_t copies =
+      (a.table_out != c.table ? (int64_t)c.B * c.max_pages : c.B) + r.T + places;
+  if (c.B <= 64 && r.T + places / 4 <= kAloneSmall) {
     small_kernel<1024><<<1, 1024, 0, s>>>(a);
     return hipGetLastError();
   }
-  if (c.B <= 256 && work <= kAlone) {
+  if (c.B <= 256 && r.T + (copies - r.T) / 4 <= kAlone) {
     reserve_kernel<true, 256><<<1, 256, 0, s>>>(a);
     return hipGetLastError();
   }
