@@ -12,7 +12,9 @@
 //    the card holds and none is much longer than the others.
 //  - Rows of sequences with few of them (decode steps, drafted tokens) all meet the
 //    shared pages together, as the rows of one sequence: those pages are read
-//    once, and up to 128 rows share the unpacking of their codes.  The sequences'
+//    from memory once, and 32 rows (a wave's; 16 of 256 channels, or where there are
+//    few) share the unpacking of their codes.  A block's other waves, and other
+//    blocks, unpack them again, from the caches.  The sequences'
 //    own items then start behind the shared pages.  Sequences with many rows gain
 //    nothing from that and read the shared pages as their own.
 //
@@ -203,10 +205,13 @@ struct Whole {
     h.few_shares = shares_of(few_steps, few_weight, wide_few ? wide_chunk : chunk, most);
     // The shared items are much alike and start first, one on each compute unit, then a
     // second: with a second on half of the units the others would wait for those.  So
-    // whole turns of them, the sequences' own items beside the last.  64 decode steps
-    // behind 16384 tokens: 256 items in 54 us, 288 in 54, 384 (what the weights say) in 61,
-    // 464 in 67; four fifths of a turn are made a whole one (480 items 89 us; 256 93, 512
-    // 87).
+    // whole turns of them, the sequences' own items beside the last.  At 25 sizes (20 to 128
+    // decode steps behind 4096 to 32768 tokens, 2 to 32 cached heads of 64 to 256 channels)
+    // that is as fast as what the weights say or faster (11% less time at the median of the 20
+    // sizes where the two differ): 64 behind 16384 tokens 56 us with 256 items rather than 384 in 63, 32 of 64
+    // heads behind 8192 tokens 40 us with 256 rather than 272 in 50.  What lacks a fifth of a
+    // turn is made a whole one (480 items: 80 us, with one turn 80); two fifths are too much
+    // (128 decode steps, 416 items: 87 us, with two turns 94).
     const int wide = few_blocks * a.c.H, turns = (h.few_shares * wide + kNearTurn) / kUnits;
     if (h.few_shares * wide >= kUnits)
       h.few_shares = min(max(max(turns * kUnits / wide, 1),
@@ -561,7 +566,8 @@ __device__ __forceinline__ void clear(Sums<D, CT> &A) {
 }
 
 // An item of few rows: 16 of them, four waves share the tokens.  A step is bound by its
-// loads: 32 decode steps over 8192 tokens (215 MB) take 48 us, 4.5 TB/s.
+// loads: 32 decode steps over 8192 to 4224 tokens of 8 heads of 128 channels (216 MB) take
+// 65 us, 3.3 TB/s; 50 us where a call finds them in the last cache.
 template <int D, bool F32>
 __device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, const Listed *list,
                                         int base, int h, Meet<D> &meet) {
@@ -666,11 +672,12 @@ __device__ __forceinline__ void run_few(const PackedArgs &a, const Item &x, cons
 }
 
 // An item of many rows: every wave has rows of its own, 32 (16 of 256 channels, as many as
-// its registers hold).  Bound by instructions: a step of 32 rows over 32 tokens of 128
-// channels has 48 matrix instructions and about 300 others, of which unpacking is a
-// third, and the two kinds hardly overlap on a SIMD (48 beside 240: 1033 ns for two
-// waves, alone 665 and 543).  Six prompts of 2334 to 4001 tokens, 443 us at the rate of a
-// large matrix product, take 805 us; the probabilities' second fp16 is 16 of the 48.
+// its registers hold); waves past the last row have nothing to do.  Bound by instructions:
+// a step of 32 rows over 32 tokens of 128 channels has 48 matrix instructions and 340
+// others, of which unpacking is a third (fp32 calls 64 and 530: queries in two parts, and
+// every product summed outside the matrix cores).  Six prompts of 2334 to 4001 tokens, 443
+// us at the rate of a large matrix product, take 806 us; the vector ALUs are at work for 86%
+// of that, the matrix cores for 40%, and the probabilities' second fp16 is 16 of the 48.
 template <int D, bool F32>
 __device__ __forceinline__ void run_many(const PackedArgs &a, const Item &x, const Listed *list,
                                          int base, int h) {
