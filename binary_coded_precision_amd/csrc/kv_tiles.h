@@ -151,15 +151,17 @@ __device__ __forceinline__ half2v pair_of(uint32_t w) {
 // which fp16 does not hold of queries below 2^-10, and the matrix cores keep
 // fewer bits of a product with a smaller subnormal (measured: 1e-6 of a sum of 32
 // products with c * 2^-24, 2e-8 with c * 2^-20).
-template <int D>
-__device__ __forceinline__ half8 k_frag(const Tiles<D> &t, int s, int w) {
-  const uint32_t x = t.k[s][w];
+__device__ __forceinline__ half8 code_frag(uint32_t x) {
   Frag f;
   f.w[0] = (x << 4) & 0x00f000f0u;
   f.w[1] = x & 0x00f000f0u;
   f.w[2] = (x >> 4) & 0x00f000f0u;
   f.w[3] = (x >> 8) & 0x00f000f0u;
   return f.h;
+}
+template <int D>
+__device__ __forceinline__ half8 k_frag(const Tiles<D> &t, int s, int w) {
+  return code_frag(t.k[s][w]);
 }
 
 // (code - 7.5) / 512 of two tokens, the low (N = 0) or high nibbles of the bytes
@@ -494,11 +496,40 @@ __device__ __forceinline__ void softmax_tiles(Sums<D, CT> &A, Frag (&P)[CT], Fra
     }
 }
 
+// Channels 64hh .. 64hh + 63 of the outputs, from 32 tokens' V by the channel's place in
+// its four.
+template <int D, int CT, bool F32>
+__device__ __forceinline__ void add_block(Sums<D, CT> &A, const Frag (&P)[CT],
+                                          const Frag (&Plo)[CT], const half8 (&vf)[4], int hh) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float4v x = {0.f, 0.f, 0.f, 0.f};
+        x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct].h, x, 0, 0, 0);
+        A.o[ct][4 * hh + j] += __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct].h, x, 0, 0, 0);
+      }
+  } else {
+    // no product waits for the one before it
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float4v &o = A.o[ct][4 * hh + j];
+          const half8 p = part ? P[ct].h : Plo[ct].h;
+          o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], p, o, 0, 0, 0);
+        }
+  }
+}
+
 template <int D, int CT, bool F32>
 __device__ __forceinline__ void add_values(Sums<D, CT> &A, const Frag (&P)[CT],
                                            const Frag (&Plo)[CT], const Tiles<D> &T) {
 #pragma unroll
-  for (int hh = 0; hh < D / 64; ++hh) {  // channels 64hh .. 64hh + 63
+  for (int hh = 0; hh < D / 64; ++hh) {
     half8 vf[4];  // by the channel's place in its four
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -507,28 +538,7 @@ __device__ __forceinline__ void add_values(Sums<D, CT> &A, const Frag (&P)[CT],
 #pragma unroll
       for (int j = 0; j < 4; ++j) vf[j][2 * e] = x[j][0], vf[j][2 * e + 1] = x[j][1];
     }
-    if constexpr (F32) {
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float4v x = {0.f, 0.f, 0.f, 0.f};
-          x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], Plo[ct].h, x, 0, 0, 0);
-          A.o[ct][4 * hh + j] += __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], P[ct].h, x, 0, 0, 0);
-        }
-    } else {
-      // no product waits for the one before it
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float4v &o = A.o[ct][4 * hh + j];
-            const half8 p = part ? P[ct].h : Plo[ct].h;
-            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[j], p, o, 0, 0, 0);
-          }
-    }
+    add_block<D, CT, F32>(A, P, Plo, vf, hh);
   }
 }
 
